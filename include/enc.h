@@ -68,13 +68,15 @@
  *    "0"), the asynchronous entry points synchronise their stream after
  *    launching (except while it is being captured into a graph), so a kernel
  *    fault is returned as ENC_ERR_HIP by the call that caused it.
- *  - Two more variables exist for tests: ENC_LOOKBACK_SPINS (polls of an
+ *  - Three more variables exist for tests: ENC_VERIFY_SPINS (polls after
+ *    which a workgroup of enc_verify_tree computes the others' sums itself;
+ *    0: at once, unless they are there), ENC_LOOKBACK_SPINS (polls of an
  *    unpublished tile before the single-pass encoder gives up and the
  *    two-pass encoder takes over; 0 makes every tile after the first give
  *    up at once, so that path always runs) and
  *    ENC_DECODE_MAX_GRID (workgroups per decode launch, below the default
  *    2^23, to run the several-launch path on small inputs). Results do not
- *    depend on either.
+ *    depend on any of them.
  */
 #ifndef ENC_H
 #define ENC_H
@@ -380,6 +382,190 @@ enc_status enc_validate(const void *d_comp, const enc_info *h_info, void *d_ws, 
  * ENC_ERR_UNSUPPORTED (sizes past the index arithmetic), ENC_ERR_HIP. */
 enc_status enc_stream_probe(const void *d_src, uint64_t src_bytes, void *d_dst, uint64_t dst_bytes,
                             uint32_t items_per_thread, uint32_t threads_per_workgroup, void *stream);
+
+/* ------------------------------------------------------------------------
+ * One decoding step around the fused GEMMs.
+ *
+ * A pass over the coded weights costs nearly the same for 1 token and for 16
+ * (single-token decoding is bound by the weights read, MINE Abstract), so a
+ * step can check a tree of drafted tokens for the price of one token. The
+ * entry points below are the parts of such a step that are not products with
+ * a weight: head norms and rotation between the projections and attention,
+ * attention of the tree's nodes over a paged cache, verification of the
+ * drafts, and the cache's pages. A tree has `nodes` nodes per sequence; node
+ * 0 is the pending token (known, but not yet in the cache), every other node
+ * is a drafted token whose parent has a lower index. nodes = 1 is ordinary
+ * single-token decoding.
+ *
+ * The conventions at the top of this file hold. In addition: strides count
+ * elements; the last (head_dim) axis of every array is contiguous; base
+ * pointers are 16-byte aligned and every other stride is a multiple of 16
+ * bytes. Whole numbers on the device (lengths, tables, parents, tokens,
+ * paths) cannot be checked on the host: out of range, they give the results
+ * stated with each entry point, and never an access outside the arrays.
+ * ---------------------------------------------------------------------- */
+
+enum { ENC_TREE_MAX_NODES = 256 };
+
+/* Norms of query and key heads, rotary embedding and conversion, one launch:
+ *   y = x * rsqrt(mean(x^2) + eps) * w              (per head, over head_dim)
+ *   (y_a, y_b) <- (y_a c - y_b s, y_b c + y_a s)    (first rot_dim values)
+ * with pairs (a, b) = (i, i + rot_dim/2), or (2i, 2i+1) with
+ * ENC_ROPE_ADJACENT, and c, s = d_table[position][i],
+ * d_table[position][rot_dim/2 + i] (fp32, [max_pos, rot_dim]). Values are
+ * converted from in_dtype (usually the fp32 rows of a GEMM) to fp32, and
+ * rounded once, to out_dtype. Values of d_v are only converted.
+ * ENC_QK_NO_NORM leaves the norm out; NULL weights count as ones. */
+enum { ENC_ROPE_ADJACENT = 1, ENC_QK_NO_NORM = 2 };
+typedef struct enc_qk_args {
+  const void *d_q, *d_k, *d_v;     /* [tokens, heads, head_dim]; d_v may be NULL */
+  void *d_q_out, *d_k_out, *d_v_out;
+  const void *d_q_weight, *d_k_weight; /* [head_dim] of w_dtype, or NULL */
+  const int32_t *d_positions;      /* [tokens]; outside [0, max_pos): that token's q and k are NaN */
+  const float *d_table;            /* [max_pos, rot_dim]; may be NULL if rot_dim is 0 */
+  uint64_t q_token, q_head, k_token, k_head, v_token, v_head;                   /* strides */
+  uint64_t q_out_token, q_out_head, k_out_token, k_out_head, v_out_token, v_out_head;
+  uint32_t tokens, q_heads, kv_heads, head_dim, rot_dim, max_pos;
+  uint32_t in_dtype, out_dtype, w_dtype; /* 1 BF16, 2 FP16, 3 FP32 */
+  uint32_t flags;
+  float eps;
+  uint32_t reserved;               /* 0 */
+} enc_qk_args;
+
+/* head_dim: a multiple of 8 up to 512; rot_dim: even, at most head_dim.
+ * An output may be its input itself (same pointer, type and strides);
+ * otherwise they must not overlap. tokens = 0 does nothing. Asynchronous. */
+enc_status enc_qk_norm_rope(const enc_qk_args *h_args, void *stream);
+
+/* Attention of a tree's nodes over a paged cache and the tree itself:
+ *   out[b,i,h] = sum_j softmax_j(scale * q[b,i,h] . k_j) v_j
+ * where j runs over the sequence's cached tokens and over the nodes that
+ * node i may see: bit j % 64 of d_mask[b][i][j / 64] (any pattern; for a
+ * tree: i and its ancestors), or, with d_mask NULL, nodes j <= i. Query head
+ * h reads KV head h / (q_heads / kv_heads). Cached token t of sequence s lies
+ * in page d_table[s][t / page_size], row t % page_size. Infinities and NaN
+ * in rows that a node does not see leave its output alone. A node that sees
+ * nothing has output 0 and lse -infinity. d_lse: log sum exp of the scaled
+ * scores (natural logarithm). */
+typedef struct enc_tree_attention_args {
+  const void *d_q;                 /* [batch, nodes, q_heads, head_dim] */
+  const void *d_k_new, *d_v_new;   /* the nodes' own rows, [batch, nodes, kv_heads, head_dim] */
+  const void *d_k_cache, *d_v_cache; /* [n_pages, page_size, kv_heads, head_dim], same strides for both */
+  void *d_out;                     /* [batch, nodes, q_heads, head_dim] */
+  float *d_lse;                    /* [batch, nodes, q_heads] contiguous, or NULL */
+  const int32_t *d_table;          /* [max_seqs, max_pages] contiguous */
+  const int32_t *d_lens;           /* [max_seqs] cached tokens; clamped to [0, max_pages * page_size] */
+  const int32_t *d_seqs;           /* [batch] row of the table for each b, or NULL: row b; out of range: no cached tokens */
+  const int32_t *d_nodes;          /* [batch] live nodes of each tree, or NULL: all; clamped to [0, nodes] */
+  const uint64_t *d_mask;          /* [batch, nodes, ceil(nodes / 64)] contiguous, or NULL */
+  uint64_t q_batch, q_node, q_head;
+  uint64_t k_new_batch, k_new_node, k_new_head, v_new_batch, v_new_node, v_new_head;
+  uint64_t cache_page, cache_token, cache_head;
+  uint64_t out_batch, out_node, out_head;
+  uint32_t batch, nodes, q_heads, kv_heads, head_dim, dtype; /* dtype: 1 BF16 or 2 FP16, of all value arrays */
+  uint32_t n_pages, page_size, max_pages, max_seqs;
+  float scale;
+  uint32_t reserved;               /* 0 */
+} enc_tree_attention_args;
+
+/* Rows of nodes past a tree's live ones are 0 (lse -infinity). head_dim: a
+ * multiple of 8 up to 256; nodes up to ENC_TREE_MAX_NODES; q_heads a multiple
+ * of kv_heads; page_size up to 65536. A table entry outside [0, n_pages)
+ * reads some page of the cache. The workspace (any contents) holds the parts
+ * of rows whose history is split over workgroups, joined in a fixed order by
+ * a second kernel: equal inputs give equal bits. Its size depends on batch,
+ * nodes, heads, head_dim and max_pages * page_size. Asynchronous. */
+uint64_t enc_tree_attention_workspace_bytes(const enc_tree_attention_args *h_args);
+enc_status enc_tree_attention(const enc_tree_attention_args *h_args, void *d_ws, uint64_t ws_bytes,
+                              void *stream);
+
+/* Verification of a tree of drafted tokens against the target's
+ * probabilities, from given random numbers. The walk starts at node 0 with
+ * r = target[0] and looks at the current node's children in index order:
+ * child c with token x is accepted, and becomes the current node, if
+ *   u[c] * q(x) < r(x),   q = draft[current node];
+ * otherwise r <- max(r - q, 0) / sum(max(r - q, 0)) (unless that sum is 0,
+ * which leaves r). When the current node has no child left, the next token is
+ * drawn from r. With children drawn from q (each one by itself, or one alone)
+ * the accepted tokens and the next one are distributed as the target's.
+ * draft NULL stands for children named without chance (q = 1 at the child's
+ * token, 0 elsewhere).
+ *   path[b]:  the nodes walked, node 0 first, then -1; count[b]: their number
+ *   token[b]: the smallest t with sum_{i <= t} r(i) > u[0] * sum_i r(i)
+ * Arithmetic, so that the answer does not depend on how the work is split:
+ * probabilities are read as fp32 and clamped to [0, 1] (NaN: 0); products,
+ * differences and quotients are rounded to fp32 one by one; sums are exact
+ * sums of whole multiples of 2^-40 (each term rounded to nearest, ties to
+ * even); u counts in units of 2^-24, rounded down, clamped to [0, 1).
+ * A child whose token lies outside [0, vocab) is rejected without changing
+ * r. If r is 0 everywhere token is -1. A sequence without live nodes has
+ * count 0 and token -1. */
+typedef struct enc_verify_args {
+  const int32_t *d_parents;        /* [batch, nodes] contiguous; entry 0 of each row is not read */
+  const int32_t *d_tokens;         /* [batch, nodes] contiguous; entry 0 of each row is not read */
+  const void *d_target;            /* [batch, nodes, vocab]: row i is the distribution after node i */
+  const void *d_draft;             /* the same of the draft, or NULL */
+  const float *d_u;                /* [batch, nodes] contiguous */
+  const int32_t *d_nodes;          /* [batch] live nodes of each tree, or NULL: all; clamped to [0, nodes] */
+  int32_t *d_path, *d_count, *d_token; /* [batch, nodes], [batch], [batch] */
+  uint64_t target_batch, target_node, draft_batch, draft_node; /* strides */
+  uint32_t batch, nodes, vocab, dtype; /* dtype of both distributions: 1 BF16, 2 FP16, 3 FP32 */
+} enc_verify_args;
+
+/* nodes up to ENC_TREE_MAX_NODES, vocab up to 2^22. Rows need no alignment
+ * beyond their type's. The workspace must be zero-filled before its first use
+ * with this entry point; every call leaves it ready for the next; calls
+ * sharing one must not overlap. Asynchronous. */
+uint64_t enc_verify_tree_workspace_bytes(uint32_t batch, uint32_t nodes, uint32_t vocab);
+enc_status enc_verify_tree(const enc_verify_args *h_args, void *d_ws, uint64_t ws_bytes, void *stream);
+
+/* Pages of a cache. n_planes arrays of pages (2 per layer, K and V; any
+ * element type) share one table: token t of sequence s is row t % page_size
+ * of page d_table[s][t / page_size] in every plane. d_refs counts the
+ * sequences that hold a page; a page is free when its count is 0. Entries
+ * past a sequence's last page are -1. The functions keep this true; a program
+ * starts with lengths 0, entries -1 and counts 0. */
+typedef struct enc_cache {
+  void *d_data;                    /* plane p, page g, row r at d_data + p * plane_stride + (g * page_size + r) * row_bytes */
+  int32_t *d_table;                /* [max_seqs, max_pages] contiguous */
+  int32_t *d_lens;                 /* [max_seqs] */
+  int32_t *d_refs;                 /* [n_pages] */
+  uint64_t plane_stride;           /* bytes, a multiple of 16 */
+  uint32_t n_planes, n_pages, page_size, row_bytes; /* row_bytes: a multiple of 16 */
+  uint32_t max_seqs, max_pages;
+} enc_cache;
+
+/* Append the accepted rows of a verified tree: for sequence b of the call,
+ * rows d_path[b][0 .. d_count[b]) of its draft rows (plane p, node i at
+ * d_draft + p * draft_plane + b * draft_seq + i * row_bytes) become the
+ * cache's rows d_lens[s] .. d_lens[s] + d_count[b] - 1, s = d_seqs[b], in
+ * every plane, and d_lens[s] grows. Pages are taken from the free ones,
+ * lowest number first, in the order of the call's sequences. A partly filled
+ * last page that another sequence holds too is left to it: its filled rows
+ * are copied to a new page first. Sequences of one call must be distinct.
+ * *d_status (device) becomes 0, or, with nothing changed: the number of pages
+ * missing, -1 (a sequence outside the table), -2 (a count or path entry
+ * outside the nodes), -3 (a length past max_pages * page_size), -4 (a table
+ * entry or length that no call of this group left). The workspace may hold
+ * anything. Asynchronous. */
+uint64_t enc_cache_workspace_bytes(const enc_cache *h_cache, uint32_t batch, uint32_t nodes);
+enc_status enc_cache_commit(const enc_cache *h_cache, const int32_t *d_seqs, uint32_t batch,
+                            const void *d_draft, uint64_t draft_plane, uint64_t draft_seq,
+                            const int32_t *d_path, const int32_t *d_count, uint32_t nodes,
+                            int32_t *d_status, void *d_ws, uint64_t ws_bytes, void *stream);
+
+/* Sequence d_dst[i] lets go of what it held and shares all pages and the
+ * length of d_src[i] (no row is copied until one of them appends). d_dst must
+ * be distinct and none of them a d_src of the call; a pair outside the table,
+ * or of one sequence with itself, does nothing. Asynchronous. */
+enc_status enc_cache_fork(const enc_cache *h_cache, const int32_t *d_src, const int32_t *d_dst,
+                          uint32_t pairs, void *stream);
+
+/* Cut sequence d_seqs[i] to d_new_lens[i] tokens (no longer than it is; 0
+ * frees it) and free the pages past its end that nobody else holds. d_seqs
+ * must be distinct; one outside the table does nothing. Asynchronous. */
+enc_status enc_cache_truncate(const enc_cache *h_cache, const int32_t *d_seqs,
+                              const int32_t *d_new_lens, uint32_t count, void *stream);
 
 /* Static text for a status code. */
 const char *enc_status_string(enc_status s);

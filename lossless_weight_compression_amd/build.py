@@ -16,7 +16,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libenc.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["decode.hip", "encode.hip", "encode_onepass.hip", "encode_wide.hip", "gemm.hip", "validate.hip", "probe.hip", "noalloc.hip",
-           "enc_api.cpp"]
+           "qk_rope.hip", "tree_attention.hip", "verify_tree.hip", "cache_pages.hip",
+           "enc_api.cpp", "step_api.cpp"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,0 +1,287 @@
+// cache_pages.hip -- pages of a key/value cache: append accepted rows (with
+// copy on write of a shared last page), share all pages with a fork, free the
+// pages past a new end.
+//
+// The bookkeeping is integers only, so its results do not depend on order:
+// free pages are those whose count is 0 when the call begins, and the r-th
+// page that the call's sequences need (in the order of the call) is the r-th
+// free one. A commit is two kernels. The first, one workgroup, checks every
+// number it was given, counts needs and free pages and either updates the
+// table, the counts and the lengths or leaves everything as it was. The
+// second moves the rows, and is bound by HBM traffic: a workgroup per
+// (sequence, plane, slice), 16 bytes a lane, several loads in flight.
+#include "step_common.h"
+
+namespace enc {
+namespace {
+
+constexpr uint32_t kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
+constexpr uint32_t kCopyThreads = 256;
+
+enum { kBadSeq = -1, kBadPath = -2, kPastEnd = -3, kBadTable = -4 };
+
+__device__ __forceinline__ uint32_t wave_scan_incl(uint32_t v, uint32_t lane) {
+  for (uint32_t o = 1; o < 64; o <<= 1) {
+    const uint32_t u = __shfl_up(v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// Exclusive sum over the workgroup; total to every thread.
+__device__ __forceinline__ uint32_t block_scan_excl(uint32_t v, uint32_t *sums, uint32_t &total) {
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t incl = wave_scan_incl(v, lane);
+  __syncthreads();
+  if (lane == 63) sums[wave] = incl;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+  for (uint32_t w = 0; w < kPlanWaves; ++w) {
+    const uint32_t t = sums[w];
+    if (w < wave) before += t;
+    all += t;
+  }
+  total = all;
+  return before + incl - v;
+}
+
+// The new pages sequence b needs: its partly filled last page if somebody
+// else holds that too, and every page that its new rows reach and it lacks.
+struct Need {
+  int32_t seq, len, rows, last;   // last: the shared page to copy, or -1
+  uint32_t pages;
+  int32_t error;
+};
+
+__device__ __forceinline__ Need need_of(const CommitArgs &k, uint32_t b) {
+  Need n;
+  n.seq = k.seqs[b];
+  n.rows = k.count[b];
+  n.len = 0;
+  n.last = -1;
+  n.pages = 0;
+  n.error = 0;
+  if ((uint32_t)n.seq >= k.c.max_seqs) { n.error = kBadSeq; return n; }
+  if (n.rows < 0 || (uint32_t)n.rows > k.nodes) { n.error = kBadPath; return n; }
+  n.len = k.c.d_lens[n.seq];
+  const uint64_t room = (uint64_t)k.c.max_pages * k.c.page_size;
+  if (n.len < 0 || (uint64_t)n.len > room) { n.error = kBadTable; return n; }
+  if ((uint64_t)n.len + n.rows > room) { n.error = kPastEnd; return n; }
+  if (n.rows == 0) return n;
+  const int32_t *row = k.c.d_table + (uint64_t)n.seq * k.c.max_pages;
+  const uint32_t p0 = k.page.quot(n.len), p1 = k.page.quot(n.len + n.rows - 1);
+  const bool partly = p0 * k.c.page_size != (uint32_t)n.len;
+  for (uint32_t p = p0; p <= p1; ++p) {
+    const int32_t e = row[p];
+    if (partly && p == p0) {
+      if ((uint32_t)e >= k.c.n_pages) { n.error = kBadTable; return n; }
+      if (k.c.d_refs[e] > 1) {
+        n.last = e;
+        ++n.pages;
+      }
+    } else {
+      if (e != -1) { n.error = kBadTable; return n; }
+      ++n.pages;
+    }
+  }
+  return n;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void k_commit_plan(CommitArgs k) {
+  __shared__ uint32_t sums[kPlanWaves];
+  __shared__ int32_t error;
+  __shared__ uint32_t wave_free[kPlanWaves];
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (tid == 0) error = 0;
+  __syncthreads();
+
+  for (uint64_t i = tid; i < (uint64_t)k.batch * k.nodes; i += kPlanThreads) {
+    const uint32_t b = (uint32_t)(i / k.nodes), j = (uint32_t)(i - (uint64_t)b * k.nodes);
+    if ((int32_t)j < k.count[b] && (uint32_t)k.path[i] >= k.nodes) atomicMin(&error, (int32_t)kBadPath);
+  }
+  uint32_t need = 0;
+  for (uint32_t b0 = 0; b0 < k.batch; b0 += kPlanThreads) {
+    const uint32_t b = b0 + tid;
+    Need n;
+    n.pages = 0;
+    if (b < k.batch) {
+      n = need_of(k, b);
+      if (n.error) atomicMin(&error, n.error);
+    }
+    uint32_t all;
+    const uint32_t before = block_scan_excl(n.pages, sums, all);
+    if (b < k.batch) {
+      k.first[b] = (int32_t)(need + before);
+      k.info[4 * b + 0] = n.len;
+      k.info[4 * b + 1] = n.rows;
+      k.info[4 * b + 2] = n.last;
+      k.info[4 * b + 3] = -1;
+    }
+    need += all;
+  }
+  __syncthreads();
+
+  // Free pages: each wave counts those of its range, then, knowing how many
+  // lie before it, ranks the ones the call needs.
+  const uint32_t range = ((k.c.n_pages + kPlanWaves - 1) / kPlanWaves + 63) & ~63u;
+  const uint32_t g0 = min(wave * range, k.c.n_pages), g1 = min(g0 + range, k.c.n_pages);
+  uint32_t found = 0;
+  if (need && !error) {
+    uint32_t mine = 0;
+    for (uint32_t g = g0 + lane; g < g1; g += 64) mine += k.c.d_refs[g] == 0;
+    for (uint32_t o = 32; o; o >>= 1) mine += __shfl_xor(mine, o);
+    if (lane == 0) wave_free[wave] = mine;
+    __syncthreads();
+    uint32_t before = 0;
+    for (uint32_t w = 0; w < kPlanWaves; ++w) {
+      if (w < wave) before += wave_free[w];
+      found += wave_free[w];
+    }
+    if (found >= need) {
+      for (uint32_t g = g0; g < g1 && before < need; g += 64) {
+        const bool is_free = g + lane < g1 && k.c.d_refs[g + lane] == 0;
+        const uint64_t m = __ballot(is_free);
+        const uint32_t rank = before + __popcll(m & ((1ull << lane) - 1));
+        if (is_free && rank < need) k.pick[rank] = (int32_t)(g + lane);
+        before += __popcll(m);
+      }
+    }
+  }
+  __syncthreads();
+  const int32_t status = error ? error : found < need ? (int32_t)(need - found) : 0;
+  if (tid == 0) *k.status = status;
+  if (status) {
+    for (uint32_t b = tid; b < k.batch; b += kPlanThreads) k.info[4 * b + 1] = 0;   // nothing to move
+    return;
+  }
+
+  for (uint32_t b = tid; b < k.batch; b += kPlanThreads) {
+    const int32_t len = k.info[4 * b], rows = k.info[4 * b + 1];
+    if (rows == 0) continue;
+    const uint32_t seq = (uint32_t)k.seqs[b];
+    const int32_t last = k.info[4 * b + 2];
+    int32_t *row = k.c.d_table + (uint64_t)seq * k.c.max_pages;
+    const uint32_t p0 = k.page.quot(len), p1 = k.page.quot(len + rows - 1);
+    uint32_t next = (uint32_t)k.first[b];
+    for (uint32_t p = p0; p <= p1; ++p) {
+      // the page's count may have changed since: a page that several sequences
+      // of this call share is left by each of them
+      const bool leave = p == p0 && last >= 0;
+      if (row[p] >= 0 && !leave) continue;
+      const int32_t got = k.pick[next++];
+      row[p] = got;
+      k.c.d_refs[got] = 1;
+      if (leave) {
+        atomicSub(&k.c.d_refs[last], 1);
+        k.info[4 * b + 3] = got;
+      }
+    }
+    k.c.d_lens[seq] = len + rows;
+  }
+}
+
+// Rows of one (sequence, plane): first the filled rows of a page that is
+// left, then the accepted rows; in 16-byte items, four in flight a lane.
+__global__ __launch_bounds__(kCopyThreads) void k_commit_move(CommitArgs k) {
+  const uint32_t b = blockIdx.x;
+  const uint64_t plane = blockIdx.y;
+  const int32_t len = k.info[4 * b], rows = k.info[4 * b + 1];
+  if (rows <= 0) return;
+  const int32_t from = k.info[4 * b + 2], to = k.info[4 * b + 3];
+  const uint32_t per = k.c.row_bytes / 16, ps = k.c.page_size;
+  const uint32_t copied = to >= 0 ? (uint32_t)len - k.page.quot(len) * ps : 0;
+  uint8_t *base = static_cast<uint8_t *>(k.c.d_data) + plane * k.c.plane_stride;
+  const uint8_t *draft = k.draft + plane * k.draft_plane + (uint64_t)b * k.draft_seq;
+  const int32_t *row = k.c.d_table + (uint64_t)(uint32_t)k.seqs[b] * k.c.max_pages;
+  const int32_t *path = k.path + (uint64_t)b * k.nodes;
+  const uint64_t items = (uint64_t)(copied + (uint32_t)rows) * per;
+  const uint64_t step = (uint64_t)gridDim.z * kCopyThreads;
+  for (uint64_t i0 = blockIdx.z * kCopyThreads + threadIdx.x; i0 < items; i0 += 4 * step) {
+    uint4 v[4];
+    uint8_t *dst[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint64_t i = i0 + u * step;
+      dst[u] = nullptr;
+      if (i < items) {
+        const uint32_t r = (uint32_t)(i / per), o = (uint32_t)(i - (uint64_t)r * per) * 16;
+        const uint8_t *src;
+        if (r < copied) {
+          src = base + ((uint64_t)(uint32_t)from * ps + r) * k.c.row_bytes + o;
+          dst[u] = base + ((uint64_t)(uint32_t)to * ps + r) * k.c.row_bytes + o;
+        } else {
+          const uint32_t j = r - copied, t = (uint32_t)len + j, p = k.page.quot(t);
+          src = draft + (uint64_t)(uint32_t)path[j] * k.c.row_bytes + o;
+          dst[u] = base + ((uint64_t)(uint32_t)row[p] * ps + (t - p * ps)) * k.c.row_bytes + o;
+        }
+        v[u] = *reinterpret_cast<const uint4 *>(src);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (dst[u]) *reinterpret_cast<uint4 *>(dst[u]) = v[u];
+  }
+}
+
+__global__ __launch_bounds__(kCopyThreads) void k_fork(enc_cache c, const int32_t *src, const int32_t *dst) {
+  const uint32_t i = blockIdx.y, p = blockIdx.x * kCopyThreads + threadIdx.x;
+  const uint32_t s = (uint32_t)src[i], d = (uint32_t)dst[i];
+  if (s >= c.max_seqs || d >= c.max_seqs || s == d) return;
+  if (p < c.max_pages) {
+    const int32_t gain = c.d_table[(uint64_t)s * c.max_pages + p];
+    int32_t *at = c.d_table + (uint64_t)d * c.max_pages + p;
+    const int32_t loss = *at;
+    if (loss != gain) {
+      if ((uint32_t)loss < c.n_pages) atomicSub(&c.d_refs[loss], 1);
+      if ((uint32_t)gain < c.n_pages) atomicAdd(&c.d_refs[gain], 1);
+      *at = gain;
+    }
+  }
+  if (p == 0) c.d_lens[d] = c.d_lens[s];
+}
+
+// Lengths may be written before another workgroup of the same sequence reads
+// them: the smaller of old and new length is the same either way.
+__global__ __launch_bounds__(kCopyThreads) void k_truncate(enc_cache c, const int32_t *seqs, const int32_t *lens) {
+  const uint32_t i = blockIdx.y, p = blockIdx.x * kCopyThreads + threadIdx.x;
+  const uint32_t s = (uint32_t)seqs[i];
+  if (s >= c.max_seqs) return;
+  const int32_t keep = max(0, min(c.d_lens[s], lens[i]));
+  if (p < c.max_pages && (uint64_t)p * c.page_size >= (uint32_t)keep) {
+    int32_t *at = c.d_table + (uint64_t)s * c.max_pages + p;
+    const int32_t e = *at;
+    if (e >= 0) {
+      if ((uint32_t)e < c.n_pages) atomicSub(&c.d_refs[e], 1);
+      *at = -1;
+    }
+  }
+  if (p == 0) c.d_lens[s] = keep;
+}
+
+}  // namespace
+
+hipError_t launch_cache_commit(const CommitArgs &k, hipStream_t s) {
+  hipLaunchKernelGGL(k_commit_plan, dim3(1), dim3(kPlanThreads), 0, s, k);
+  // slices of about 64 KiB of the most a (sequence, plane) can have to move
+  const uint64_t most = (uint64_t)(k.nodes + k.c.page_size) * k.c.row_bytes;
+  const uint64_t slices = (most + 65535) / 65536;
+  hipLaunchKernelGGL(k_commit_move, dim3(k.batch, k.c.n_planes, (uint32_t)(slices < 64 ? slices : 64)),
+                     dim3(kCopyThreads), 0, s, k);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_fork(const enc_cache &c, const int32_t *src, const int32_t *dst, uint32_t pairs,
+                             hipStream_t s) {
+  hipLaunchKernelGGL(k_fork, dim3((c.max_pages + kCopyThreads - 1) / kCopyThreads, pairs), dim3(kCopyThreads), 0, s,
+                     c, src, dst);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_truncate(const enc_cache &c, const int32_t *seqs, const int32_t *lens, uint32_t count,
+                                 hipStream_t s) {
+  hipLaunchKernelGGL(k_truncate, dim3((c.max_pages + kCopyThreads - 1) / kCopyThreads, count), dim3(kCopyThreads), 0,
+                     s, c, seqs, lens);
+  return hipGetLastError();
+}
+
+}  // namespace enc

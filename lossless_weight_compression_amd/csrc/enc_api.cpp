@@ -16,6 +16,7 @@
 
 #include "enc_common.h"
 #include "encode_batch.h"
+#include "step_common.h"
 
 using namespace enc;
 
@@ -395,6 +396,8 @@ enc_status enc::set_error(enc_status st, const char *fmt, ...) {
   va_end(ap);
   return st;
 }
+
+enc_status enc::after_launch(hipError_t e, hipStream_t s, const char *what) { return launched(e, s, what); }
 
 extern "C" {
 

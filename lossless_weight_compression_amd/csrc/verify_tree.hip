@@ -1,0 +1,385 @@
+// verify_tree.hip -- verification of drafted tokens against the target's
+// probabilities, from given random numbers (enc_verify_tree).
+//
+// The walk itself needs a target and a draft probability per child, gathered
+// for all nodes at once. What it reads in bulk is one row of the target and
+// of the draft per rejection (the sum of max(r - q, 0)) and at its end (the
+// draw). r is never stored: with the sums S_1 .. S_k of the rejections before,
+// element i is recomputed from p_i and q_i in k steps, so a row is read
+// again, from cache, rather than written.
+//
+// Sums are whole numbers of 2^-40: exact, so neither the split over lanes,
+// waves and workgroups nor its order shows in the answer.
+//
+// Bound: HBM traffic of those rows, and the rounds' latency. A row is split
+// over up to 16 workgroups (one for small rows, fewer for large batches);
+// every workgroup makes the same walk, sums its part of a row, publishes the
+// sums of its waves' segments and takes those of the others. A workgroup that
+// waits too long for the others (which may not have been scheduled) computes
+// all segments by itself from then on, so no wait is unbounded. The
+// workgroup whose segment holds the drawn token finds it.
+#include "step_common.h"
+
+#include <cstdlib>
+
+namespace enc {
+namespace {
+
+constexpr uint32_t kThreadsV = 1024, kWaves = kThreadsV / 64;
+constexpr uint32_t kMaxGroups = 16, kMaxSegments = kMaxGroups * kWaves;
+constexpr uint32_t kMaxNodes = ENC_TREE_MAX_NODES;
+typedef unsigned long long u64;
+
+__device__ __forceinline__ float clamp01(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
+
+__device__ __forceinline__ u64 mass(float x) {
+  // x 2^40 = hi 2^20 + lo: exact, and above 2^24 there is nothing to round
+  const float y = x * 1099511627776.f;
+  const float hi = truncf(y * (1.f / 1048576.f));
+  const float lo = fmaf(-hi, 1048576.f, y);
+  return ((u64)(uint32_t)hi << 20) + (u64)(uint32_t)rintf(lo);
+}
+
+template <typename T> __device__ __forceinline__ float value_at(const void *row, uint32_t i);
+template <> __device__ __forceinline__ float value_at<float>(const void *row, uint32_t i) {
+  return clamp01(static_cast<const float *>(row)[i]);
+}
+template <> __device__ __forceinline__ float value_at<__bf16>(const void *row, uint32_t i) {
+  return clamp01(__uint_as_float((uint32_t)static_cast<const uint16_t *>(row)[i] << 16));
+}
+template <> __device__ __forceinline__ float value_at<_Float16>(const void *row, uint32_t i) {
+  return clamp01((float)static_cast<const _Float16 *>(row)[i]);
+}
+
+__device__ __forceinline__ u64 wave_sum(u64 v) {
+  for (uint32_t o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// The rejections at the current node.
+struct Rejections {
+  uint32_t n;                 // how many
+  float sum[kMaxNodes];       // fp32 sum of max(r - q, 0) after each; 0: r was left as it was
+  int32_t token[kMaxNodes];
+};
+
+// r_i after the first n rejections, and in `left` what it is a multiple of:
+// the last nonempty difference (p_i if there is none).
+template <bool POINT>
+__device__ __forceinline__ float residual(float p, float q, int32_t i, const Rejections &x, uint32_t n,
+                                          float &left) {
+  float r = p;
+  left = p;
+  for (uint32_t k = 0; k < n; ++k) {
+    const float s = x.sum[k];
+    if (s > 0.f) {
+      const float qk = POINT ? (x.token[k] == i ? 1.f : 0.f) : q;
+      left = fmaxf(r - qk, 0.f);
+      r = left / s;
+    }
+  }
+  return r;
+}
+
+template <typename T, bool POINT>
+__global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
+  const enc_verify_args &a = k.a;
+  __shared__ int32_t token[kMaxNodes];
+  __shared__ float u[kMaxNodes], pc[kMaxNodes], qc[kMaxNodes];
+  __shared__ int32_t path[kMaxNodes];
+  __shared__ Rejections rej;
+  __shared__ u64 totals[kMaxSegments], kept[kMaxSegments];
+  __shared__ u64 scan[kWaves];
+  __shared__ uint32_t alone;
+
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint32_t G = k.groups, b = blockIdx.x / G, g = blockIdx.x - b * G;
+  const uint32_t segments = G * kWaves;
+  const uint32_t T_ = a.nodes, V = a.vocab;
+  int32_t live = a.d_nodes ? a.d_nodes[b] : (int32_t)T_;
+  live = max(0, min(live, (int32_t)T_));
+  const char *target = static_cast<const char *>(a.d_target) + (uint64_t)b * a.target_batch * sizeof(T);
+  const char *draft = static_cast<const char *>(a.d_draft) + (POINT ? 0 : (uint64_t)b * a.draft_batch * sizeof(T));
+  const uint64_t trow = a.target_node * sizeof(T), drow = a.draft_node * sizeof(T);
+
+  // every node's parent, in registers of every wave: node 64 j + lane
+  int32_t parent[kMaxNodes / 64];
+#pragma unroll
+  for (uint32_t j = 0; j < kMaxNodes / 64; ++j) {
+    const int32_t i = (int32_t)(64 * j + lane);
+    parent[j] = i >= 1 && i < live ? a.d_parents[(uint64_t)b * T_ + i] : -1;
+    if (parent[j] >= i) parent[j] = -1;
+  }
+  if (tid < T_) {
+    const int32_t i = (int32_t)tid;
+    u[tid] = a.d_u[(uint64_t)b * T_ + tid];
+    path[tid] = -1;
+    float p = 0.f, q = 0.f;
+    int32_t x = -1;
+    if (i >= 1 && i < live) {
+      const int32_t up = a.d_parents[(uint64_t)b * T_ + i];
+      x = a.d_tokens[(uint64_t)b * T_ + i];
+      if ((uint32_t)x >= V) x = -1;
+      if (up >= 0 && up < i && x >= 0) {
+        p = value_at<T>(target + up * trow, (uint32_t)x);
+        q = POINT ? 1.f : value_at<T>(draft + up * drow, (uint32_t)x);
+      }
+    }
+    token[tid] = x;
+    pc[tid] = p;
+    qc[tid] = q;
+  }
+  if (tid == 0) {
+    rej.n = 0;
+    alone = 0;
+  }
+  __syncthreads();
+
+  u64 total = 0;             // of what `kept` holds the segments of
+  uint32_t round = 0;
+  bool solo = false;         // this workgroup no longer waits for the others
+
+  // Sums of `left` over every segment of the current node's row, after n
+  // rejections, into totals[]; returns their sum. With `pending`, the n-th
+  // rejection's own sum is what is being computed: r - q is taken of r.
+  auto sum_row = [&](uint32_t cur, uint32_t n, bool pending) -> u64 {
+    const char *prow = target + cur * trow, *qrow = draft + cur * drow;
+    const int32_t ptoken = pending ? rej.token[n] : -1;
+    auto segment_sum = [&](uint32_t seg) -> u64 {
+      const uint64_t lo = (uint64_t)seg * k.segment;
+      u64 acc = 0;
+      if (lo < V) {
+        const uint32_t hi = (uint32_t)(lo + k.segment < V ? lo + k.segment : V);
+        for (uint32_t i0 = (uint32_t)lo; i0 < hi; i0 += 256) {
+          float p[4], q[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t i = i0 + 64 * e + lane;
+            p[e] = i < hi ? value_at<T>(prow, i) : 0.f;
+            q[e] = !POINT && i < hi ? value_at<T>(qrow, i) : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int32_t i = (int32_t)(i0 + 64 * e + lane);
+            float left;
+            const float r = residual<POINT>(p[e], q[e], i, rej, n, left);
+            if (pending) left = fmaxf(r - (POINT ? (i == ptoken ? 1.f : 0.f) : q[e]), 0.f);
+            acc += mass(left);
+          }
+        }
+      }
+      return wave_sum(acc);
+    };
+    if (G > 1 && !solo) {
+      // a sum and the round it belongs to (modulo 3, plus 1) in one word, so a
+      // word is there or not; two slots in turn: nobody writes round r + 2
+      // before everybody has published r + 1, and so has read r
+      u64 *out = k.totals + ((uint64_t)b * 2 + (round & 1)) * segments;
+      const u64 tag = (u64)(round % 3 + 1) << 62;
+      const u64 t = segment_sum(g * kWaves + wave);
+      if (lane == 0)
+        __hip_atomic_store(&out[g * kWaves + wave], t | tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (wave * 64 < segments) {
+        u64 got = tag;
+        uint32_t polls = 0;
+        while (true) {
+          if (tid < segments) got = __hip_atomic_load(&out[tid], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          if (__all(got >> 62 == tag >> 62)) break;
+          if (polls++ >= k.spins) {
+            if (lane == 0) alone = 1;
+            break;
+          }
+          __builtin_amdgcn_s_sleep(1);
+        }
+        if (tid < segments) totals[tid] = got & ~(3ull << 62);
+      }
+      __syncthreads();
+      solo = alone;
+    }
+    if (G == 1 || solo) {
+      for (uint32_t s = wave; s < segments; s += kWaves) {
+        const u64 t = segment_sum(s);
+        if (lane == 0) totals[s] = t;
+      }
+    }
+    ++round;
+    __syncthreads();
+    const u64 mine = tid < segments ? totals[tid] : 0;
+    const u64 ws = wave_sum(mine);
+    if (lane == 0) scan[wave] = ws;
+    __syncthreads();
+    u64 all = 0;
+    for (uint32_t w = 0; w < kWaves; ++w) all += scan[w];
+    __syncthreads();
+    return all;
+  };
+
+  // ---- the walk: the same in every thread
+  uint32_t cur = 0, count = 0;
+  bool have = false;          // kept[] and total hold the current node's `left`
+  if (live > 0) {
+    if (tid == 0) path[0] = 0;
+    count = 1;
+    int32_t last = 0;         // children up to here are done with
+    while (true) {
+      uint32_t c = 0;
+#pragma unroll
+      for (uint32_t j = 0; j < kMaxNodes / 64; ++j) {
+        const int32_t i = (int32_t)(64 * j + lane);
+        const uint64_t m = __ballot(parent[j] == (int32_t)cur && i > last);
+        if (!c && m) c = 64 * j + (uint32_t)__builtin_ctzll(m);
+      }
+      if (!c) break;
+      last = (int32_t)c;
+      const int32_t x = token[c];
+      if (x < 0) continue;
+      float left;
+      const uint32_t n = rej.n;
+      const float r = residual<POINT>(pc[c], qc[c], x, rej, n, left);
+      if (u[c] * qc[c] < r) {
+        cur = c;
+        have = false;
+        __syncthreads();
+        if (tid == 0) {
+          path[count] = (int32_t)c;
+          rej.n = 0;
+        }
+        ++count;
+        __syncthreads();
+        continue;
+      }
+      __syncthreads();
+      if (tid == 0) rej.token[n] = x;
+      __syncthreads();
+      const u64 sum = sum_row(cur, n, true);
+      if (sum) {
+        if (tid < segments) kept[tid] = totals[tid];
+        total = sum;
+        have = true;
+      }
+      if (tid == 0) {
+        rej.sum[n] = (float)sum * (1.f / 1099511627776.f);
+        rej.n = n + 1;
+      }
+      __syncthreads();
+    }
+    if (!have) {
+      total = sum_row(cur, rej.n, false);
+      if (tid < segments) kept[tid] = totals[tid];
+      __syncthreads();
+    }
+  }
+
+  if (g == 0) {
+    for (uint32_t i = tid; i < T_; i += kThreadsV) a.d_path[(uint64_t)b * T_ + i] = path[i];
+    if (tid == 0) {
+      a.d_count[b] = (int32_t)count;
+      if (total == 0) a.d_token[b] = -1;
+    }
+  }
+  if (total) {
+    // the segment in which the running sum passes the goal, then the element
+    const float u0 = u[0];
+    const uint32_t point = u0 > 0.f ? (uint32_t)(fminf(u0, 1.f - 1.f / 16777216.f) * 16777216.f) : 0u;
+    const u64 goal = (total >> 24) * point + (((total & 0xFFFFFFull) * point) >> 24);
+    auto block_excl = [&](u64 v) -> u64 {
+      u64 incl = v;
+      for (uint32_t o = 1; o < 64; o <<= 1) {
+        const u64 t = __shfl_up(incl, o);
+        if (lane >= o) incl += t;
+      }
+      __syncthreads();
+      if (lane == 63) scan[wave] = incl;
+      __syncthreads();
+      u64 before = 0;
+      for (uint32_t w = 0; w < wave; ++w) before += scan[w];
+      return before + incl - v;
+    };
+    const u64 mine = tid < segments ? kept[tid] : 0;
+    const u64 before = block_excl(mine);
+    __shared__ uint32_t hit;
+    __shared__ u64 hit_before;
+    if (before <= goal && goal < before + mine) {
+      hit = tid;
+      hit_before = before;
+    }
+    __syncthreads();
+    const uint32_t seg = hit;
+    if (seg / kWaves == g) {
+      const char *prow = target + cur * trow, *qrow = draft + cur * drow;
+      const uint32_t lo = seg * k.segment, hi = min(lo + k.segment, V);
+      const uint32_t per = (k.segment + kThreadsV - 1) / kThreadsV;
+      auto left_at = [&](uint32_t i) -> u64 {
+        float left;
+        residual<POINT>(value_at<T>(prow, i), POINT ? 0.f : value_at<T>(qrow, i), (int32_t)i, rej, rej.n, left);
+        return mass(left);
+      };
+      const uint32_t i0 = lo + tid * per;
+      u64 sum = 0;
+      for (uint32_t i = i0; i < min(i0 + per, hi); ++i) sum += left_at(i);
+      u64 at = hit_before + block_excl(sum);
+      if (at <= goal && goal < at + sum) {
+        for (uint32_t i = i0; i < hi; ++i) {
+          at += left_at(i);
+          if (at > goal) {
+            a.d_token[b] = (int32_t)i;
+            break;
+          }
+        }
+      }
+    }
+  }
+
+  // the last workgroup of a sequence leaves its words at zero for the next call
+  if (G > 1) {
+    __shared__ uint32_t order;
+    __syncthreads();
+    if (tid == 0) order = __hip_atomic_fetch_add(&k.done[b], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (order == G - 1) {
+      for (uint32_t i = tid; i < 2 * segments; i += kThreadsV)
+        __hip_atomic_store(&k.totals[(uint64_t)b * 2 * segments + i], 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (tid == 0) __hip_atomic_store(&k.done[b], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+}
+
+template <typename T>
+void launch_t(const VerifyKernelArgs &k, hipStream_t s) {
+  const dim3 grid(k.a.batch * k.groups), block(kThreadsV);
+  if (k.a.d_draft)
+    hipLaunchKernelGGL((k_verify<T, false>), grid, block, 0, s, k);
+  else
+    hipLaunchKernelGGL((k_verify<T, true>), grid, block, 0, s, k);
+}
+
+}  // namespace
+
+// Workgroups per sequence: the device's 256 compute units shared among the
+// sequences, at most 16 (a wave's sums then fit one thread each), and no
+// more than leave a workgroup 4096 elements.
+VerifyPlan plan_verify_tree(uint32_t batch, uint32_t vocab) {
+  VerifyPlan p;
+  uint32_t g = batch ? 256 / batch : 1;
+  const uint32_t most = (vocab + 4095) / 4096;
+  if (g > most) g = most;
+  if (g > kMaxGroups) g = kMaxGroups;
+  if (g < 1) g = 1;
+  p.groups = g;
+  const uint32_t segments = g * kWaves;
+  p.segment = ((vocab + segments - 1) / segments + 255) & ~255u;
+  p.totals_bytes = align_up(8ull * batch * 2 * segments, 256);
+  p.done_bytes = align_up(4ull * batch, 256);
+  return p;
+}
+
+hipError_t launch_verify_tree(const VerifyKernelArgs &k, hipStream_t s) {
+  switch (k.a.dtype) {
+    case 1: launch_t<__bf16>(k, s); break;
+    case 2: launch_t<_Float16>(k, s); break;
+    default: launch_t<float>(k, s); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace enc

@@ -66,6 +66,47 @@ class EncCItem(ctypes.Structure):
                 ("d_out", ctypes.c_void_p), ("out_capacity", ctypes.c_uint64)]
 
 
+class EncQkArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in (
+        "d_q", "d_k", "d_v", "d_q_out", "d_k_out", "d_v_out", "d_q_weight", "d_k_weight", "d_positions",
+        "d_table")]
+        + [(n, ctypes.c_uint64) for n in (
+            "q_token", "q_head", "k_token", "k_head", "v_token", "v_head", "q_out_token", "q_out_head",
+            "k_out_token", "k_out_head", "v_out_token", "v_out_head")]
+        + [(n, ctypes.c_uint32) for n in (
+            "tokens", "q_heads", "kv_heads", "head_dim", "rot_dim", "max_pos", "in_dtype", "out_dtype",
+            "w_dtype", "flags")]
+        + [("eps", ctypes.c_float), ("reserved", ctypes.c_uint32)])
+
+
+class EncTreeAttentionArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in (
+        "d_q", "d_k_new", "d_v_new", "d_k_cache", "d_v_cache", "d_out", "d_lse", "d_table", "d_lens",
+        "d_seqs", "d_nodes", "d_mask")]
+        + [(n, ctypes.c_uint64) for n in (
+            "q_batch", "q_node", "q_head", "k_new_batch", "k_new_node", "k_new_head", "v_new_batch",
+            "v_new_node", "v_new_head", "cache_page", "cache_token", "cache_head", "out_batch", "out_node",
+            "out_head")]
+        + [(n, ctypes.c_uint32) for n in (
+            "batch", "nodes", "q_heads", "kv_heads", "head_dim", "dtype", "n_pages", "page_size",
+            "max_pages", "max_seqs")]
+        + [("scale", ctypes.c_float), ("reserved", ctypes.c_uint32)])
+
+
+class EncVerifyArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in (
+        "d_parents", "d_tokens", "d_target", "d_draft", "d_u", "d_nodes", "d_path", "d_count", "d_token")]
+        + [(n, ctypes.c_uint64) for n in ("target_batch", "target_node", "draft_batch", "draft_node")]
+        + [(n, ctypes.c_uint32) for n in ("batch", "nodes", "vocab", "dtype")])
+
+
+class EncCache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("d_data", "d_table", "d_lens", "d_refs")]
+                + [("plane_stride", ctypes.c_uint64)]
+                + [(n, ctypes.c_uint32) for n in ("n_planes", "n_pages", "page_size", "row_bytes", "max_seqs",
+                                                  "max_pages")])
+
+
 _VP = ctypes.c_void_p
 _U32 = ctypes.c_uint32
 _U64 = ctypes.c_uint64
@@ -103,6 +144,16 @@ SIGNATURES = {
     "enc_decompress_gemm_nt": (_ST, [_VP, _U32, _U32, _VP, _INFO_P, _U32, _VP, _VP, _U64, _VP]),
     "enc_gemm_dense_nt": (_ST, [_VP, _U32, _U32, _VP, _U32, _VP, _VP, _U64, _VP]),
     "enc_stream_probe": (_ST, [_VP, _U64, _VP, _U64, _U32, _U32, _VP]),
+    "enc_qk_norm_rope": (_ST, [ctypes.POINTER(EncQkArgs), _VP]),
+    "enc_tree_attention_workspace_bytes": (_U64, [ctypes.POINTER(EncTreeAttentionArgs)]),
+    "enc_tree_attention": (_ST, [ctypes.POINTER(EncTreeAttentionArgs), _VP, _U64, _VP]),
+    "enc_verify_tree_workspace_bytes": (_U64, [_U32, _U32, _U32]),
+    "enc_verify_tree": (_ST, [ctypes.POINTER(EncVerifyArgs), _VP, _U64, _VP]),
+    "enc_cache_workspace_bytes": (_U64, [ctypes.POINTER(EncCache), _U32, _U32]),
+    "enc_cache_commit": (_ST, [ctypes.POINTER(EncCache), _VP, _U32, _VP, _U64, _U64, _VP, _VP, _U32, _VP,
+                               _VP, _U64, _VP]),
+    "enc_cache_fork": (_ST, [ctypes.POINTER(EncCache), _VP, _VP, _U32, _VP]),
+    "enc_cache_truncate": (_ST, [ctypes.POINTER(EncCache), _VP, _VP, _U32, _VP]),
     "enc_status_string": (ctypes.c_char_p, [_ST]),
     "enc_last_error": (ctypes.c_char_p, []),
 }
@@ -514,6 +565,326 @@ def enc_stream_probe(src, dst, items_per_thread=1, threads_per_workgroup=256, st
     _check(lib().enc_stream_probe(_ptr(src), src.numel() * src.element_size(), _ptr(dst),
                                   dst.numel() * dst.element_size(), items_per_thread,
                                   threads_per_workgroup, _stream(stream)))
+
+
+# ------------------------------------------------------ one decoding step
+ENC_TREE_MAX_NODES = 256
+ENC_ROPE_ADJACENT, ENC_QK_NO_NORM = 1, 2
+_codes = {}
+
+
+def _code(t, what):
+    """Header element type of a floating tensor."""
+    if not _codes:
+        import torch
+        _codes.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+    code = _codes.get(t.dtype if hasattr(t, "dtype") else t)
+    if code is None:
+        raise TypeError("%s must be bfloat16, float16 or float32" % what)
+    return code
+
+
+def _on(stream):
+    """Context in which torch allocates for `stream`, so that memory of a
+    tensor made in a call is not handed out again before the call's work."""
+    import contextlib
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def _plain(t, what, dtype, shape, device):
+    """A contiguous CUDA tensor of exactly this type and shape (None in the
+    shape: any size); returns its address."""
+    if t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor on %s" % (what, dtype, device))
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), tuple(shape)))
+    return t.data_ptr()
+
+
+def _values(t, what, dtype, shape, device):
+    """A CUDA tensor of values with a contiguous last axis; returns its strides."""
+    if t.dtype != dtype or t.device != device:
+        raise ValueError("%s must be a %s tensor on %s" % (what, dtype, device))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), tuple(shape)))
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError("%s: the last axis must be contiguous" % what)
+    return st
+
+
+def _scratch(ws, device):
+    """Address and bytes of a workspace, which must lie on the same device."""
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor on %s" % device)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _device_of(t):
+    import torch
+    if not t.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("tensors are on %s, the current device is %d" % (t.device, torch.cuda.current_device()))
+    return t.device
+
+
+def enc_qk_norm_rope(q, k, v, positions, table, q_weight=None, k_weight=None, eps=1e-6, adjacent=False, norm=True,
+                     out_dtype=None, out=None, stream=None):
+    """Norm and rotate query and key heads, convert v (or None). q: [tokens,
+    q_heads, head_dim], k and v: [tokens, kv_heads, head_dim], of one type, any
+    strides that keep rows 16-byte aligned. positions: int32 [tokens]; table:
+    fp32 [max_pos, rot_dim], rot_dim/2 cosines then as many sines (None: no
+    rotation). out: (q, k, v) tensors, allocated in out_dtype (bfloat16) if
+    None; an out tensor may be its input. Returns (q, k, v)."""
+    import torch
+    device = _device_of(q)
+    tokens, q_heads, dim = q.shape
+    kv_heads = k.shape[1]
+    a = EncQkArgs()
+    qs = _values(q, "q", q.dtype, (tokens, q_heads, dim), device)
+    ks = _values(k, "k", q.dtype, (tokens, kv_heads, dim), device)
+    vs = _values(v, "v", q.dtype, (tokens, kv_heads, dim), device) if v is not None else (0, 0, 0)
+    if out is None:
+        dtype = out_dtype or torch.bfloat16
+        with _on(stream):
+            out = (torch.empty((tokens, q_heads, dim), dtype=dtype, device=device),
+                   torch.empty((tokens, kv_heads, dim), dtype=dtype, device=device),
+                   torch.empty((tokens, kv_heads, dim), dtype=dtype, device=device) if v is not None else None)
+    qo, ko, vo = out
+    qos = _values(qo, "q output", qo.dtype, (tokens, q_heads, dim), device)
+    kos = _values(ko, "k output", qo.dtype, (tokens, kv_heads, dim), device)
+    if v is not None:
+        vos = _values(vo, "v output", qo.dtype, (tokens, kv_heads, dim), device)
+        a.d_v, a.d_v_out = v.data_ptr(), vo.data_ptr()
+        a.v_token, a.v_head, a.v_out_token, a.v_out_head = vs[0], vs[1], vos[0], vos[1]
+    a.d_q, a.d_k, a.d_q_out, a.d_k_out = q.data_ptr(), k.data_ptr(), qo.data_ptr(), ko.data_ptr()
+    a.w_dtype = FP32
+    for name, w in (("d_q_weight", q_weight), ("d_k_weight", k_weight)):
+        if w is not None:
+            setattr(a, name, _plain(w, name[2:], w.dtype, (dim,), device))
+            a.w_dtype = _code(w, "a weight")
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise TypeError("the weights must have one type")
+    if table is not None:
+        a.d_positions = _plain(positions, "positions", torch.int32, (tokens,), device)
+        a.d_table = _plain(table, "table", torch.float32, (None, None), device)
+        a.max_pos, a.rot_dim = table.shape
+    a.q_token, a.q_head, a.k_token, a.k_head = qs[0], qs[1], ks[0], ks[1]
+    a.q_out_token, a.q_out_head, a.k_out_token, a.k_out_head = qos[0], qos[1], kos[0], kos[1]
+    a.tokens, a.q_heads, a.kv_heads, a.head_dim = tokens, q_heads, kv_heads, dim
+    a.in_dtype, a.out_dtype = _code(q, "q"), _code(qo, "the output")
+    a.flags = (ENC_ROPE_ADJACENT if adjacent else 0) | (0 if norm else ENC_QK_NO_NORM)
+    a.eps = eps
+    _check(lib().enc_qk_norm_rope(ctypes.byref(a), _stream(stream)))
+    return qo, ko, vo
+
+
+def _attention_sizes(q, k_new, table, k_cache):
+    a = EncTreeAttentionArgs()
+    a.batch, a.nodes, a.q_heads, a.head_dim = q.shape
+    a.kv_heads = k_new.shape[2]
+    a.dtype = _code(q, "q")
+    a.n_pages, a.page_size = k_cache.shape[0], k_cache.shape[1]
+    a.max_seqs, a.max_pages = table.shape
+    return a
+
+
+def enc_tree_attention_workspace_bytes(q, k_new, table, k_cache):
+    return int(lib().enc_tree_attention_workspace_bytes(ctypes.byref(_attention_sizes(q, k_new, table, k_cache))))
+
+
+def tree_attention_workspace(q, k_new, table, k_cache):
+    """A workspace for enc_tree_attention of these shapes (no initialisation needed)."""
+    return _empty_u8(enc_tree_attention_workspace_bytes(q, k_new, table, k_cache), q.device)
+
+
+def enc_tree_attention(q, k_new, v_new, k_cache, v_cache, table, lens, mask=None, seqs=None, nodes=None, scale=None,
+                       return_lse=False, out=None, ws=None, stream=None):
+    """Attention of a tree's nodes over a paged cache and the tree. q: [batch,
+    nodes, q_heads, head_dim]; k_new, v_new: [batch, nodes, kv_heads,
+    head_dim]; k_cache, v_cache: [n_pages, page_size, kv_heads, head_dim] with
+    the same strides; table: int32 [max_seqs, max_pages]; lens: int32
+    [max_seqs]; mask: int64 [batch, nodes, ceil(nodes / 64)] bit words, or None
+    for nodes j <= i; seqs: int32 [batch] rows of the table, or None; nodes:
+    int32 [batch] live nodes, or None. scale: 1 / sqrt(head_dim) if None.
+    Returns (out, lse or None)."""
+    import torch
+    device = _device_of(q)
+    batch, n, q_heads, dim = q.shape
+    kv_heads = k_new.shape[2]
+    a = _attention_sizes(q, k_new, table, k_cache)
+    a.q_batch, a.q_node, a.q_head, _ = _values(q, "q", q.dtype, q.shape, device)
+    a.k_new_batch, a.k_new_node, a.k_new_head, _ = _values(k_new, "k_new", q.dtype, (batch, n, kv_heads, dim), device)
+    a.v_new_batch, a.v_new_node, a.v_new_head, _ = _values(v_new, "v_new", q.dtype, (batch, n, kv_heads, dim), device)
+    cs = _values(k_cache, "k_cache", q.dtype, (a.n_pages, a.page_size, kv_heads, dim), device)
+    if _values(v_cache, "v_cache", q.dtype, k_cache.shape, device) != cs:
+        raise ValueError("k_cache and v_cache must have the same strides")
+    a.cache_page, a.cache_token, a.cache_head, _ = cs
+    a.d_q, a.d_k_new, a.d_v_new = q.data_ptr(), k_new.data_ptr(), v_new.data_ptr()
+    a.d_k_cache, a.d_v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    a.d_table = _plain(table, "table", torch.int32, (None, None), device)
+    a.d_lens = _plain(lens, "lens", torch.int32, (a.max_seqs,), device)
+    if mask is not None:
+        a.d_mask = _plain(mask, "mask", torch.int64, (batch, n, (n + 63) // 64), device)
+    if seqs is not None:
+        a.d_seqs = _plain(seqs, "seqs", torch.int32, (batch,), device)
+    if nodes is not None:
+        a.d_nodes = _plain(nodes, "nodes", torch.int32, (batch,), device)
+    lse = None
+    if out is None or return_lse or ws is None:
+        with _on(stream):
+            if out is None:
+                out = torch.empty((batch, n, q_heads, dim), dtype=q.dtype, device=device)
+            if return_lse:
+                lse = torch.empty((batch, n, q_heads), dtype=torch.float32, device=device)
+                a.d_lse = lse.data_ptr()
+            if ws is None:
+                ws = _empty_u8(lib().enc_tree_attention_workspace_bytes(ctypes.byref(a)), device)
+    a.out_batch, a.out_node, a.out_head, _ = _values(out, "out", q.dtype, q.shape, device)
+    a.d_out = out.data_ptr()
+    a.scale = dim ** -0.5 if scale is None else scale
+    _check(lib().enc_tree_attention(ctypes.byref(a), *_scratch(ws, device), _stream(stream)))
+    return out, lse
+
+
+def enc_verify_tree_workspace_bytes(batch, nodes, vocab):
+    return int(lib().enc_verify_tree_workspace_bytes(batch, nodes, vocab))
+
+
+def verify_tree_workspace(tokens, target):
+    """A zero-filled workspace for enc_verify_tree of these shapes (every call
+    leaves it ready for the next)."""
+    import torch
+    batch, nodes = tokens.shape
+    n = enc_verify_tree_workspace_bytes(batch, nodes, target.shape[2])
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=tokens.device)
+
+
+def enc_verify_tree(parents, tokens, target, draft, u, nodes=None, ws=None, stream=None):
+    """Verify a tree of drafted tokens. parents, tokens: int32 [batch, nodes];
+    target, draft (or None): [batch, nodes, vocab] probabilities of one type;
+    u: fp32 [batch, nodes] random numbers in [0, 1): u[:, i] decides on node i,
+    u[:, 0] draws the next token. Returns (path, count, token), int32."""
+    import torch
+    device = _device_of(tokens)
+    batch, n = tokens.shape
+    vocab = target.shape[2]
+    a = EncVerifyArgs()
+    a.d_parents = _plain(parents, "parents", torch.int32, (batch, n), device)
+    a.d_tokens = _plain(tokens, "tokens", torch.int32, (batch, n), device)
+    a.d_u = _plain(u, "u", torch.float32, (batch, n), device)
+    a.target_batch, a.target_node, _ = _values(target, "target", target.dtype, (batch, n, vocab), device)
+    a.d_target = target.data_ptr()
+    if draft is not None:
+        a.draft_batch, a.draft_node, _ = _values(draft, "draft", target.dtype, (batch, n, vocab), device)
+        a.d_draft = draft.data_ptr()
+    if nodes is not None:
+        a.d_nodes = _plain(nodes, "nodes", torch.int32, (batch,), device)
+    with _on(stream):
+        path = torch.empty((batch, n), dtype=torch.int32, device=device)
+        count = torch.empty((batch,), dtype=torch.int32, device=device)
+        token = torch.empty((batch,), dtype=torch.int32, device=device)
+        if ws is None:
+            ws = verify_tree_workspace(tokens, target)
+    a.d_path, a.d_count, a.d_token = path.data_ptr(), count.data_ptr(), token.data_ptr()
+    a.batch, a.nodes, a.vocab, a.dtype = batch, n, vocab, _code(target, "target")
+    _check(lib().enc_verify_tree(ctypes.byref(a), *_scratch(ws, device), _stream(stream)))
+    return path, count, token
+
+
+class Cache:
+    """Pages of a cache and their bookkeeping. data: [planes, n_pages,
+    page_size, ...] (2 planes per layer; a page's rows contiguous), table:
+    int32 [max_seqs, max_pages], lens: int32 [max_seqs], refs: int32 [n_pages];
+    new ones start with lengths 0, entries -1 and counts 0. `status`: int32 on
+    the device, what the last commit found (0: done)."""
+
+    def __init__(self, data, table, lens, refs):
+        import torch
+        device = _device_of(data)
+        planes, pages, page = data.shape[:3]
+        row = data[0, 0, 0].numel()
+        st = data.stride()
+        if data.dim() < 4 or not data[0].is_contiguous():
+            raise ValueError("data must be [planes, pages, page_size, ...] with contiguous planes")
+        size = data.element_size()
+        c = EncCache()
+        c.d_data = data.data_ptr()
+        c.d_table = _plain(table, "table", torch.int32, (None, None), device)
+        c.d_lens = _plain(lens, "lens", torch.int32, (table.shape[0],), device)
+        c.d_refs = _plain(refs, "refs", torch.int32, (pages,), device)
+        c.plane_stride = st[0] * size
+        c.n_planes, c.n_pages, c.page_size, c.row_bytes = planes, pages, page, row * size
+        c.max_seqs, c.max_pages = table.shape
+        self.c, self.data, self.table, self.lens, self.refs = c, data, table, lens, refs
+        self.row_shape = data.shape[3:]
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    @classmethod
+    def empty(cls, planes, n_pages, page_size, row_shape, max_seqs, max_pages, dtype=None, device="cuda"):
+        """A cache with nothing in it."""
+        import torch
+        return cls(torch.empty((planes, n_pages, page_size) + tuple(row_shape), dtype=dtype or torch.bfloat16,
+                               device=device),
+                   torch.full((max_seqs, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(max_seqs, dtype=torch.int32, device=device),
+                   torch.zeros(n_pages, dtype=torch.int32, device=device))
+
+
+def enc_cache_workspace_bytes(cache, batch, nodes):
+    return int(lib().enc_cache_workspace_bytes(ctypes.byref(cache.c), batch, nodes))
+
+
+def cache_workspace(cache, path):
+    """A workspace for enc_cache_commit with this path's shape (no initialisation needed)."""
+    return _empty_u8(enc_cache_workspace_bytes(cache, path.shape[0], path.shape[1]), cache.data.device)
+
+
+def enc_cache_commit(cache, seqs, draft, path, count, ws=None, stream=None):
+    """Append rows path[b, :count[b]] of draft [planes, batch, nodes, ...] to
+    sequence seqs[b] of the cache. Returns cache.status (on the device: 0, or
+    why nothing was changed)."""
+    import torch
+    device = _device_of(cache.data)
+    batch, nodes = path.shape
+    if draft.dtype != cache.data.dtype or draft.device != device:
+        raise ValueError("draft must have the cache's type and device")
+    if draft.shape != (cache.c.n_planes, batch, nodes) + tuple(cache.row_shape):
+        raise ValueError("draft has shape %s" % (tuple(draft.shape),))
+    if batch and not draft[0, 0].is_contiguous():
+        raise ValueError("a sequence's draft rows must be contiguous")
+    st, size = draft.stride(), draft.element_size()
+    if ws is None:
+        with _on(stream):
+            ws = cache_workspace(cache, path)
+    _check(lib().enc_cache_commit(
+        ctypes.byref(cache.c), _plain(seqs, "seqs", torch.int32, (batch,), device), batch, draft.data_ptr(),
+        st[0] * size, st[1] * size, _plain(path, "path", torch.int32, (batch, nodes), device),
+        _plain(count, "count", torch.int32, (batch,), device), nodes, cache.status.data_ptr(),
+        *_scratch(ws, device), _stream(stream)))
+    return cache.status
+
+
+def enc_cache_fork(cache, src, dst, stream=None):
+    """Sequence dst[i] lets go of its pages and shares those of src[i]."""
+    import torch
+    device = _device_of(cache.data)
+    _check(lib().enc_cache_fork(
+        ctypes.byref(cache.c), _plain(src, "src", torch.int32, (None,), device),
+        _plain(dst, "dst", torch.int32, src.shape, device), src.shape[0], _stream(stream)))
+
+
+def enc_cache_truncate(cache, seqs, lens, stream=None):
+    """Cut sequence seqs[i] to lens[i] tokens and free the pages past its end."""
+    import torch
+    device = _device_of(cache.data)
+    _check(lib().enc_cache_truncate(
+        ctypes.byref(cache.c), _plain(seqs, "seqs", torch.int32, (None,), device),
+        _plain(lens, "lens", torch.int32, seqs.shape, device), seqs.shape[0], _stream(stream)))
 
 
 def enc_status_string(status):
