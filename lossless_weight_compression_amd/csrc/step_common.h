@@ -68,8 +68,9 @@ struct TreeAttnArgs {
   float *part_ml;            // [batch, kv_heads, splits, rows, 2] running maximum and sum
 };
 struct TreeAttnPlan {
-  uint32_t units;            // 16-row units a wave holds
-  uint32_t row_ways;         // waves of a workgroup that hold different rows
+  uint32_t wide;             // rows on different waves, keys through LDS
+  uint32_t units, waves;     // 16-row units a wave holds; waves of a workgroup
+  uint32_t ways, unit;       // waves that take different keys; keys in a unit of work
   uint32_t row_tiles, splits;
   uint64_t part_bytes, ml_bytes;
 };

@@ -32,6 +32,8 @@
 // each) or different strips, joined through LDS at the end.
 #include "step_common.h"
 
+#include <type_traits>
+
 namespace enc {
 namespace {
 
@@ -64,10 +66,31 @@ template <> struct Half<_Float16> {
   }
 };
 
+// Maximum / sum over the four lanes that hold the same query row (l, l ^ 16,
+// l ^ 32, l ^ 48), by exchanging rows of 16 lanes: no LDS round trip.
+__device__ __forceinline__ float rows_max(float x) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float rows_sum(float x) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
 // Strips a workgroup takes: an equal share, whole rounds of its key ways.
 __device__ __forceinline__ uint32_t split_chunk(uint32_t strips, uint32_t splits, uint32_t ways) {
   const uint32_t c = (strips + splits - 1) / splits;
   return max((c + ways - 1) / ways * ways, ways);
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint2 read_transposed(const void *lds) {
+  typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(uintptr_t)lds));
 }
 
 struct Seq {
@@ -90,10 +113,22 @@ __device__ __forceinline__ Seq sequence_of(const enc_tree_attention_args &a, uin
   return q;
 }
 
+// Bit j: node i of tree b may see node first + j.
+__device__ __forceinline__ uint32_t tree_bits(const enc_tree_attention_args &a, const TreeAttnArgs &k, uint32_t b,
+                                              uint32_t i, uint32_t first, uint32_t live) {
+  if (first >= live) return 0;
+  uint32_t bits = live - first < 32 ? (1u << (live - first)) - 1u : 0xFFFFFFFFu;
+  if (a.d_mask)
+    bits &= reinterpret_cast<const uint32_t *>(a.d_mask)[((uint64_t)b * a.nodes + i) * k.mask_words + first / 32];
+  else
+    bits &= i >= first + 31 ? 0xFFFFFFFFu : i < first ? 0u : (2u << (i - first)) - 1u;
+  return bits;
+}
+
 // DP: head_dim rounded up to what the fragments hold; EXACT: equal to it.
 // U: 16-row units of a wave.
 template <typename T, int DP, int U, bool EXACT>
-__global__ __launch_bounds__(256) void k_tree_attention(TreeAttnArgs k, uint32_t row_ways) {
+__global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(TreeAttnArgs k) {
   constexpr int KS = DP / 32;                   // k steps of Q K^T
   constexpr int C = DP >= 128 ? 8 : DP / 16;    // consecutive values a lane transposes
   constexpr int NH = DP / (16 * C);             // groups of 16 C values
@@ -105,21 +140,17 @@ __global__ __launch_bounds__(256) void k_tree_attention(TreeAttnArgs k, uint32_t
   const uint32_t l16 = lane & 15, g4 = lane >> 4;
   const uint32_t D = a.head_dim;
 
-  // workgroups of one (sequence, split, head) differ in 8, so they meet in one
-  // compute die's L2 (workgroups go to the 8 dies in turn)
-  const uint32_t groups = a.batch * k.splits * a.kv_heads;
-  const uint32_t id8 = blockIdx.x >> 3;
-  const uint32_t grp = id8 / k.row_tiles * 8 + (blockIdx.x & 7), rt = id8 % k.row_tiles;
-  if (grp >= groups) return;
-  const uint32_t h = grp % a.kv_heads, bs = grp / a.kv_heads, split = bs % k.splits, b = bs / k.splits;
+  const uint32_t grp = blockIdx.x;
+  const uint32_t bs = grp / a.kv_heads, h = (grp + bs) % a.kv_heads, split = bs % k.splits, b = bs / k.splits;
   const Seq q = sequence_of(a, b);
-  const uint32_t ways = kWavesA / row_ways, rw = wave % row_ways, kw = wave / row_ways;
+  constexpr uint32_t ways = kWavesA;
+  const uint32_t kw = wave;
   const uint32_t chunk = split_chunk(q.strips, k.splits, ways);
   const uint32_t lo = split * chunk, hi = min(lo + chunk, q.strips);
   if (lo >= q.strips && k.splits > 1) return;   // nothing for this split; the join does not look for it
 
   // ---- Q fragments: query row l % 16 of each unit, 8 values per k step
-  const uint32_t row0 = (rt * row_ways + rw) * (U * 16) + l16;
+  const uint32_t row0 = l16;
   uint4 qf[U][KS];
   uint32_t node[U];
   bool alive[U];
@@ -215,132 +246,144 @@ __global__ __launch_bounds__(256) void k_tree_attention(TreeAttnArgs k, uint32_t
     }
   };
 
+  // One strip, its K and V on the way into the registers. SPECIAL: a last strip
+  // that is not full, and the tree's: keys that a row may not see score
+  // -infinity, values that are no keys' or (tree) not finite become 0. `after_k`
+  // and `after_v` load the next strip's halves.
+  bool strange = false;   // infinities or NaN were among the tree's values
+  auto compute = [&](auto special_, uint32_t strip, auto after_k, auto after_v) {
+    constexpr bool SPECIAL = decltype(special_)::value;
+    float p[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < KS; ++e) s = Half<T>::mfma(kf[t][e], qf[u][e], s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[u][4 * t + e] = s[e];
+      }
+    after_k();
+
+    const bool tree = SPECIAL && strip >= q.strips_ctx;
+    const uint32_t first = (tree ? strip - q.strips_ctx : strip) * 32;
+    const uint32_t valid = SPECIAL ? min((tree ? q.live : q.len) - first, 32u) : 32;
+    uint32_t seen[U];
+    if constexpr (SPECIAL) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        uint32_t bits = valid < 32 ? (1u << valid) - 1u : 0xFFFFFFFFu;
+        if (tree) bits = alive[u] ? tree_bits(a, k, b, node[u], first, q.live) : 0u;
+        seen[u] = bits;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool is_key = 16 * (j >> 2) + 4 * g4 + (j & 3) < valid;
+#pragma unroll
+        for (int n = 0; n < NH; ++n)
+#pragma unroll
+          for (int w = 0; w < C / 2; ++w) {
+            uint32_t t = is_key ? vr[j][n][w] : 0u;
+            constexpr uint32_t E = Half<T>::kExp;
+            if (tree && (t & E) == E) t &= 0xFFFF0000u, strange = true;
+            if (tree && (t & (E << 16)) == (E << 16)) t &= 0x0000FFFFu, strange = true;
+            vr[j][n][w] = t;
+          }
+      }
+    }
+
+    uint4 pf[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float top = kLowest;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        p[u][j] *= a.scale;
+        if constexpr (SPECIAL)
+          if (!(seen[u] >> (16 * (j >> 2) + 4 * g4 + (j & 3)) & 1u)) p[u][j] = -__builtin_inff();
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, p[u][j]);
+      top = rows_max(top);
+      if (__any(top > m[u] + (kSlack + Half<T>::kLift))) {
+        const float up = fmaxf(top - Half<T>::kLift, m[u]), shrink = exp_of(m[u] - up);
+        m[u] = up;
+        l[u] *= shrink;
+#pragma unroll
+        for (int n = 0; n < NH; ++n)
+#pragma unroll
+          for (int f = 0; f < C; ++f) o[u][n][f] *= shrink;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        p[u][j] = exp_of(p[u][j] - m[u]);
+        l[u] += p[u][j];
+      }
+      pf[u] = make_uint4(pack2<T>(p[u][0], p[u][1]), pack2<T>(p[u][2], p[u][3]), pack2<T>(p[u][4], p[u][5]),
+                         pack2<T>(p[u][6], p[u][7]));
+    }
+#pragma unroll
+    for (int n = 0; n < NH; ++n)
+#pragma unroll
+      for (int f = 0; f < C; ++f) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = __builtin_amdgcn_perm(vr[2 * e + 1][n][f >> 1], vr[2 * e][n][f >> 1],
+                                       f & 1 ? 0x07060302u : 0x05040100u);
+        const uint4 vf = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) o[u][n][f] = Half<T>::mfma(vf, pf[u], o[u][n][f]);
+      }
+
+    after_v();
+  };
+
   uint32_t strip = lo + kw;
-  if (strip < hi) {
-    uint32_t ko, vo;
+  const uint32_t whole = min(hi, q.len / 32);     // strips of 32 cached keys
+  uint32_t ko, vo;
+  if (strip < whole) {
     offsets_of(strip, entry_of(strip), ko, vo);
     load_k(strip, ko);
     load_v(strip, vo);
-    int32_t entry = strip + ways < hi ? entry_of(strip + ways) : 0;
+    int32_t entry = strip + ways < whole ? entry_of(strip + ways) : 0;
     while (true) {
       const uint32_t next = strip + ways;
-      const bool more = next < hi, tree = strip >= q.strips_ctx;
-      const uint32_t first = (tree ? strip - q.strips_ctx : strip) * 32;
-      const uint32_t valid = min((tree ? q.live : q.len) - first, 32u);
+      const bool more = next < whole;
       if (more) offsets_of(next, entry, ko, vo);
-
-      float p[U][8];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          f32x4 s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int e = 0; e < KS; ++e) s = Half<T>::mfma(kf[t][e], qf[u][e], s);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) p[u][4 * t + e] = s[e];
-        }
-      if (more) {
-        load_k(next, ko);
-        entry = next + ways < hi ? entry_of(next + ways) : 0;
-      }
-
-      // a last strip that is not full, and the tree's: keys that a row may not
-      // see score -infinity, values that are no keys' or (tree) not finite
-      // become 0
-      uint32_t seen[U];
-      bool strange = false;
-      const bool special = tree || valid < 32;
-      if (special) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          uint32_t bits = valid < 32 ? (1u << valid) - 1u : 0xFFFFFFFFu;
-          if (tree) {
-            if (!alive[u])
-              bits = 0;
-            else if (a.d_mask)
-              bits &= reinterpret_cast<const uint32_t *>(a.d_mask)[((uint64_t)b * a.nodes + node[u]) * k.mask_words +
-                                                                    first / 32];
-            else
-              bits &= node[u] >= first + 31 ? 0xFFFFFFFFu : node[u] < first ? 0u : (2u << (node[u] - first)) - 1u;
-          }
-          seen[u] = bits;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const bool is_key = 16 * (j >> 2) + 4 * g4 + (j & 3) < valid;
-#pragma unroll
-          for (int n = 0; n < NH; ++n)
-#pragma unroll
-            for (int w = 0; w < C / 2; ++w) {
-              uint32_t t = is_key ? vr[j][n][w] : 0u;
-              constexpr uint32_t E = Half<T>::kExp;
-              if (tree && (t & E) == E) t &= 0xFFFF0000u, strange = true;
-              if (tree && (t & (E << 16)) == (E << 16)) t &= 0x0000FFFFu, strange = true;
-              vr[j][n][w] = t;
-            }
-        }
-      }
-
-      uint4 pf[U];
+      compute(
+          std::false_type{}, strip,
+          [&] {
+            if (!more) return;
+            load_k(next, ko);
+            entry = next + ways < whole ? entry_of(next + ways) : 0;
+          },
+          [&] {
+            if (more) load_v(next, vo);
+          });
+      strip = next;
+      if (!more) break;
+    }
+  }
+  for (; strip < hi; strip += ways) {
+    offsets_of(strip, entry_of(strip), ko, vo);
+    load_k(strip, ko);
+    load_v(strip, vo);
+    compute(std::true_type{}, strip, [] {}, [] {});
+  }
+  // Infinities and NaN went in as zeros, since 0 times them would reach rows
+  // that do not see them: add them to the rows that do.
+  if (__any(strange)) {
+    for (strip = lo + kw; strip < hi; strip += ways) {
+      if (strip < q.strips_ctx) continue;
+      const uint32_t first = (strip - q.strips_ctx) * 32;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        float top = kLowest;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[u][j] *= a.scale;
-        if (special) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (!(seen[u] >> (16 * (j >> 2) + 4 * g4 + (j & 3)) & 1u)) p[u][j] = -__builtin_inff();
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, p[u][j]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        if (__any(top > m[u] + (kSlack + Half<T>::kLift))) {
-          const float up = fmaxf(top - Half<T>::kLift, m[u]), shrink = exp_of(m[u] - up);
-          m[u] = up;
-          l[u] *= shrink;
-#pragma unroll
-          for (int n = 0; n < NH; ++n)
-#pragma unroll
-            for (int f = 0; f < C; ++f) o[u][n][f] *= shrink;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          p[u][j] = exp_of(p[u][j] - m[u]);
-          l[u] += p[u][j];
-        }
-        pf[u] = make_uint4(pack2<T>(p[u][0], p[u][1]), pack2<T>(p[u][2], p[u][3]), pack2<T>(p[u][4], p[u][5]),
-                           pack2<T>(p[u][6], p[u][7]));
-      }
-#pragma unroll
-      for (int n = 0; n < NH; ++n)
-#pragma unroll
-        for (int f = 0; f < C; ++f) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = __builtin_amdgcn_perm(vr[2 * e + 1][n][f >> 1], vr[2 * e][n][f >> 1],
-                                         f & 1 ? 0x07060302u : 0x05040100u);
-          const uint4 vf = make_uint4(w[0], w[1], w[2], w[3]);
-#pragma unroll
-          for (int u = 0; u < U; ++u) o[u][n][f] = Half<T>::mfma(vf, pf[u], o[u][n][f]);
-        }
-
-      // Infinities and NaN among the tree's values: add them to the rows that
-      // see them (each wave's p through its own part of `joint`).
-      if (special && __any(strange)) {
-        float *mine = joint + wave * (U * 8 * 64);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) mine[(u * 8 + j) * 64 + lane] = p[u][j];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        for (uint32_t key = 0; key < valid; ++key) {
+        const uint32_t seen = alive[u] ? tree_bits(a, k, b, node[u], first, q.live) : 0u;
+        for (uint32_t key = 0; key < 32 && first + key < q.live; ++key) {
           const T *row = vn + (uint64_t)(first + key) * a.v_new_node;
-          const uint32_t at = ((key >> 4) * 4 + (key & 3)) * 64 + ((key >> 2) & 3) * 16 + l16;
+          if (!(seen >> key & 1u)) continue;
 #pragma unroll
           for (int n = 0; n < NH; ++n)
 #pragma unroll
@@ -349,30 +392,19 @@ __global__ __launch_bounds__(256) void k_tree_attention(TreeAttnArgs k, uint32_t
               for (int f = 0; f < C; ++f) {
                 const uint32_t d = (n * 16 + 4 * g4 + i) * C + f;
                 const float v = EXACT || d < D ? (float)row[d] : 0.f;
-                if (!__builtin_isfinite(v)) {
-#pragma unroll
-                  for (int u = 0; u < U; ++u)
-                    if (seen[u] >> key & 1u) o[u][n][f][i] += mine[u * 8 * 64 + at] * v;
-                }
+                if (!__builtin_isfinite(v)) o[u][n][f][i] += v;
               }
         }
-        __builtin_amdgcn_wave_barrier();
       }
-      if (!more) break;
-      load_v(next, vo);
-      strip = next;
     }
   }
 
   // ---- join the waves that hold the same rows
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    l[u] += __shfl_xor(l[u], 16);
-    l[u] += __shfl_xor(l[u], 32);
-  }
+  for (int u = 0; u < U; ++u) l[u] = rows_sum(l[u]);
   __syncthreads();
   for (uint32_t st = ways / 2; st; st >>= 1) {
-    const uint32_t slot = (kw & (st - 1)) * row_ways + rw;
+    const uint32_t slot = kw & (st - 1);
     float *mine = joint + slot * (NREG + 2 * U) * 64 + lane;
     if (kw >= st && kw < 2 * st) {
       uint32_t at = 0;
@@ -459,10 +491,298 @@ __global__ __launch_bounds__(256) void k_tree_attention(TreeAttnArgs k, uint32_t
   }
 }
 
+// ---- many rows: K and V through LDS
+//
+// W waves of U units each hold W U 16 different rows and go through the same
+// keys, a stage of SK at a time, held twice in LDS (the next stage is on its
+// way into registers while one is computed). Rows of a stage lie 16 bytes
+// further apart than they are long, so that reading one chunk of 16 rows (K)
+// and 32 bytes of 16 rows (V) touches all banks evenly, at offsets known at
+// compile time. V^T fragments come from ds_read_b64_tr: of 16 lanes, lane
+// 4 j + c names values 4 c .. 4 c + 3 of key j, and lane i gets value i of the
+// 4 keys.
+template <typename T, int DP, int U, int W>
+__global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs k) {
+  constexpr int KS = DP / 32, NF = DP / 16, NCH = DP / 8;
+  constexpr int SK = DP == 256 ? 32 : 64;
+  constexpr int NT = 64 * W, NR = SK * NCH / NT;   // chunks of K (and of V) a thread brings in
+  constexpr int PITCH = NCH + 1;                   // 16-byte chunks from row to row
+  const enc_tree_attention_args &a = k.a;
+  __shared__ __align__(16) uint4 ks[2][SK * PITCH], vs[2][SK * PITCH];
+  __shared__ uint32_t odd;
+
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint32_t l16 = lane & 15, g4 = lane >> 4;
+  const uint32_t D = a.head_dim;
+  // workgroups of one (sequence, split, head) differ in 8, so they meet in one
+  // compute die's L2 (workgroups go to the 8 dies in turn)
+  const uint32_t groups = a.batch * k.splits * a.kv_heads;
+  const uint32_t id8 = blockIdx.x >> 3;
+  const uint32_t grp = id8 / k.row_tiles * 8 + (blockIdx.x & 7), rt = id8 % k.row_tiles;
+  if (grp >= groups) return;
+  const uint32_t bs = grp / a.kv_heads, h = (grp + bs) % a.kv_heads, split = bs % k.splits, b = bs / k.splits;
+  const Seq q = sequence_of(a, b);
+  const uint32_t ctx = (q.len + SK - 1) / SK, stages = ctx + (q.live + SK - 1) / SK;
+  const uint32_t chunk = split_chunk(stages, k.splits, 1);
+  const uint32_t lo = split * chunk, hi = min(lo + chunk, stages);
+  if (lo >= stages && k.splits > 1) return;
+
+  const uint32_t row0 = (rt * W + wave) * (U * 16) + l16;
+  const bool busy = (rt * W + wave) * (U * 16) < k.rows;   // this wave has rows
+  uint4 qf[U][KS];
+  uint32_t node[U];
+  bool alive[U];
+  const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;   // -scale (-q).k
+  const float scale = fabsf(a.scale), c2 = scale * kLog2e;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t r = row0 + 16 * u;
+    const uint32_t rr = min(r, k.rows - 1);
+    node[u] = k.group.quot(rr);
+    const uint32_t head = h * k.group.d + (rr - node[u] * k.group.d);
+    alive[u] = r < k.rows && node[u] < q.live;
+    const T *p = static_cast<const T *>(a.d_q) + b * a.q_batch + node[u] * a.q_node + head * a.q_head;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const uint32_t d = 32 * s + 8 * g4;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (alive[u] && d < D) v = *reinterpret_cast<const uint4 *>(p + d);
+      qf[u][s] = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+    }
+  }
+  f32x4 o[U][NF];
+  float m[U], mc[U], l[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    m[u] = kLowest;
+    mc[u] = kLowest;
+    l[u] = 0.f;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) o[u][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  bool far = false;   // some row's maximum times log2(e) leaves fp32
+
+  // ---- bringing a stage in: thread's chunk i is chunk ch of row r0 + i rstep
+  const uint32_t ch = tid % NCH, r0 = tid / NCH;
+  constexpr uint32_t kRowStep = NT / NCH;
+  const bool chunk_live = ch * 8 < D;
+  const uint4 *kc = static_cast<const uint4 *>(a.d_k_cache) + h * (a.cache_head / 8) + ch;
+  const uint4 *vc = static_cast<const uint4 *>(a.d_v_cache) + h * (a.cache_head / 8) + ch;
+  const T *kn = static_cast<const T *>(a.d_k_new) + b * a.k_new_batch + h * a.k_new_head;
+  const T *vn = static_cast<const T *>(a.d_v_new) + b * a.v_new_batch + h * a.v_new_head;
+  const uint32_t page_units = (uint32_t)(a.cache_page / 8), token_units = (uint32_t)(a.cache_token / 8);
+  uint4 kr[NR], vr[NR];
+  int32_t entry[NR];
+  auto find = [&](uint32_t st) {
+    if (st >= ctx) return;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) entry[i] = q.table[k.page.quot(min(st * SK + r0 + i * kRowStep, q.len - 1))];
+  };
+  auto fetch = [&](uint32_t st) {
+    const bool tree = st >= ctx;
+    const uint32_t first = (tree ? st - ctx : st) * SK, end = tree ? q.live : q.len;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const uint32_t key = first + r0 + i * kRowStep;
+      kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+      if (key < end && chunk_live) {
+        if (tree) {
+          kr[i] = *(reinterpret_cast<const uint4 *>(kn + key * a.k_new_node) + ch);
+          vr[i] = *(reinterpret_cast<const uint4 *>(vn + key * a.v_new_node) + ch);
+        } else {
+          const uint32_t page = min((uint32_t)max(entry[i], 0), a.n_pages - 1);
+          const uint32_t at = page * page_units + (key - k.page.quot(key) * k.page.d) * token_units;
+          kr[i] = kc[at];
+          vr[i] = vc[at];
+        }
+      }
+    }
+  };
+  auto place = [&](uint32_t st, uint32_t buf) {
+    if (st >= ctx) {   // the tree's values go in finite
+      constexpr uint32_t E = Half<T>::kExp;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        uint32_t w[4] = {vr[i].x, vr[i].y, vr[i].z, vr[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if ((w[e] & E) == E) w[e] &= 0xFFFF0000u, bad = true;
+          if ((w[e] & (E << 16)) == (E << 16)) w[e] &= 0x0000FFFFu, bad = true;
+        }
+        vr[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (bad) odd = 1;
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const uint32_t at = (r0 + i * kRowStep) * PITCH + ch;
+      ks[buf][at] = kr[i];
+      vs[buf][at] = vr[i];
+    }
+  };
+
+  // ---- one strip of 32 keys of a stage
+  auto compute = [&](auto special_, uint32_t st, uint32_t half, uint32_t buf) {
+    constexpr bool SPECIAL = decltype(special_)::value;
+    float p[U][8];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint4 *row = ks[buf] + (half * 32 + 16 * t + l16) * PITCH + g4;
+      f32x4 s[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < KS; ++e) {
+        const uint4 kf = row[4 * e];
+#pragma unroll
+        for (int u = 0; u < U; ++u) s[u] = Half<T>::mfma(kf, qf[u][e], s[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[u][4 * t + e] = s[u][e];
+    }
+
+    const bool tree = SPECIAL && st >= ctx;
+    const uint32_t first = (tree ? st - ctx : st) * SK + half * 32, end = tree ? q.live : q.len;
+    uint32_t seen[U];
+    if constexpr (SPECIAL) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        uint32_t bits = end >= first + 32 ? 0xFFFFFFFFu : end <= first ? 0u : (1u << (end - first)) - 1u;
+        if (tree) bits = alive[u] ? tree_bits(a, k, b, node[u], first, q.live) : 0u;
+        seen[u] = bits;
+      }
+    }
+    uint4 pf[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (SPECIAL) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (!(seen[u] >> (16 * (j >> 2) + 4 * g4 + (j & 3)) & 1u)) p[u][j] = -__builtin_inff();
+      }
+      float top = p[u][0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) top = fmaxf(top, p[u][j]);
+      top = rows_max(top) * scale;
+      if (__any(top > m[u] + (kSlack + Half<T>::kLift))) {
+        const float up = fmaxf(top - Half<T>::kLift, m[u]), shrink = exp_of(m[u] - up);
+        m[u] = up;
+        mc[u] = fmaxf(up * kLog2e, kLowest);   // a row that has seen nothing keeps a finite one
+        far = far || __any(!(fabsf(up) < 1e38f) && up != kLowest);
+        l[u] *= shrink;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) o[u][f] *= shrink;
+      }
+      if (far) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[u][j] = exp_of(fmaf(p[u][j], scale, -m[u]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[u][j] = __builtin_amdgcn_exp2f(fmaf(p[u][j], c2, -mc[u]));
+      }
+      l[u] += ((p[u][0] + p[u][1]) + (p[u][2] + p[u][3])) + ((p[u][4] + p[u][5]) + (p[u][6] + p[u][7]));
+      pf[u] = make_uint4(pack2<T>(p[u][0], p[u][1]), pack2<T>(p[u][2], p[u][3]), pack2<T>(p[u][4], p[u][5]),
+                         pack2<T>(p[u][6], p[u][7]));
+    }
+    const char *vb = reinterpret_cast<const char *>(vs[buf] + (half * 32 + 4 * g4 + (l16 >> 2)) * PITCH) + (l16 & 3) * 8;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const uint2 v0 = read_transposed(vb + 32 * f), v1 = read_transposed(vb + 16 * PITCH * 16 + 32 * f);
+      const uint4 vf = make_uint4(v0.x, v0.y, v1.x, v1.y);
+#pragma unroll
+      for (int u = 0; u < U; ++u) o[u][f] = Half<T>::mfma(vf, pf[u], o[u][f]);
+    }
+  };
+
+  if (tid == 0) odd = 0;
+  __syncthreads();
+  if (lo < hi) {
+    find(lo);
+    fetch(lo);
+    if (lo + 1 < hi) find(lo + 1);
+    for (uint32_t st = lo; st < hi; ++st) {
+      const uint32_t buf = (st - lo) & 1;
+      place(st, buf);
+      if (st + 1 < hi) fetch(st + 1);
+      if (st + 2 < hi) find(st + 2);
+      __syncthreads();
+      if (busy) {
+        const bool whole = st < ctx && (st + 1) * SK <= q.len;
+        if (whole) {
+#pragma unroll 1
+          for (uint32_t half = 0; half < SK / 32; ++half) compute(std::false_type{}, st, half, buf);
+        } else {
+#pragma unroll 1
+          for (uint32_t half = 0; half < SK / 32; ++half) compute(std::true_type{}, st, half, buf);
+        }
+      }
+    }
+  }
+  if (!busy) return;
+  // infinities and NaN, left out above: to the rows that see them
+  if (hi > ctx && odd) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      for (uint32_t first = (max(lo, ctx) - ctx) * SK; first < (hi - ctx) * SK && first < q.live; first += 32) {
+        const uint32_t seen = alive[u] ? tree_bits(a, k, b, node[u], first, q.live) : 0u;
+        for (uint32_t key = 0; key < 32 && first + key < q.live; ++key) {
+          const T *row = vn + (uint64_t)(first + key) * a.v_new_node;
+          if (!(seen >> key & 1u)) continue;
+#pragma unroll
+          for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t d = 16 * f + 4 * g4 + i;
+              const float v = d < D ? (float)row[d] : 0.f;
+              if (!__builtin_isfinite(v)) o[u][f][i] += v;
+            }
+        }
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    l[u] = rows_sum(l[u]);
+    const uint32_t r = row0 + 16 * u;
+    if (r >= k.rows) continue;
+    if (k.splits == 1) {
+      const uint32_t head = h * k.group.d + (r - node[u] * k.group.d);
+      T *dst = static_cast<T *>(a.d_out) + b * a.out_batch + node[u] * a.out_node + head * a.out_head;
+      const bool any = alive[u] && l[u] != 0.f;
+      const float inv = any ? 1.0f / l[u] : 0.f;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const uint32_t d = 16 * f + 4 * g4;
+        if (d < D)
+          *reinterpret_cast<uint2 *>(dst + d) =
+              any ? make_uint2(pack2<T>(o[u][f][0] * inv, o[u][f][1] * inv), pack2<T>(o[u][f][2] * inv, o[u][f][3] * inv))
+                  : make_uint2(0u, 0u);
+      }
+      if (a.d_lse && g4 == 0)
+        a.d_lse[((uint64_t)b * a.nodes + node[u]) * a.q_heads + head] =
+            any ? m[u] + __log2f(l[u]) * kLn2 : -__builtin_inff();
+    } else {
+      const uint64_t at = (((uint64_t)b * a.kv_heads + h) * k.splits + split) * k.rows + r;
+      if (g4 == 0) {
+        k.part_ml[2 * at] = m[u];
+        k.part_ml[2 * at + 1] = l[u];
+      }
+      float *dst = k.part + at * D;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const uint32_t d = 16 * f + 4 * g4;
+        if (d < D) *reinterpret_cast<f32x4 *>(dst + d) = o[u][f];
+      }
+    }
+  }
+}
+
 // One wave per query row: the parts' sums, brought to their common maximum
 // and added in the order of the splits (64 / LD of them side by side).
 template <typename T, uint32_t LD>
-__global__ __launch_bounds__(256) void k_tree_attention_join(TreeAttnArgs k, uint32_t ways) {
+__global__ __launch_bounds__(256) void k_tree_attention_join(TreeAttnArgs k, uint32_t unit, uint32_t ways) {
   const enc_tree_attention_args &a = k.a;
   constexpr uint32_t W = 64 / LD;
   const uint32_t lane = threadIdx.x & 63;
@@ -471,8 +791,10 @@ __global__ __launch_bounds__(256) void k_tree_attention_join(TreeAttnArgs k, uin
   const uint32_t bh = item / k.rows, r = item - bh * k.rows;
   const uint32_t b = bh / a.kv_heads, h = bh - b * a.kv_heads;
   const Seq q = sequence_of(a, b);
-  const uint32_t chunk = split_chunk(q.strips, k.splits, ways);
-  const uint32_t live = (q.strips + chunk - 1) / chunk;
+  // the splits that had something: units of `unit` keys, as they counted them
+  const uint32_t units = (q.len + unit - 1) / unit + (q.live + unit - 1) / unit;
+  const uint32_t chunk = split_chunk(units, k.splits, ways);
+  const uint32_t live = (units + chunk - 1) / chunk;
   const uint32_t node = k.group.quot(r), head = h * k.group.d + (r - node * k.group.d);
 
   const uint64_t row = (uint64_t)bh * k.splits * k.rows + r;
@@ -507,23 +829,36 @@ __global__ __launch_bounds__(256) void k_tree_attention_join(TreeAttnArgs k, uin
 }
 
 template <typename T, int DP, int U>
-void launch_unit(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
-  const uint32_t groups = k.a.batch * k.splits * k.a.kv_heads;
-  const dim3 grid((groups + 7) / 8 * 8 * k.row_tiles), block(256);
+void launch_unit(const TreeAttnArgs &k, hipStream_t s) {
+  const dim3 grid(k.a.batch * k.splits * k.a.kv_heads), block(256);
   if (k.a.head_dim == DP)
-    hipLaunchKernelGGL((k_tree_attention<T, DP, U, true>), grid, block, 0, s, k, p.row_ways);
+    hipLaunchKernelGGL((k_tree_attention<T, DP, U, true>), grid, block, 0, s, k);
   else
-    hipLaunchKernelGGL((k_tree_attention<T, DP, U, false>), grid, block, 0, s, k, p.row_ways);
+    hipLaunchKernelGGL((k_tree_attention<T, DP, U, false>), grid, block, 0, s, k);
+}
+
+template <typename T, int DP, int U, int W>
+void launch_wide(const TreeAttnArgs &k, hipStream_t s) {
+  const uint32_t groups = k.a.batch * k.splits * k.a.kv_heads;
+  hipLaunchKernelGGL((k_tree_attention_wide<T, DP, U, W>), dim3((groups + 7) / 8 * 8 * k.row_tiles), dim3(64 * W), 0, s,
+                     k);
 }
 
 template <typename T, int DP>
 void launch_dim(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
-  if (p.units == 1)
-    launch_unit<T, DP, 1>(k, p, s);
-  else if (p.units == 2)
-    launch_unit<T, DP, 2>(k, p, s);
-  else if constexpr (DP <= 128)
-    launch_unit<T, DP, 4>(k, p, s);
+  if (p.wide) {
+    if (p.waves == 4) {
+      launch_wide<T, DP, 1, 4>(k, s);
+    } else if (p.units == 1) {
+      launch_wide<T, DP, 1, 8>(k, s);
+    } else if constexpr (DP <= 128) {
+      launch_wide<T, DP, 2, 8>(k, s);
+    }
+  } else if (p.units == 1) {
+    launch_unit<T, DP, 1>(k, s);
+  } else if constexpr (DP <= 128) {
+    launch_unit<T, DP, 2>(k, s);
+  }
 }
 
 template <typename T>
@@ -536,35 +871,47 @@ void launch_type(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
   else
     launch_dim<T, 256>(k, p, s);
   if (k.splits == 1) return;
-  const uint32_t ways = kWavesA / p.row_ways;
   const dim3 grid((k.a.batch * k.a.kv_heads * k.rows + kWavesA - 1) / kWavesA), block(256);
   if (D <= 64)
-    hipLaunchKernelGGL((k_tree_attention_join<T, 16>), grid, block, 0, s, k, ways);
+    hipLaunchKernelGGL((k_tree_attention_join<T, 16>), grid, block, 0, s, k, p.unit, p.ways);
   else if (D <= 128)
-    hipLaunchKernelGGL((k_tree_attention_join<T, 32>), grid, block, 0, s, k, ways);
+    hipLaunchKernelGGL((k_tree_attention_join<T, 32>), grid, block, 0, s, k, p.unit, p.ways);
   else
-    hipLaunchKernelGGL((k_tree_attention_join<T, 64>), grid, block, 0, s, k, ways);
+    hipLaunchKernelGGL((k_tree_attention_join<T, 64>), grid, block, 0, s, k, p.unit, p.ways);
 }
 
 }  // namespace
 
-// Rows: 16, 32 or 64 of them to a wave (64 rows of 128 values are 64 + 128
-// registers of Q and O a lane; of 256 values, 32 rows are), then 1, 2 or 4
-// waves of different rows, then tiles. Splits: enough workgroups to fill 256
-// compute units several times over, with at least a strip for every wave.
+// Up to 32 rows (16 for heads above 128): one wave holds them all, and the four
+// of a workgroup take different keys. More: waves hold different rows, 16 or
+// 32 each, 4 or 8 to a workgroup, then tiles. Splits: workgroups to fill 256
+// compute units, with a stage (or a strip for every wave) each at least.
 TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a) {
   TreeAttnPlan p;
   const uint32_t rows = a.nodes * (a.q_heads / a.kv_heads);
-  const uint32_t most = a.head_dim > 128 ? 2 : 4;
-  p.units = rows <= 16 ? 1 : rows <= 32 ? 2 : most;
-  const uint32_t waves = (rows + 16 * p.units - 1) / (16 * p.units);
-  p.row_ways = waves <= 1 ? 1 : waves <= 2 ? 2 : 4;
-  p.row_tiles = (waves + p.row_ways - 1) / p.row_ways;
-  const uint32_t ways = kWavesA / p.row_ways;
-  const uint64_t strips = ((uint64_t)a.max_pages * a.page_size + 31) / 32 + (a.nodes + 31) / 32;
+  const bool large = a.head_dim > 128;
+  uint64_t fill;
+  if (rows <= (large ? 16u : 32u)) {
+    p.wide = 0;
+    p.units = rows <= 16 ? 1 : 2;
+    p.waves = p.ways = 4;
+    p.unit = 32;
+    p.row_tiles = 1;
+    fill = 1024;
+  } else {
+    p.wide = 1;
+    p.units = large || rows <= 128 ? 1 : 2;
+    p.waves = rows <= 64 ? 4 : 8;
+    p.ways = 1;
+    p.unit = large ? 32 : 64;
+    const uint32_t tile = 16 * p.units * p.waves;
+    p.row_tiles = (rows + tile - 1) / tile;
+    fill = p.waves == 4 ? 512 : 256;
+  }
+  const uint64_t units = ((uint64_t)a.max_pages * a.page_size + p.unit - 1) / p.unit + (a.nodes + p.unit - 1) / p.unit;
   const uint64_t tiles = (uint64_t)a.batch * a.kv_heads * p.row_tiles;
-  uint64_t splits = (1024 + tiles - 1) / tiles;
-  const uint64_t cap = (strips + ways - 1) / ways;
+  uint64_t splits = (fill + tiles - 1) / tiles;
+  const uint64_t cap = (units + p.ways - 1) / p.ways;
   if (splits > cap) splits = cap;
   if (splits > 128) splits = 128;
   p.splits = splits < 1 ? 1 : (uint32_t)splits;

@@ -7,6 +7,7 @@ library has not been built, the first call raises -- there is no fallback.
 """
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libenc.so")
@@ -182,10 +183,22 @@ def _check(status):
         raise EncError(status, lib().enc_last_error().decode())
 
 
+_raw_stream = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            # the handle alone, where torch offers it: a Stream object costs as
+            # much as a kernel launch (2.6 us against 0.1 us)
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            if raw is not None:
+                _raw_stream = lambda: raw(torch.cuda.current_device())  # noqa: E731
+            else:
+                _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        return ctypes.c_void_p(_raw_stream())
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -571,65 +584,82 @@ def enc_stream_probe(src, dst, items_per_thread=1, threads_per_workgroup=256, st
 ENC_TREE_MAX_NODES = 256
 ENC_ROPE_ADJACENT, ENC_QK_NO_NORM = 1, 2
 _codes = {}
+# the argument structs in one go (field by field costs about 0.1 us each)
+_QK_PACK = struct.Struct("=22Q10IfI").pack
+_ATTN_PACK = struct.Struct("=27Q10IfI").pack
+_VERIFY_PACK = struct.Struct("=13Q4I").pack
 
 
-def _code(t, what):
-    """Header element type of a floating tensor."""
+def _code(dtype):
+    """Header element type of a floating torch type."""
     if not _codes:
         import torch
         _codes.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
-    code = _codes.get(t.dtype if hasattr(t, "dtype") else t)
+    code = _codes.get(dtype)
     if code is None:
-        raise TypeError("%s must be bfloat16, float16 or float32" % what)
+        raise TypeError("%s: values must be bfloat16, float16 or float32" % dtype)
     return code
+
+
+class _Here:
+    """Allocations for the current stream need no context."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_here = _Here()
 
 
 def _on(stream):
     """Context in which torch allocates for `stream`, so that memory of a
     tensor made in a call is not handed out again before the call's work."""
-    import contextlib
     if stream is None:
-        return contextlib.nullcontext()
+        return _here
     import torch
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
-def _plain(t, what, dtype, shape, device):
-    """A contiguous CUDA tensor of exactly this type and shape (None in the
-    shape: any size); returns its address."""
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor on %s" % (what, dtype, device))
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), tuple(shape)))
-    return t.data_ptr()
+def _plain(t, what, dtype, shape, index):
+    """Address of a contiguous tensor of exactly this type and shape (None: any
+    size of two axes) on CUDA device `index`."""
+    if (t.dtype is dtype and t.is_contiguous() and t.get_device() == index
+            and (t.shape == shape if shape is not None else t.dim() == 2)):
+        return t.data_ptr()
+    raise ValueError("%s must be a contiguous %s tensor of shape %s on CUDA device %d, got %s %s on %s"
+                     % (what, dtype, "[., .]" if shape is None else tuple(shape), index, t.dtype, tuple(t.shape), t.device))
 
 
-def _values(t, what, dtype, shape, device):
-    """A CUDA tensor of values with a contiguous last axis; returns its strides."""
-    if t.dtype != dtype or t.device != device:
-        raise ValueError("%s must be a %s tensor on %s" % (what, dtype, device))
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), tuple(shape)))
+def _values(t, what, dtype, shape, index):
+    """Strides of a tensor of values with a contiguous last axis."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape:
+        raise ValueError("%s must be a %s tensor of shape %s on CUDA device %d, got %s %s on %s"
+                         % (what, dtype, tuple(shape), index, t.dtype, tuple(t.shape), t.device))
     st = t.stride()
     if st[-1] != 1 and shape[-1] != 1:
         raise ValueError("%s: the last axis must be contiguous" % what)
     return st
 
 
-def _scratch(ws, device):
+def _scratch(ws, index):
     """Address and bytes of a workspace, which must lie on the same device."""
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError("the workspace must be a contiguous tensor on %s" % device)
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor on CUDA device %d" % index)
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _device_of(t):
+    """Index of the CUDA device a call works on: the current one, and its tensors'."""
     import torch
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError("expected CUDA tensors")
-    if t.device.index != torch.cuda.current_device():
+    if index != torch.cuda.current_device():
         raise ValueError("tensors are on %s, the current device is %d" % (t.device, torch.cuda.current_device()))
-    return t.device
+    return index
 
 
 def enc_qk_norm_rope(q, k, v, positions, table, q_weight=None, k_weight=None, eps=1e-6, adjacent=False, norm=True,
@@ -642,59 +672,52 @@ def enc_qk_norm_rope(q, k, v, positions, table, q_weight=None, k_weight=None, ep
     None; an out tensor may be its input. Returns (q, k, v)."""
     import torch
     device = _device_of(q)
-    tokens, q_heads, dim = q.shape
-    kv_heads = k.shape[1]
-    a = EncQkArgs()
-    qs = _values(q, "q", q.dtype, (tokens, q_heads, dim), device)
-    ks = _values(k, "k", q.dtype, (tokens, kv_heads, dim), device)
-    vs = _values(v, "v", q.dtype, (tokens, kv_heads, dim), device) if v is not None else (0, 0, 0)
+    tokens, q_heads, dim = shape = q.shape
+    kv_shape = (tokens, k.shape[1], dim)
+    qs = _values(q, "q", q.dtype, shape, device)
+    ks = _values(k, "k", q.dtype, kv_shape, device)
     if out is None:
         dtype = out_dtype or torch.bfloat16
         with _on(stream):
-            out = (torch.empty((tokens, q_heads, dim), dtype=dtype, device=device),
-                   torch.empty((tokens, kv_heads, dim), dtype=dtype, device=device),
-                   torch.empty((tokens, kv_heads, dim), dtype=dtype, device=device) if v is not None else None)
-    qo, ko, vo = out
-    qos = _values(qo, "q output", qo.dtype, (tokens, q_heads, dim), device)
-    kos = _values(ko, "k output", qo.dtype, (tokens, kv_heads, dim), device)
+            qo, ko = q.new_empty(shape, dtype=dtype), q.new_empty(kv_shape, dtype=dtype)
+            vo = q.new_empty(kv_shape, dtype=dtype) if v is not None else None
+    else:
+        qo, ko, vo = out
+    dtype = qo.dtype
+    qos = _values(qo, "q output", dtype, shape, device)
+    kos = _values(ko, "k output", dtype, kv_shape, device)
+    vs = vos = (0, 0)
+    vp = vop = 0
     if v is not None:
-        vos = _values(vo, "v output", qo.dtype, (tokens, kv_heads, dim), device)
-        a.d_v, a.d_v_out = v.data_ptr(), vo.data_ptr()
-        a.v_token, a.v_head, a.v_out_token, a.v_out_head = vs[0], vs[1], vos[0], vos[1]
-    a.d_q, a.d_k, a.d_q_out, a.d_k_out = q.data_ptr(), k.data_ptr(), qo.data_ptr(), ko.data_ptr()
-    a.w_dtype = FP32
-    for name, w in (("d_q_weight", q_weight), ("d_k_weight", k_weight)):
-        if w is not None:
-            setattr(a, name, _plain(w, name[2:], w.dtype, (dim,), device))
-            a.w_dtype = _code(w, "a weight")
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise TypeError("the weights must have one type")
+        vs, vos = _values(v, "v", q.dtype, kv_shape, device), _values(vo, "v output", dtype, kv_shape, device)
+        vp, vop = v.data_ptr(), vo.data_ptr()
+    qw = kw = tp = pp = max_pos = rot = 0
+    w_code = FP32
+    if q_weight is not None:
+        qw, w_code = _plain(q_weight, "q_weight", q_weight.dtype, (dim,), device), _code(q_weight.dtype)
+    if k_weight is not None:
+        kw, w_code = _plain(k_weight, "k_weight", k_weight.dtype, (dim,), device), _code(k_weight.dtype)
+        if q_weight is not None and q_weight.dtype is not k_weight.dtype:
+            raise TypeError("the weights must have one type")
     if table is not None:
-        a.d_positions = _plain(positions, "positions", torch.int32, (tokens,), device)
-        a.d_table = _plain(table, "table", torch.float32, (None, None), device)
-        a.max_pos, a.rot_dim = table.shape
-    a.q_token, a.q_head, a.k_token, a.k_head = qs[0], qs[1], ks[0], ks[1]
-    a.q_out_token, a.q_out_head, a.k_out_token, a.k_out_head = qos[0], qos[1], kos[0], kos[1]
-    a.tokens, a.q_heads, a.kv_heads, a.head_dim = tokens, q_heads, kv_heads, dim
-    a.in_dtype, a.out_dtype = _code(q, "q"), _code(qo, "the output")
-    a.flags = (ENC_ROPE_ADJACENT if adjacent else 0) | (0 if norm else ENC_QK_NO_NORM)
-    a.eps = eps
+        pp, tp = _plain(positions, "positions", torch.int32, (tokens,), device), _plain(table, "table", torch.float32, None,
+                                                                                        device)
+        max_pos, rot = table.shape
+    flags = (ENC_ROPE_ADJACENT if adjacent else 0) | (0 if norm else ENC_QK_NO_NORM)
+    a = EncQkArgs.from_buffer_copy(_QK_PACK(
+        q.data_ptr(), k.data_ptr(), vp, qo.data_ptr(), ko.data_ptr(), vop, qw, kw, pp, tp,
+        qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], qos[0], qos[1], kos[0], kos[1], vos[0], vos[1],
+        tokens, q_heads, kv_shape[1], dim, rot, max_pos, _code(q.dtype), _code(dtype), w_code, flags, eps, 0))
     _check(lib().enc_qk_norm_rope(ctypes.byref(a), _stream(stream)))
     return qo, ko, vo
 
 
-def _attention_sizes(q, k_new, table, k_cache):
-    a = EncTreeAttentionArgs()
-    a.batch, a.nodes, a.q_heads, a.head_dim = q.shape
-    a.kv_heads = k_new.shape[2]
-    a.dtype = _code(q, "q")
-    a.n_pages, a.page_size = k_cache.shape[0], k_cache.shape[1]
-    a.max_seqs, a.max_pages = table.shape
-    return a
-
-
 def enc_tree_attention_workspace_bytes(q, k_new, table, k_cache):
-    return int(lib().enc_tree_attention_workspace_bytes(ctypes.byref(_attention_sizes(q, k_new, table, k_cache))))
+    batch, nodes, q_heads, dim = q.shape
+    a = EncTreeAttentionArgs.from_buffer_copy(_ATTN_PACK(
+        *[0] * 27, batch, nodes, q_heads, k_new.shape[2], dim, _code(q.dtype), k_cache.shape[0], k_cache.shape[1],
+        table.shape[1], table.shape[0], 0.0, 0))
+    return int(lib().enc_tree_attention_workspace_bytes(ctypes.byref(a)))
 
 
 def tree_attention_workspace(q, k_new, table, k_cache):
@@ -714,39 +737,37 @@ def enc_tree_attention(q, k_new, v_new, k_cache, v_cache, table, lens, mask=None
     Returns (out, lse or None)."""
     import torch
     device = _device_of(q)
-    batch, n, q_heads, dim = q.shape
-    kv_heads = k_new.shape[2]
-    a = _attention_sizes(q, k_new, table, k_cache)
-    a.q_batch, a.q_node, a.q_head, _ = _values(q, "q", q.dtype, q.shape, device)
-    a.k_new_batch, a.k_new_node, a.k_new_head, _ = _values(k_new, "k_new", q.dtype, (batch, n, kv_heads, dim), device)
-    a.v_new_batch, a.v_new_node, a.v_new_head, _ = _values(v_new, "v_new", q.dtype, (batch, n, kv_heads, dim), device)
-    cs = _values(k_cache, "k_cache", q.dtype, (a.n_pages, a.page_size, kv_heads, dim), device)
-    if _values(v_cache, "v_cache", q.dtype, k_cache.shape, device) != cs:
+    dtype = q.dtype
+    batch, n, q_heads, dim = shape = q.shape
+    pages, page, kv_heads = k_cache.shape[:3]
+    new_shape = (batch, n, kv_heads, dim)
+    qs = _values(q, "q", dtype, shape, device)
+    ks = _values(k_new, "k_new", dtype, new_shape, device)
+    vs = _values(v_new, "v_new", dtype, new_shape, device)
+    cs = _values(k_cache, "k_cache", dtype, (pages, page, kv_heads, dim), device)
+    if _values(v_cache, "v_cache", dtype, k_cache.shape, device) != cs:
         raise ValueError("k_cache and v_cache must have the same strides")
-    a.cache_page, a.cache_token, a.cache_head, _ = cs
-    a.d_q, a.d_k_new, a.d_v_new = q.data_ptr(), k_new.data_ptr(), v_new.data_ptr()
-    a.d_k_cache, a.d_v_cache = k_cache.data_ptr(), v_cache.data_ptr()
-    a.d_table = _plain(table, "table", torch.int32, (None, None), device)
-    a.d_lens = _plain(lens, "lens", torch.int32, (a.max_seqs,), device)
-    if mask is not None:
-        a.d_mask = _plain(mask, "mask", torch.int64, (batch, n, (n + 63) // 64), device)
-    if seqs is not None:
-        a.d_seqs = _plain(seqs, "seqs", torch.int32, (batch,), device)
-    if nodes is not None:
-        a.d_nodes = _plain(nodes, "nodes", torch.int32, (batch,), device)
+    tp = _plain(table, "table", torch.int32, None, device)
+    max_seqs, max_pages = table.shape
+    lp = _plain(lens, "lens", torch.int32, (max_seqs,), device)
+    mp = _plain(mask, "mask", torch.int64, (batch, n, (n + 63) // 64), device) if mask is not None else 0
+    sp = _plain(seqs, "seqs", torch.int32, (batch,), device) if seqs is not None else 0
+    np_ = _plain(nodes, "nodes", torch.int32, (batch,), device) if nodes is not None else 0
     lse = None
-    if out is None or return_lse or ws is None:
-        with _on(stream):
-            if out is None:
-                out = torch.empty((batch, n, q_heads, dim), dtype=q.dtype, device=device)
-            if return_lse:
-                lse = torch.empty((batch, n, q_heads), dtype=torch.float32, device=device)
-                a.d_lse = lse.data_ptr()
-            if ws is None:
-                ws = _empty_u8(lib().enc_tree_attention_workspace_bytes(ctypes.byref(a)), device)
-    a.out_batch, a.out_node, a.out_head, _ = _values(out, "out", q.dtype, q.shape, device)
-    a.d_out = out.data_ptr()
-    a.scale = dim ** -0.5 if scale is None else scale
+    with _on(stream):
+        if out is None:
+            out = q.new_empty(shape)
+        if return_lse:
+            lse = q.new_empty((batch, n, q_heads), dtype=torch.float32)
+        if ws is None:
+            ws = tree_attention_workspace(q, k_new, table, k_cache)
+    os = _values(out, "out", dtype, shape, device)
+    a = EncTreeAttentionArgs.from_buffer_copy(_ATTN_PACK(
+        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
+        lse.data_ptr() if lse is not None else 0, tp, lp, sp, np_, mp,
+        qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], cs[0], cs[1], cs[2], os[0], os[1], os[2],
+        batch, n, q_heads, kv_heads, dim, _code(dtype), pages, page, max_pages, max_seqs,
+        dim ** -0.5 if scale is None else scale, 0))
     _check(lib().enc_tree_attention(ctypes.byref(a), *_scratch(ws, device), _stream(stream)))
     return out, lse
 
@@ -771,27 +792,25 @@ def enc_verify_tree(parents, tokens, target, draft, u, nodes=None, ws=None, stre
     u[:, 0] draws the next token. Returns (path, count, token), int32."""
     import torch
     device = _device_of(tokens)
-    batch, n = tokens.shape
+    batch, n = shape = tokens.shape
     vocab = target.shape[2]
-    a = EncVerifyArgs()
-    a.d_parents = _plain(parents, "parents", torch.int32, (batch, n), device)
-    a.d_tokens = _plain(tokens, "tokens", torch.int32, (batch, n), device)
-    a.d_u = _plain(u, "u", torch.float32, (batch, n), device)
-    a.target_batch, a.target_node, _ = _values(target, "target", target.dtype, (batch, n, vocab), device)
-    a.d_target = target.data_ptr()
+    dtype = target.dtype
+    pp = _plain(parents, "parents", torch.int32, shape, device)
+    xp = _plain(tokens, "tokens", torch.int32, shape, device)
+    up = _plain(u, "u", torch.float32, shape, device)
+    ts = _values(target, "target", dtype, (batch, n, vocab), device)
+    ds, dp = (0, 0), 0
     if draft is not None:
-        a.draft_batch, a.draft_node, _ = _values(draft, "draft", target.dtype, (batch, n, vocab), device)
-        a.d_draft = draft.data_ptr()
-    if nodes is not None:
-        a.d_nodes = _plain(nodes, "nodes", torch.int32, (batch,), device)
+        ds, dp = _values(draft, "draft", dtype, (batch, n, vocab), device), draft.data_ptr()
+    np_ = _plain(nodes, "nodes", torch.int32, (batch,), device) if nodes is not None else 0
     with _on(stream):
-        path = torch.empty((batch, n), dtype=torch.int32, device=device)
-        count = torch.empty((batch,), dtype=torch.int32, device=device)
-        token = torch.empty((batch,), dtype=torch.int32, device=device)
+        path = tokens.new_empty(shape)
+        count, token = tokens.new_empty(batch), tokens.new_empty(batch)
         if ws is None:
             ws = verify_tree_workspace(tokens, target)
-    a.d_path, a.d_count, a.d_token = path.data_ptr(), count.data_ptr(), token.data_ptr()
-    a.batch, a.nodes, a.vocab, a.dtype = batch, n, vocab, _code(target, "target")
+    a = EncVerifyArgs.from_buffer_copy(_VERIFY_PACK(
+        pp, xp, target.data_ptr(), dp, up, np_, path.data_ptr(), count.data_ptr(), token.data_ptr(),
+        ts[0], ts[1], ds[0], ds[1], batch, n, vocab, _code(dtype)))
     _check(lib().enc_verify_tree(ctypes.byref(a), *_scratch(ws, device), _stream(stream)))
     return path, count, token
 
@@ -814,15 +833,16 @@ class Cache:
         size = data.element_size()
         c = EncCache()
         c.d_data = data.data_ptr()
-        c.d_table = _plain(table, "table", torch.int32, (None, None), device)
+        c.d_table = _plain(table, "table", torch.int32, None, device)
         c.d_lens = _plain(lens, "lens", torch.int32, (table.shape[0],), device)
         c.d_refs = _plain(refs, "refs", torch.int32, (pages,), device)
         c.plane_stride = st[0] * size
         c.n_planes, c.n_pages, c.page_size, c.row_bytes = planes, pages, page, row * size
         c.max_seqs, c.max_pages = table.shape
         self.c, self.data, self.table, self.lens, self.refs = c, data, table, lens, refs
-        self.row_shape = data.shape[3:]
-        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.row_shape, self.planes = tuple(data.shape[3:]), planes
+        self.status = torch.zeros(1, dtype=torch.int32, device=data.device)
+        self.ref = ctypes.byref(c)
 
     @classmethod
     def empty(cls, planes, n_pages, page_size, row_shape, max_seqs, max_pages, dtype=None, device="cuda"):
@@ -850,20 +870,20 @@ def enc_cache_commit(cache, seqs, draft, path, count, ws=None, stream=None):
     why nothing was changed)."""
     import torch
     device = _device_of(cache.data)
-    batch, nodes = path.shape
-    if draft.dtype != cache.data.dtype or draft.device != device:
+    batch, nodes = shape = path.shape
+    if draft.dtype is not cache.data.dtype or draft.get_device() != device:
         raise ValueError("draft must have the cache's type and device")
-    if draft.shape != (cache.c.n_planes, batch, nodes) + tuple(cache.row_shape):
+    if draft.shape != (cache.planes, batch, nodes) + cache.row_shape:
         raise ValueError("draft has shape %s" % (tuple(draft.shape),))
-    if batch and not draft[0, 0].is_contiguous():
+    if not draft.is_contiguous() and batch and not draft[0, 0].is_contiguous():
         raise ValueError("a sequence's draft rows must be contiguous")
     st, size = draft.stride(), draft.element_size()
     if ws is None:
         with _on(stream):
             ws = cache_workspace(cache, path)
     _check(lib().enc_cache_commit(
-        ctypes.byref(cache.c), _plain(seqs, "seqs", torch.int32, (batch,), device), batch, draft.data_ptr(),
-        st[0] * size, st[1] * size, _plain(path, "path", torch.int32, (batch, nodes), device),
+        cache.ref, _plain(seqs, "seqs", torch.int32, (batch,), device), batch, draft.data_ptr(),
+        st[0] * size, st[1] * size, _plain(path, "path", torch.int32, shape, device),
         _plain(count, "count", torch.int32, (batch,), device), nodes, cache.status.data_ptr(),
         *_scratch(ws, device), _stream(stream)))
     return cache.status
@@ -874,7 +894,7 @@ def enc_cache_fork(cache, src, dst, stream=None):
     import torch
     device = _device_of(cache.data)
     _check(lib().enc_cache_fork(
-        ctypes.byref(cache.c), _plain(src, "src", torch.int32, (None,), device),
+        cache.ref, _plain(src, "src", torch.int32, (src.numel(),), device),
         _plain(dst, "dst", torch.int32, src.shape, device), src.shape[0], _stream(stream)))
 
 
@@ -883,7 +903,7 @@ def enc_cache_truncate(cache, seqs, lens, stream=None):
     import torch
     device = _device_of(cache.data)
     _check(lib().enc_cache_truncate(
-        ctypes.byref(cache.c), _plain(seqs, "seqs", torch.int32, (None,), device),
+        cache.ref, _plain(seqs, "seqs", torch.int32, (seqs.numel(),), device),
         _plain(lens, "lens", torch.int32, seqs.shape, device), seqs.shape[0], _stream(stream)))
 
 
