@@ -81,12 +81,6 @@ __device__ __forceinline__ float rows_sum(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Strips a workgroup takes: an equal share, whole rounds of its key ways.
-__device__ __forceinline__ uint32_t split_chunk(uint32_t strips, uint32_t splits, uint32_t ways) {
-  const uint32_t c = (strips + splits - 1) / splits;
-  return max((c + ways - 1) / ways * ways, ways);
-}
-
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ uint2 read_transposed(const void *lds) {
   typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
@@ -94,7 +88,7 @@ __device__ __forceinline__ uint2 read_transposed(const void *lds) {
 }
 
 struct Seq {
-  uint32_t len, live, strips_ctx, strips;
+  uint32_t len, live;
   const int32_t *table;
 };
 
@@ -108,18 +102,88 @@ __device__ __forceinline__ Seq sequence_of(const enc_tree_attention_args &a, uin
   q.table = a.d_table + (uint64_t)(s < a.max_seqs ? s : 0) * a.max_pages;
   int32_t live = a.d_nodes ? a.d_nodes[b] : (int32_t)a.nodes;
   q.live = (uint32_t)max(0, min(live, (int32_t)a.nodes));
-  q.strips_ctx = (q.len + 31) / 32;
-  q.strips = q.strips_ctx + (q.live + 31) / 32;
   return q;
 }
 
+// The work of a call in units of `unit` keys (a history's units, then its
+// tree's), cut into parts of the same number of units over all sequences: a
+// short sequence has one part, a long one many. Which part is whose follows
+// from the lengths, which only the device knows: a wave adds up the units of
+// all sequences, 64 at a time, and derives the part size, then finds its part
+// (or its sequence's parts) in the running number of parts.
+struct Share {
+  uint32_t b;              // sequence
+  uint32_t first, parts;   // its first part's number, and how many it has
+  uint32_t size;           // units in a part
+  bool found;
+};
+
+__device__ __forceinline__ uint32_t units_of(const enc_tree_attention_args &a, uint32_t b, uint32_t unit) {
+  if (b >= a.batch) return 0;
+  const Seq q = sequence_of(a, b);
+  return (q.len + unit - 1) / unit + (q.live + unit - 1) / unit;
+}
+
+// BY_PART: of part `index`; else of sequence `index`.
+template <bool BY_PART>
+__device__ __forceinline__ Share share_of(const TreeAttnArgs &k, uint32_t unit, uint32_t ways, uint32_t index) {
+  const enc_tree_attention_args &a = k.a;
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t mine = units_of(a, lane, unit);
+  uint64_t total = 0;
+  for (uint32_t b0 = 0; b0 < a.batch; b0 += 64) {
+    uint64_t u = b0 ? units_of(a, b0 + lane, unit) : mine;
+    for (uint32_t o = 32; o; o >>= 1) u += __shfl_xor(u, o);
+    total += u;
+  }
+  const uint64_t each = (total + k.parts - 1) / k.parts;
+  Share s;
+  s.size = max((uint32_t)((each + ways - 1) / ways * ways), ways);
+  s.found = false;
+  s.b = s.first = s.parts = 0;
+  uint32_t before = 0;
+  for (uint32_t b0 = 0; b0 < a.batch; b0 += 64) {
+    const uint32_t u = b0 ? units_of(a, b0 + lane, unit) : mine;
+    const uint32_t n = b0 + lane < a.batch ? max((u + s.size - 1) / s.size, 1u) : 0;
+    uint32_t incl = n;
+    for (uint32_t o = 1; o < 64; o <<= 1) {
+      const uint32_t t = __shfl_up(incl, o);
+      if (lane >= o) incl += t;
+    }
+    const uint32_t from = before + incl - n;
+    const uint64_t hit = BY_PART ? __ballot(n && index >= from && index < from + n)
+                                 : __ballot(b0 + lane == index);
+    if (hit) {
+      const int at = __builtin_ctzll(hit);
+      s.b = b0 + at;
+      s.first = __builtin_amdgcn_readlane(from, at);
+      s.parts = __builtin_amdgcn_readlane(n, at);
+      s.found = true;
+      return s;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return s;
+}
+
+// The kernel's arguments, read again where they are used: kept in scalar
+// registers from the start, those of the first and last steps push the main
+// loop's own into spills (a vector instruction for each use).
+typedef const __attribute__((address_space(4))) TreeAttnArgs *ArgsPtr;
+__device__ __forceinline__ ArgsPtr args_again() {
+  ArgsPtr p = (ArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
+}
+
 // Bit j: node i of tree b may see node first + j.
-__device__ __forceinline__ uint32_t tree_bits(const enc_tree_attention_args &a, const TreeAttnArgs &k, uint32_t b,
-                                              uint32_t i, uint32_t first, uint32_t live) {
+__device__ __forceinline__ uint32_t tree_bits(uint32_t b, uint32_t i, uint32_t first, uint32_t live) {
   if (first >= live) return 0;
   uint32_t bits = live - first < 32 ? (1u << (live - first)) - 1u : 0xFFFFFFFFu;
-  if (a.d_mask)
-    bits &= reinterpret_cast<const uint32_t *>(a.d_mask)[((uint64_t)b * a.nodes + i) * k.mask_words + first / 32];
+  const ArgsPtr k = args_again();
+  const uint32_t *mask = reinterpret_cast<const uint32_t *>(k->a.d_mask);
+  if (mask)
+    bits &= mask[((uint64_t)b * k->a.nodes + i) * k->mask_words + first / 32];
   else
     bits &= i >= first + 31 ? 0xFFFFFFFFu : i < first ? 0u : (2u << (i - first)) - 1u;
   return bits;
@@ -140,14 +204,16 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
   const uint32_t l16 = lane & 15, g4 = lane >> 4;
   const uint32_t D = a.head_dim;
 
-  const uint32_t grp = blockIdx.x;
-  const uint32_t bs = grp / a.kv_heads, h = (grp + bs) % a.kv_heads, split = bs % k.splits, b = bs / k.splits;
-  const Seq q = sequence_of(a, b);
+  // neighbouring workgroups (on different dies) differ in their head, and each
+  // die sees all heads
+  const uint32_t part = blockIdx.x / a.kv_heads, h = (blockIdx.x + part) % a.kv_heads;
   constexpr uint32_t ways = kWavesA;
-  const uint32_t kw = wave;
-  const uint32_t chunk = split_chunk(q.strips, k.splits, ways);
-  const uint32_t lo = split * chunk, hi = min(lo + chunk, q.strips);
-  if (lo >= q.strips && k.splits > 1) return;   // nothing for this split; the join does not look for it
+  const Share sh = share_of<true>(k, 32, ways, part);
+  if (!sh.found) return;
+  const uint32_t b = sh.b, kw = wave;
+  const Seq q = sequence_of(a, b);
+  const uint32_t strips_ctx = (q.len + 31) / 32, strips = strips_ctx + (q.live + 31) / 32;
+  const uint32_t lo = (part - sh.first) * sh.size, hi = min(lo + sh.size, strips);
 
   // ---- Q fragments: query row l % 16 of each unit, 8 values per k step
   const uint32_t row0 = l16;
@@ -195,21 +261,21 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
   // Offsets, in 16-byte units, of the rows of key lane % 32 of a strip; keys
   // past the end stand for the last one.
   auto entry_of = [&](uint32_t strip) -> int32_t {
-    if (strip >= q.strips_ctx) return 0;
+    if (strip >= strips_ctx) return 0;
     return q.table[k.page.quot(min(strip * 32 + (lane & 31), q.len - 1))];
   };
   auto offsets_of = [&](uint32_t strip, int32_t e, uint32_t &ko, uint32_t &vo) {
-    if (strip < q.strips_ctx) {
+    if (strip < strips_ctx) {
       const uint32_t key = min(strip * 32 + (lane & 31), q.len - 1), page = min((uint32_t)max(e, 0), a.n_pages - 1);
       ko = vo = page * page_units + (key - k.page.quot(key) * k.page.d) * token_units;
     } else {
-      const uint32_t key = min((strip - q.strips_ctx) * 32 + (lane & 31), q.live - 1);
+      const uint32_t key = min((strip - strips_ctx) * 32 + (lane & 31), q.live - 1);
       ko = key * (uint32_t)(a.k_new_node / 8);
       vo = key * (uint32_t)(a.v_new_node / 8);
     }
   };
   auto load_k = [&](uint32_t strip, uint32_t off) {
-    const uint4 *base = strip < q.strips_ctx ? kc : reinterpret_cast<const uint4 *>(kn);
+    const uint4 *base = strip < strips_ctx ? kc : reinterpret_cast<const uint4 *>(kn);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const uint4 *p = base + (uint32_t)__shfl((int)off, 16 * t + l16);
@@ -226,7 +292,7 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
     }
   };
   auto load_v = [&](uint32_t strip, uint32_t off) {
-    const uint4 *base = strip < q.strips_ctx ? vc : reinterpret_cast<const uint4 *>(vn);
+    const uint4 *base = strip < strips_ctx ? vc : reinterpret_cast<const uint4 *>(vn);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint4 *p = base + (uint32_t)__shfl((int)off, 16 * (j >> 2) + 4 * g4 + (j & 3));
@@ -266,15 +332,15 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
       }
     after_k();
 
-    const bool tree = SPECIAL && strip >= q.strips_ctx;
-    const uint32_t first = (tree ? strip - q.strips_ctx : strip) * 32;
+    const bool tree = SPECIAL && strip >= strips_ctx;
+    const uint32_t first = (tree ? strip - strips_ctx : strip) * 32;
     const uint32_t valid = SPECIAL ? min((tree ? q.live : q.len) - first, 32u) : 32;
     uint32_t seen[U];
     if constexpr (SPECIAL) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         uint32_t bits = valid < 32 ? (1u << valid) - 1u : 0xFFFFFFFFu;
-        if (tree) bits = alive[u] ? tree_bits(a, k, b, node[u], first, q.live) : 0u;
+        if (tree) bits = alive[u] ? tree_bits(b, node[u], first, q.live) : 0u;
         seen[u] = bits;
       }
 #pragma unroll
@@ -376,11 +442,11 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
   // that do not see them: add them to the rows that do.
   if (__any(strange)) {
     for (strip = lo + kw; strip < hi; strip += ways) {
-      if (strip < q.strips_ctx) continue;
-      const uint32_t first = (strip - q.strips_ctx) * 32;
+      if (strip < strips_ctx) continue;
+      const uint32_t first = (strip - strips_ctx) * 32;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const uint32_t seen = alive[u] ? tree_bits(a, k, b, node[u], first, q.live) : 0u;
+        const uint32_t seen = alive[u] ? tree_bits(b, node[u], first, q.live) : 0u;
         for (uint32_t key = 0; key < 32 && first + key < q.live; ++key) {
           const T *row = vn + (uint64_t)(first + key) * a.v_new_node;
           if (!(seen >> key & 1u)) continue;
@@ -441,14 +507,16 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
     __syncthreads();
   }
   if (kw != 0) return;
+  const ArgsPtr g = args_again();
+  const uint32_t group = g->group.d;
 
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const uint32_t r = row0 + 16 * u;
-    if (r >= k.rows) continue;
-    if (k.splits == 1) {
-      const uint32_t head = h * k.group.d + (r - node[u] * k.group.d);
-      T *dst = static_cast<T *>(a.d_out) + b * a.out_batch + node[u] * a.out_node + head * a.out_head;
+    if (r >= g->rows) continue;
+    if (sh.parts == 1) {
+      const uint32_t head = h * group + (r - node[u] * group);
+      T *dst = static_cast<T *>(g->a.d_out) + b * g->a.out_batch + node[u] * g->a.out_node + head * g->a.out_head;
       const bool any = alive[u] && l[u] != 0.f;
       const float inv = any ? 1.0f / l[u] : 0.f;
 #pragma unroll
@@ -466,16 +534,16 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
           else
             *reinterpret_cast<uint2 *>(dst + d) = make_uint2(w[0], w[1]);
         }
-      if (a.d_lse && g4 == 0)
-        a.d_lse[((uint64_t)b * a.nodes + node[u]) * a.q_heads + head] =
+      if (g->a.d_lse && g4 == 0)
+        g->a.d_lse[((uint64_t)b * g->a.nodes + node[u]) * g->a.q_heads + head] =
             any ? m[u] + __log2f(l[u]) * kLn2 : -__builtin_inff();
     } else {
-      const uint64_t at = (((uint64_t)b * a.kv_heads + h) * k.splits + split) * k.rows + r;
+      const uint64_t at = ((uint64_t)part * g->a.kv_heads + h) * g->rows + r;
       if (g4 == 0) {
-        k.part_ml[2 * at] = m[u];
-        k.part_ml[2 * at + 1] = l[u];
+        g->part_ml[2 * at] = m[u];
+        g->part_ml[2 * at + 1] = l[u];
       }
-      float *dst = k.part + at * D;
+      float *dst = g->part + at * D;
 #pragma unroll
       for (int n = 0; n < NH; ++n)
 #pragma unroll
@@ -506,6 +574,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
   constexpr int KS = DP / 32, NF = DP / 16, NCH = DP / 8;
   constexpr int SK = DP == 256 ? 32 : 64;
   constexpr int NT = 64 * W, NR = SK * NCH / NT;   // chunks of K (and of V) a thread brings in
+  constexpr bool EARLY_V = DP <= 128;              // registers for all of a strip's V fragments
   constexpr int PITCH = NCH + 1;                   // 16-byte chunks from row to row
   const enc_tree_attention_args &a = k.a;
   __shared__ __align__(16) uint4 ks[2][SK * PITCH], vs[2][SK * PITCH];
@@ -514,18 +583,17 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const uint32_t l16 = lane & 15, g4 = lane >> 4;
   const uint32_t D = a.head_dim;
-  // workgroups of one (sequence, split, head) differ in 8, so they meet in one
-  // compute die's L2 (workgroups go to the 8 dies in turn)
-  const uint32_t groups = a.batch * k.splits * a.kv_heads;
+  // row tiles of one (part, head) differ in 8, so they meet in one compute die's
+  // L2 (workgroups go to the 8 dies in turn)
   const uint32_t id8 = blockIdx.x >> 3;
   const uint32_t grp = id8 / k.row_tiles * 8 + (blockIdx.x & 7), rt = id8 % k.row_tiles;
-  if (grp >= groups) return;
-  const uint32_t bs = grp / a.kv_heads, h = (grp + bs) % a.kv_heads, split = bs % k.splits, b = bs / k.splits;
+  const uint32_t part = grp / a.kv_heads, h = (grp + part) % a.kv_heads;
+  const Share sh = share_of<true>(k, SK, 1, part);
+  if (!sh.found) return;
+  const uint32_t b = sh.b;
   const Seq q = sequence_of(a, b);
   const uint32_t ctx = (q.len + SK - 1) / SK, stages = ctx + (q.live + SK - 1) / SK;
-  const uint32_t chunk = split_chunk(stages, k.splits, 1);
-  const uint32_t lo = split * chunk, hi = min(lo + chunk, stages);
-  if (lo >= stages && k.splits > 1) return;
+  const uint32_t lo = (part - sh.first) * sh.size, hi = min(lo + sh.size, stages);
 
   const uint32_t row0 = (rt * W + wave) * (U * 16) + l16;
   const bool busy = (rt * W + wave) * (U * 16) < k.rows;   // this wave has rows
@@ -560,25 +628,53 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
 #pragma unroll
     for (int f = 0; f < NF; ++f) o[u][f] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  bool far = false;   // some row's maximum times log2(e) leaves fp32
+  uint32_t far = 0;   // some row's maximum times log2(e) leaves fp32 (the same in all lanes)
 
-  // ---- bringing a stage in: thread's chunk i is chunk ch of row r0 + i rstep
+  // ---- bringing a stage in: thread's chunk i is chunk ch of row r0 + i kRowStep
   const uint32_t ch = tid % NCH, r0 = tid / NCH;
-  constexpr uint32_t kRowStep = NT / NCH;
+  constexpr uint32_t kRowStep = NT / NCH, kWaveRows = 64 / NCH;
   const bool chunk_live = ch * 8 < D;
-  const uint4 *kc = static_cast<const uint4 *>(a.d_k_cache) + h * (a.cache_head / 8) + ch;
-  const uint4 *vc = static_cast<const uint4 *>(a.d_v_cache) + h * (a.cache_head / 8) + ch;
-  const T *kn = static_cast<const T *>(a.d_k_new) + b * a.k_new_batch + h * a.k_new_head;
-  const T *vn = static_cast<const T *>(a.d_v_new) + b * a.v_new_batch + h * a.v_new_head;
-  const uint32_t page_units = (uint32_t)(a.cache_page / 8), token_units = (uint32_t)(a.cache_token / 8);
+  const T *kc = static_cast<const T *>(a.d_k_cache) + h * a.cache_head;
+  const T *vc = static_cast<const T *>(a.d_v_cache) + h * a.cache_head;
+  // Where a page holds whole groups of the rows that a wave loads at once, the
+  // page, its table entry and its address are the wave's: scalar work, and a
+  // constant offset for each lane. Otherwise, and for a last stage that is not
+  // full, each lane finds its own row.
+  const bool by_wave = k.page.d % kWaveRows == 0 && a.cache_token * kWaveRows < (1u << 30);
+  const uint32_t wave_row = __builtin_amdgcn_readfirstlane(r0);
+  const uint32_t lane_off = (uint32_t)(r0 - wave_row) * (uint32_t)a.cache_token + ch * 8;
+  typedef const __attribute__((address_space(4))) int32_t *const_ptr;   // read through the scalar cache
+  const const_ptr table = (const_ptr)(uintptr_t)q.table;
   uint4 kr[NR], vr[NR];
-  int32_t entry[NR];
-  auto find = [&](uint32_t st) {
-    if (st >= ctx) return;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) entry[i] = q.table[k.page.quot(min(st * SK + r0 + i * kRowStep, q.len - 1))];
+  for (int i = 0; i < NR; ++i) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+  int32_t entry[NR];
+  auto whole = [&](uint32_t st) { return st < ctx && (st + 1) * SK <= q.len; };
+  auto find = [&](uint32_t st) {
+    if (by_wave && whole(st)) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+        entry[i] = table[__builtin_amdgcn_readfirstlane(k.page.quot(st * SK + wave_row + i * kRowStep))];
+    } else if (st < ctx) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i) entry[i] = q.table[k.page.quot(min(st * SK + r0 + i * kRowStep, q.len - 1))];
+    }
   };
   auto fetch = [&](uint32_t st) {
+    if (by_wave && whole(st)) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const uint32_t key = st * SK + wave_row + i * kRowStep;
+        const uint32_t page = __builtin_amdgcn_readfirstlane(min((uint32_t)max(entry[i], 0), a.n_pages - 1));
+        const uint32_t in = __builtin_amdgcn_readfirstlane(key - k.page.quot(key) * k.page.d);
+        const uint64_t at = page * a.cache_page + in * a.cache_token;
+        if (chunk_live) {
+          kr[i] = *reinterpret_cast<const uint4 *>(kc + at + lane_off);
+          vr[i] = *reinterpret_cast<const uint4 *>(vc + at + lane_off);
+        }
+      }
+      return;
+    }
     const bool tree = st >= ctx;
     const uint32_t first = (tree ? st - ctx : st) * SK, end = tree ? q.live : q.len;
 #pragma unroll
@@ -587,13 +683,16 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
       kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
       if (key < end && chunk_live) {
         if (tree) {
-          kr[i] = *(reinterpret_cast<const uint4 *>(kn + key * a.k_new_node) + ch);
-          vr[i] = *(reinterpret_cast<const uint4 *>(vn + key * a.v_new_node) + ch);
+          const ArgsPtr g = args_again();
+          const T *kn = static_cast<const T *>(g->a.d_k_new) + b * g->a.k_new_batch + h * g->a.k_new_head;
+          const T *vn = static_cast<const T *>(g->a.d_v_new) + b * g->a.v_new_batch + h * g->a.v_new_head;
+          kr[i] = *reinterpret_cast<const uint4 *>(kn + key * g->a.k_new_node + ch * 8);
+          vr[i] = *reinterpret_cast<const uint4 *>(vn + key * g->a.v_new_node + ch * 8);
         } else {
           const uint32_t page = min((uint32_t)max(entry[i], 0), a.n_pages - 1);
-          const uint32_t at = page * page_units + (key - k.page.quot(key) * k.page.d) * token_units;
-          kr[i] = kc[at];
-          vr[i] = vc[at];
+          const uint64_t at = page * a.cache_page + (key - k.page.quot(key) * k.page.d) * a.cache_token + ch * 8;
+          kr[i] = *reinterpret_cast<const uint4 *>(kc + at);
+          vr[i] = *reinterpret_cast<const uint4 *>(vc + at);
         }
       }
     }
@@ -625,23 +724,43 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
   // ---- one strip of 32 keys of a stage
   auto compute = [&](auto special_, uint32_t st, uint32_t half, uint32_t buf) {
     constexpr bool SPECIAL = decltype(special_)::value;
+    // LDS reads in two batches, each on its way while something else runs: K,
+    // then V behind the products with K
+    uint4 kf[2][KS];
+    {
+      const uint4 *row = ks[buf] + (half * 32 + l16) * PITCH + g4;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < KS; ++e) kf[t][e] = row[16 * t * PITCH + 4 * e];
+    }
+    const char *vb = reinterpret_cast<const char *>(vs[buf] + (half * 32 + 4 * g4 + (l16 >> 2)) * PITCH) + (l16 & 3) * 8;
     float p[U][8];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const uint4 *row = ks[buf] + (half * 32 + 16 * t + l16) * PITCH + g4;
       f32x4 s[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < KS; ++e) {
-        const uint4 kf = row[4 * e];
 #pragma unroll
-        for (int u = 0; u < U; ++u) s[u] = Half<T>::mfma(kf, qf[u][e], s[u]);
+        for (int u = 0; u < U; ++u) s[u] = Half<T>::mfma(kf[t][e], qf[u][e], s[u]);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[u][4 * t + e] = s[u][e];
+    }
+
+    uint4 vf[NF];
+    if constexpr (EARLY_V) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const uint2 v0 = read_transposed(vb + 32 * f), v1 = read_transposed(vb + 16 * PITCH * 16 + 32 * f);
+        vf[f] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
 
     const bool tree = SPECIAL && st >= ctx;
@@ -651,11 +770,13 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         uint32_t bits = end >= first + 32 ? 0xFFFFFFFFu : end <= first ? 0u : (1u << (end - first)) - 1u;
-        if (tree) bits = alive[u] ? tree_bits(a, k, b, node[u], first, q.live) : 0u;
+        if (tree) bits = alive[u] ? tree_bits(b, node[u], first, q.live) : 0u;
         seen[u] = bits;
       }
     }
     uint4 pf[U];
+    float top[U];
+    bool grown = false;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if constexpr (SPECIAL) {
@@ -663,37 +784,51 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
         for (int j = 0; j < 8; ++j)
           if (!(seen[u] >> (16 * (j >> 2) + 4 * g4 + (j & 3)) & 1u)) p[u][j] = -__builtin_inff();
       }
-      float top = p[u][0];
+      float t = p[u][0];
 #pragma unroll
-      for (int j = 1; j < 8; ++j) top = fmaxf(top, p[u][j]);
-      top = rows_max(top) * scale;
-      if (__any(top > m[u] + (kSlack + Half<T>::kLift))) {
-        const float up = fmaxf(top - Half<T>::kLift, m[u]), shrink = exp_of(m[u] - up);
+      for (int j = 1; j < 8; ++j) t = fmaxf(t, p[u][j]);
+      top[u] = rows_max(t) * scale;
+      grown = grown || top[u] > m[u] + (kSlack + Half<T>::kLift);
+    }
+    if (__any(grown)) {
+      uint32_t out = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float up = fmaxf(top[u] - Half<T>::kLift, m[u]), shrink = exp_of(m[u] - up);
         m[u] = up;
         mc[u] = fmaxf(up * kLog2e, kLowest);   // a row that has seen nothing keeps a finite one
-        far = far || __any(!(fabsf(up) < 1e38f) && up != kLowest);
+        out |= !(fabsf(up) < 1e38f) && up != kLowest;
         l[u] *= shrink;
 #pragma unroll
         for (int f = 0; f < NF; ++f) o[u][f] *= shrink;
       }
-      if (far) {
+      far |= (uint32_t)(__ballot(out) != 0);
+    }
+    if (far) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[u][j] = exp_of(fmaf(p[u][j], scale, -m[u]));
-      } else {
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[u][j] = __builtin_amdgcn_exp2f(fmaf(p[u][j], c2, -mc[u]));
-      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
       l[u] += ((p[u][0] + p[u][1]) + (p[u][2] + p[u][3])) + ((p[u][4] + p[u][5]) + (p[u][6] + p[u][7]));
       pf[u] = make_uint4(pack2<T>(p[u][0], p[u][1]), pack2<T>(p[u][2], p[u][3]), pack2<T>(p[u][4], p[u][5]),
                          pack2<T>(p[u][6], p[u][7]));
     }
-    const char *vb = reinterpret_cast<const char *>(vs[buf] + (half * 32 + 4 * g4 + (l16 >> 2)) * PITCH) + (l16 & 3) * 8;
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
-      const uint2 v0 = read_transposed(vb + 32 * f), v1 = read_transposed(vb + 16 * PITCH * 16 + 32 * f);
-      const uint4 vf = make_uint4(v0.x, v0.y, v1.x, v1.y);
+      if constexpr (!EARLY_V) {
+        const uint2 v0 = read_transposed(vb + 32 * f), v1 = read_transposed(vb + 16 * PITCH * 16 + 32 * f);
+        vf[f] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+      }
 #pragma unroll
-      for (int u = 0; u < U; ++u) o[u][f] = Half<T>::mfma(vf, pf[u], o[u][f]);
+      for (int u = 0; u < U; ++u) o[u][f] = Half<T>::mfma(vf[f], pf[u], o[u][f]);
     }
   };
 
@@ -710,8 +845,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
       if (st + 2 < hi) find(st + 2);
       __syncthreads();
       if (busy) {
-        const bool whole = st < ctx && (st + 1) * SK <= q.len;
-        if (whole) {
+        if (whole(st)) {
 #pragma unroll 1
           for (uint32_t half = 0; half < SK / 32; ++half) compute(std::false_type{}, st, half, buf);
         } else {
@@ -722,14 +856,17 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
     }
   }
   if (!busy) return;
+  const ArgsPtr g = args_again();
+  const uint32_t group = g->group.d;
   // infinities and NaN, left out above: to the rows that see them
   if (hi > ctx && odd) {
+    const T *vn = static_cast<const T *>(g->a.d_v_new) + b * g->a.v_new_batch + h * g->a.v_new_head;
 #pragma unroll
     for (int u = 0; u < U; ++u)
       for (uint32_t first = (max(lo, ctx) - ctx) * SK; first < (hi - ctx) * SK && first < q.live; first += 32) {
-        const uint32_t seen = alive[u] ? tree_bits(a, k, b, node[u], first, q.live) : 0u;
+        const uint32_t seen = alive[u] ? tree_bits(b, node[u], first, q.live) : 0u;
         for (uint32_t key = 0; key < 32 && first + key < q.live; ++key) {
-          const T *row = vn + (uint64_t)(first + key) * a.v_new_node;
+          const T *row = vn + (uint64_t)(first + key) * g->a.v_new_node;
           if (!(seen >> key & 1u)) continue;
 #pragma unroll
           for (int f = 0; f < NF; ++f)
@@ -746,10 +883,10 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
   for (int u = 0; u < U; ++u) {
     l[u] = rows_sum(l[u]);
     const uint32_t r = row0 + 16 * u;
-    if (r >= k.rows) continue;
-    if (k.splits == 1) {
-      const uint32_t head = h * k.group.d + (r - node[u] * k.group.d);
-      T *dst = static_cast<T *>(a.d_out) + b * a.out_batch + node[u] * a.out_node + head * a.out_head;
+    if (r >= g->rows) continue;
+    if (sh.parts == 1) {
+      const uint32_t head = h * group + (r - node[u] * group);
+      T *dst = static_cast<T *>(g->a.d_out) + b * g->a.out_batch + node[u] * g->a.out_node + head * g->a.out_head;
       const bool any = alive[u] && l[u] != 0.f;
       const float inv = any ? 1.0f / l[u] : 0.f;
 #pragma unroll
@@ -760,16 +897,16 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
               any ? make_uint2(pack2<T>(o[u][f][0] * inv, o[u][f][1] * inv), pack2<T>(o[u][f][2] * inv, o[u][f][3] * inv))
                   : make_uint2(0u, 0u);
       }
-      if (a.d_lse && g4 == 0)
-        a.d_lse[((uint64_t)b * a.nodes + node[u]) * a.q_heads + head] =
+      if (g->a.d_lse && g4 == 0)
+        g->a.d_lse[((uint64_t)b * g->a.nodes + node[u]) * g->a.q_heads + head] =
             any ? m[u] + __log2f(l[u]) * kLn2 : -__builtin_inff();
     } else {
-      const uint64_t at = (((uint64_t)b * a.kv_heads + h) * k.splits + split) * k.rows + r;
+      const uint64_t at = ((uint64_t)part * g->a.kv_heads + h) * g->rows + r;
       if (g4 == 0) {
-        k.part_ml[2 * at] = m[u];
-        k.part_ml[2 * at + 1] = l[u];
+        g->part_ml[2 * at] = m[u];
+        g->part_ml[2 * at + 1] = l[u];
       }
-      float *dst = k.part + at * D;
+      float *dst = g->part + at * D;
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
         const uint32_t d = 16 * f + 4 * g4;
@@ -790,23 +927,22 @@ __global__ __launch_bounds__(256) void k_tree_attention_join(TreeAttnArgs k, uin
   if (item >= a.batch * a.kv_heads * k.rows) return;
   const uint32_t bh = item / k.rows, r = item - bh * k.rows;
   const uint32_t b = bh / a.kv_heads, h = bh - b * a.kv_heads;
+  const Share sh = share_of<false>(k, unit, ways, b);
+  if (sh.parts <= 1) return;   // written by its only part
   const Seq q = sequence_of(a, b);
-  // the splits that had something: units of `unit` keys, as they counted them
-  const uint32_t units = (q.len + unit - 1) / unit + (q.live + unit - 1) / unit;
-  const uint32_t chunk = split_chunk(units, k.splits, ways);
-  const uint32_t live = (units + chunk - 1) / chunk;
+  const uint32_t live = sh.parts;
   const uint32_t node = k.group.quot(r), head = h * k.group.d + (r - node * k.group.d);
 
-  const uint64_t row = (uint64_t)bh * k.splits * k.rows + r;
+  const uint64_t row = ((uint64_t)sh.first * a.kv_heads + h) * k.rows + r, step = (uint64_t)a.kv_heads * k.rows;
   float m = kLowest;
-  for (uint32_t s = lane; s < live; s += 64) m = fmaxf(m, k.part_ml[2 * (row + (uint64_t)s * k.rows)]);
+  for (uint32_t s = lane; s < live; s += 64) m = fmaxf(m, k.part_ml[2 * (row + s * step)]);
   for (uint32_t o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
   const uint32_t way = lane / LD, d = lane % LD * 4;
   float l = 0.f;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (uint32_t s = way; s < live; s += W) {
-    const uint64_t at = row + (uint64_t)s * k.rows;
+    const uint64_t at = row + s * step;
     const float w = exp_of(k.part_ml[2 * at] - m);
     l += w * k.part_ml[2 * at + 1];
     if (d < a.head_dim) acc += *reinterpret_cast<const f32x4 *>(k.part + at * a.head_dim + d) * w;
@@ -830,7 +966,7 @@ __global__ __launch_bounds__(256) void k_tree_attention_join(TreeAttnArgs k, uin
 
 template <typename T, int DP, int U>
 void launch_unit(const TreeAttnArgs &k, hipStream_t s) {
-  const dim3 grid(k.a.batch * k.splits * k.a.kv_heads), block(256);
+  const dim3 grid(k.grid_parts * k.a.kv_heads), block(256);
   if (k.a.head_dim == DP)
     hipLaunchKernelGGL((k_tree_attention<T, DP, U, true>), grid, block, 0, s, k);
   else
@@ -839,7 +975,7 @@ void launch_unit(const TreeAttnArgs &k, hipStream_t s) {
 
 template <typename T, int DP, int U, int W>
 void launch_wide(const TreeAttnArgs &k, hipStream_t s) {
-  const uint32_t groups = k.a.batch * k.splits * k.a.kv_heads;
+  const uint32_t groups = k.grid_parts * k.a.kv_heads;
   hipLaunchKernelGGL((k_tree_attention_wide<T, DP, U, W>), dim3((groups + 7) / 8 * 8 * k.row_tiles), dim3(64 * W), 0, s,
                      k);
 }
@@ -870,7 +1006,7 @@ void launch_type(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
     launch_dim<T, 128>(k, p, s);
   else
     launch_dim<T, 256>(k, p, s);
-  if (k.splits == 1) return;
+  if (!p.part_bytes) return;
   const dim3 grid((k.a.batch * k.a.kv_heads * k.rows + kWavesA - 1) / kWavesA), block(256);
   if (D <= 64)
     hipLaunchKernelGGL((k_tree_attention_join<T, 16>), grid, block, 0, s, k, p.unit, p.ways);
@@ -897,7 +1033,7 @@ TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a) {
     p.waves = p.ways = 4;
     p.unit = 32;
     p.row_tiles = 1;
-    fill = 1024;
+    fill = 2048;
   } else {
     p.wide = 1;
     p.units = large || rows <= 128 ? 1 : 2;
@@ -908,14 +1044,17 @@ TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a) {
     p.row_tiles = (rows + tile - 1) / tile;
     fill = p.waves == 4 ? 512 : 256;
   }
+  // at most `parts` equal parts, and one more for each sequence (its last, short
+  // one); where that is a small share, they count towards the fill
+  const uint64_t tiles = (uint64_t)a.kv_heads * p.row_tiles;
   const uint64_t units = ((uint64_t)a.max_pages * a.page_size + p.unit - 1) / p.unit + (a.nodes + p.unit - 1) / p.unit;
-  const uint64_t tiles = (uint64_t)a.batch * a.kv_heads * p.row_tiles;
-  uint64_t splits = (fill + tiles - 1) / tiles;
-  const uint64_t cap = (units + p.ways - 1) / p.ways;
-  if (splits > cap) splits = cap;
-  if (splits > 128) splits = 128;
-  p.splits = splits < 1 ? 1 : (uint32_t)splits;
-  const uint64_t parts = p.splits == 1 ? 0 : (uint64_t)a.batch * a.kv_heads * p.splits * rows;
+  uint64_t want = (fill + tiles - 1) / tiles;
+  want = want >= 2ull * a.batch ? want - a.batch : want;
+  const uint64_t most = (units + p.ways - 1) / p.ways * a.batch;
+  p.parts = (uint32_t)(want < most ? want : most);
+  p.grid_parts = p.parts + a.batch;
+  // a sequence never has two parts if all its units fit one wave each
+  const uint64_t parts = units <= p.ways ? 0 : (uint64_t)p.grid_parts * a.kv_heads * rows;
   p.part_bytes = align_up(4 * parts * a.head_dim, 256);
   p.ml_bytes = align_up(8 * parts, 256);
   return p;
