@@ -563,21 +563,31 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
 //
 // W waves of U units each hold W U 16 different rows and go through the same
 // keys, a stage of SK at a time, held twice in LDS (the next stage is on its
-// way into registers while one is computed). Rows of a stage lie 16 bytes
-// further apart than they are long, so that reading one chunk of 16 rows (K)
-// and 32 bytes of 16 rows (V) touches all banks evenly, at offsets known at
-// compile time. V^T fragments come from ds_read_b64_tr: of 16 lanes, lane
-// 4 j + c names values 4 c .. 4 c + 3 of key j, and lane i gets value i of the
-// 4 keys.
+// way into registers while one is computed). Banks: a wave reads one 16-byte
+// chunk of 16 rows of K at a time, in groups of lanes that mix neighbouring
+// chunks, so chunk c of row r lies at c ^ k_turn(r); of V it reads 32 bytes of
+// 8 rows, so rows lie 32 bytes further apart than they are long. V^T fragments
+// come from ds_read_b64_tr: of 16 lanes, lane 4 j + c names values 4 c .. 4 c
+// + 3 of key j, and lane i gets value i of the 4 keys.
+template <int NCH>
+__device__ __forceinline__ constexpr uint32_t k_turn(uint32_t r) {
+  return NCH == 8 ? r >> 1 & 7 : r & 15;   // 16 rows (two to 256 bytes, for 8 chunks) on 16 places
+}
+
+// Keys in a stage: two strips, or one where two would leave a compute unit
+// with a single workgroup of four waves.
+constexpr int stage_keys(int dp, int waves) { return dp == 256 || (dp == 128 && waves == 4) ? 32 : 64; }
+
 template <typename T, int DP, int U, int W>
 __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs k) {
   constexpr int KS = DP / 32, NF = DP / 16, NCH = DP / 8;
-  constexpr int SK = DP == 256 ? 32 : 64;
+  constexpr int SK = stage_keys(DP, W);
+  constexpr bool PIPE = DP <= 128;                 // registers for a strip's K and V fragments at once
+  constexpr uint32_t NB = PIPE ? 3 : 2;            // stages in LDS
   constexpr int NT = 64 * W, NR = SK * NCH / NT;   // chunks of K (and of V) a thread brings in
-  constexpr bool EARLY_V = DP <= 128;              // registers for all of a strip's V fragments
-  constexpr int PITCH = NCH + 1;                   // 16-byte chunks from row to row
+  constexpr int PITCH = NCH + 2;                   // 16-byte chunks from row to row of V
   const enc_tree_attention_args &a = k.a;
-  __shared__ __align__(16) uint4 ks[2][SK * PITCH], vs[2][SK * PITCH];
+  __shared__ __align__(16) uint4 ks[NB][SK * NCH], vs[NB][SK * PITCH];
   __shared__ uint32_t odd;
 
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -699,6 +709,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
   };
   auto place = [&](uint32_t st, uint32_t buf) {
     if (st >= ctx) {   // the tree's values go in finite
+      asm volatile("");   // a branch, not selects on every stage's way
       constexpr uint32_t E = Half<T>::kExp;
       bool bad = false;
 #pragma unroll
@@ -715,24 +726,38 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
     }
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      const uint32_t at = (r0 + i * kRowStep) * PITCH + ch;
-      ks[buf][at] = kr[i];
-      vs[buf][at] = vr[i];
+      const uint32_t r = r0 + i * kRowStep;
+      ks[buf][r * NCH + (ch ^ k_turn<NCH>(r))] = kr[i];
+      vs[buf][r * PITCH + ch] = vr[i];
     }
+  };
+
+  // New maxima, and what is summed so far brought to them.
+  auto grow = [&](const float (&top)[U]) {
+    uint32_t out = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float up = fmaxf(top[u] - Half<T>::kLift, m[u]), shrink = exp_of(m[u] - up);
+      m[u] = up;
+      mc[u] = fmaxf(up * kLog2e, kLowest);   // a row that has seen nothing keeps a finite one
+      out |= !(fabsf(up) < 1e38f) && up != kLowest;
+      l[u] *= shrink;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) o[u][f] *= shrink;
+    }
+    far |= (uint32_t)(__ballot(out) != 0);
   };
 
   // ---- one strip of 32 keys of a stage
   auto compute = [&](auto special_, uint32_t st, uint32_t half, uint32_t buf) {
     constexpr bool SPECIAL = decltype(special_)::value;
-    // LDS reads in two batches, each on its way while something else runs: K,
-    // then V behind the products with K
     uint4 kf[2][KS];
     {
-      const uint4 *row = ks[buf] + (half * 32 + l16) * PITCH + g4;
+      const uint4 *row = ks[buf] + (half * 32 + l16) * NCH;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < KS; ++e) kf[t][e] = row[16 * t * PITCH + 4 * e];
+        for (int e = 0; e < KS; ++e) kf[t][e] = row[16 * t * NCH + ((4 * e + g4) ^ k_turn<NCH>(l16))];
     }
     const char *vb = reinterpret_cast<const char *>(vs[buf] + (half * 32 + 4 * g4 + (l16 >> 2)) * PITCH) + (l16 & 3) * 8;
     float p[U][8];
@@ -750,17 +775,6 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[u][4 * t + e] = s[u][e];
-    }
-
-    uint4 vf[NF];
-    if constexpr (EARLY_V) {
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const uint2 v0 = read_transposed(vb + 32 * f), v1 = read_transposed(vb + 16 * PITCH * 16 + 32 * f);
-        vf[f] = make_uint4(v0.x, v0.y, v1.x, v1.y);
-      }
-      __builtin_amdgcn_sched_barrier(0);
     }
 
     const bool tree = SPECIAL && st >= ctx;
@@ -790,20 +804,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
       top[u] = rows_max(t) * scale;
       grown = grown || top[u] > m[u] + (kSlack + Half<T>::kLift);
     }
-    if (__any(grown)) {
-      uint32_t out = 0;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float up = fmaxf(top[u] - Half<T>::kLift, m[u]), shrink = exp_of(m[u] - up);
-        m[u] = up;
-        mc[u] = fmaxf(up * kLog2e, kLowest);   // a row that has seen nothing keeps a finite one
-        out |= !(fabsf(up) < 1e38f) && up != kLowest;
-        l[u] *= shrink;
-#pragma unroll
-        for (int f = 0; f < NF; ++f) o[u][f] *= shrink;
-      }
-      far |= (uint32_t)(__ballot(out) != 0);
-    }
+    if (__any(grown)) grow(top);
     if (far) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -823,29 +824,163 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
     }
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
-      if constexpr (!EARLY_V) {
-        const uint2 v0 = read_transposed(vb + 32 * f), v1 = read_transposed(vb + 16 * PITCH * 16 + 32 * f);
-        vf[f] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+      const uint2 v0 = read_transposed(vb + 32 * f), v1 = read_transposed(vb + 16 * PITCH * 16 + 32 * f);
+      const uint4 vf = make_uint4(v0.x, v0.y, v1.x, v1.y);
+#pragma unroll
+      for (int u = 0; u < U; ++u) o[u][f] = Half<T>::mfma(vf, pf[u], o[u][f]);
+    }
+  };
+
+  // ---- whole strips, two in flight: while the exponentials of one are taken,
+  // the products of the next with K run, and while its products with V run,
+  // the next's maxima are taken
+  float p[U][8], top[U];
+  uint4 kf[2][KS];
+  auto read_k = [&](uint32_t buf, uint32_t half) {
+    const uint4 *row = ks[buf] + (half * 32 + l16) * NCH;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < KS; ++e) kf[t][e] = row[16 * t * NCH + ((4 * e + g4) ^ k_turn<NCH>(l16))];
+  };
+  auto maxima = [&] {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float t = p[u][0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) t = fmaxf(t, p[u][j]);
+      top[u] = rows_max(t) * scale;
+    }
+  };
+  auto scores = [&](float (&x)[U][8]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      f32x4 s[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < KS; ++e)
+#pragma unroll
+        for (int u = 0; u < U; ++u) s[u] = Half<T>::mfma(kf[t][e], qf[u][e], s[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[u][4 * t + e] = s[u][e];
+    }
+  };
+  auto step = [&](uint32_t buf, uint32_t half, uint32_t next_buf, uint32_t next_half) {
+    read_k(next_buf, next_half);
+    uint4 vf[NF];
+    const char *vb = reinterpret_cast<const char *>(vs[buf] + (half * 32 + 4 * g4 + (l16 >> 2)) * PITCH) + (l16 & 3) * 8;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const uint2 v0 = read_transposed(vb + 32 * f), v1 = read_transposed(vb + 16 * PITCH * 16 + 32 * f);
+      vf[f] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+    }
+    bool grown = false;
+#pragma unroll
+    for (int u = 0; u < U; ++u) grown = grown || top[u] > m[u] + (kSlack + Half<T>::kLift);
+    if (__any(grown)) grow(top);
+    float off[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) off[u] = mc[u];
+    if (far) {   // scores less their maximum first, so that nothing overflows
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float less = m[u] / scale;
+        off[u] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[u][j] -= less;
       }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    float x[U][8];
+    uint4 pf[U];
+    scores(x);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[u][j] = __builtin_amdgcn_exp2f(fmaf(p[u][j], c2, -off[u]));
+      l[u] += ((p[u][0] + p[u][1]) + (p[u][2] + p[u][3])) + ((p[u][4] + p[u][5]) + (p[u][6] + p[u][7]));
+      pf[u] = make_uint4(pack2<T>(p[u][0], p[u][1]), pack2<T>(p[u][2], p[u][3]), pack2<T>(p[u][4], p[u][5]),
+                         pack2<T>(p[u][6], p[u][7]));
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * KS * U; ++i) {   // a product, then a few of the others, in turn
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[u][j] = x[u][j];
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
 #pragma unroll
       for (int u = 0; u < U; ++u) o[u][f] = Half<T>::mfma(vf[f], pf[u], o[u][f]);
+    maxima();
+#pragma unroll
+    for (int i = 0; i < NF * U; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   if (tid == 0) odd = 0;
   __syncthreads();
   if (lo < hi) {
+    // one stage is placed ahead of the one that is computed (its first K is
+    // read before the other's end), the one after it is on its way
+    uint32_t st = lo, buf = 0;
+    auto advance = [&] {
+      const uint32_t next = buf + 1 == NB ? 0 : buf + 1;
+      if constexpr (PIPE) {
+        if (st + 1 < hi) place(st + 1, next);
+        if (st + 2 < hi) fetch(st + 2);
+        if (st + 3 < hi) find(st + 3);
+      } else {
+        place(st, buf);
+        if (st + 1 < hi) fetch(st + 1);
+        if (st + 2 < hi) find(st + 2);
+      }
+      __syncthreads();
+      return next;
+    };
     find(lo);
     fetch(lo);
     if (lo + 1 < hi) find(lo + 1);
-    for (uint32_t st = lo; st < hi; ++st) {
-      const uint32_t buf = (st - lo) & 1;
-      place(st, buf);
-      if (st + 1 < hi) fetch(st + 1);
-      if (st + 2 < hi) find(st + 2);
-      __syncthreads();
+    if constexpr (PIPE) {
+      place(lo, 0);
+      if (lo + 1 < hi) fetch(lo + 1);
+      if (lo + 2 < hi) find(lo + 2);
+    }
+    const uint32_t whole_end = min(hi, q.len / SK);
+    if constexpr (PIPE) {
+      for (; st < whole_end; ++st) {
+        const uint32_t next = advance();
+        if (busy) {
+          if (st == lo) {
+            read_k(buf, 0);
+            scores(p);
+            maxima();
+          }
+          const bool more = st + 1 < whole_end;   // else: products that nobody asks for
+          if constexpr (SK == 64) {
+            step(buf, 0, buf, 1);
+            step(buf, 1, more ? next : buf, 0);
+          } else {
+            step(buf, 0, more ? next : buf, 0);
+          }
+        }
+        buf = next;
+      }
+    }
+    for (; st < hi; ++st) {
+      const uint32_t next = advance();
       if (busy) {
-        if (whole(st)) {
+        if (!PIPE && whole(st)) {
 #pragma unroll 1
           for (uint32_t half = 0; half < SK / 32; ++half) compute(std::false_type{}, st, half, buf);
         } else {
@@ -853,6 +988,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
           for (uint32_t half = 0; half < SK / 32; ++half) compute(std::true_type{}, st, half, buf);
         }
       }
+      buf = next;
     }
   }
   if (!busy) return;
@@ -1039,7 +1175,7 @@ TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a) {
     p.units = large || rows <= 128 ? 1 : 2;
     p.waves = rows <= 64 ? 4 : 8;
     p.ways = 1;
-    p.unit = large ? 32 : 64;
+    p.unit = stage_keys(large ? 256 : a.head_dim > 64 ? 128 : 64, p.waves);
     const uint32_t tile = 16 * p.units * p.waves;
     p.row_tiles = (rows + tile - 1) / tile;
     fill = p.waves == 4 ? 512 : 256;
