@@ -868,8 +868,11 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
         for (int e = 0; e < 4; ++e) x[u][4 * t + e] = s[u][e];
     }
   };
-  auto step = [&](uint32_t buf, uint32_t half, uint32_t next_buf, uint32_t next_half) {
-    read_k(next_buf, next_half);
+  // (k_buf, k_half): the strip whose K is read here: the next one, before its
+  // products, or, where a stage holds two strips, the one after it, as soon as
+  // the next one's products have been started
+  auto step = [&](uint32_t buf, uint32_t half, uint32_t k_buf, uint32_t k_half) {
+    if constexpr (SK == 32) read_k(k_buf, k_half);
     uint4 vf[NF];
     const char *vb = reinterpret_cast<const char *>(vs[buf] + (half * 32 + 4 * g4 + (l16 >> 2)) * PITCH) + (l16 & 3) * 8;
 #pragma unroll
@@ -911,6 +914,10 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
       __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (SK == 64) {
+      read_k(k_buf, k_half);
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -965,11 +972,12 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
             read_k(buf, 0);
             scores(p);
             maxima();
+            if constexpr (SK == 64) read_k(buf, 1);
           }
           const bool more = st + 1 < whole_end;   // else: products that nobody asks for
           if constexpr (SK == 64) {
-            step(buf, 0, buf, 1);
-            step(buf, 1, more ? next : buf, 0);
+            step(buf, 0, more ? next : buf, 0);
+            step(buf, 1, more ? next : buf, 1);
           } else {
             step(buf, 0, more ? next : buf, 0);
           }
