@@ -3,17 +3,16 @@
 //
 // The walk itself needs a target and a draft probability per child, gathered
 // for all nodes at once. What it reads in bulk is one row of the target and
-// of the draft per rejection (the sum of max(r - q, 0)) and at its end (the
-// draw). r is never stored: with the sums S_1 .. S_k of the rejections before,
-// element i is recomputed from p_i and q_i in k steps, so a row is read
-// again, from cache, rather than written.
+// of the draft for each node at which a child is rejected (the sum of
+// max(r - q, 0)) or at which it ends (the draw). A lane keeps its part of the
+// row in registers from the first rejection to the draw; without them, r is
+// recomputed from p, q and the sums of the rejections before.
 //
 // Sums are whole numbers of 2^-40: exact, so neither the split over lanes,
 // waves and workgroups nor its order shows in the answer.
 //
 // Bound: HBM traffic of those rows, and the rounds' latency. A row is split
-// over up to 16 workgroups (one for small rows, fewer for large batches);
-// every workgroup makes the same walk, sums its part of a row, publishes the
+// over up to 16 workgroups; every workgroup makes the same walk, sums its part of a row, publishes the
 // sums of its waves' segments and takes those of the others. A workgroup that
 // waits too long for the others (which may not have been scheduled) computes
 // all segments by itself from then on, so no wait is unbounded. The
@@ -32,12 +31,19 @@ typedef unsigned long long u64;
 
 __device__ __forceinline__ float clamp01(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
 
-__device__ __forceinline__ u64 mass(float x) {
-  // x 2^40 = hi 2^20 + lo: exact, and above 2^24 there is nothing to round
+// x in whole multiples of 2^-40: hi 2^20 + lo. Exact but for lo's rounding;
+// above 2^24 there is nothing to round. Sums of up to 4096 of either fit 32
+// bits.
+__device__ __forceinline__ void mass_parts(float x, uint32_t &hi, uint32_t &lo) {
   const float y = x * 1099511627776.f;
-  const float hi = truncf(y * (1.f / 1048576.f));
-  const float lo = fmaf(-hi, 1048576.f, y);
-  return ((u64)(uint32_t)hi << 20) + (u64)(uint32_t)rintf(lo);
+  const float h = truncf(y * (1.f / 1048576.f));
+  hi = (uint32_t)h;
+  lo = (uint32_t)rintf(fmaf(-h, 1048576.f, y));
+}
+__device__ __forceinline__ u64 mass(float x) {
+  uint32_t hi, lo;
+  mass_parts(x, hi, lo);
+  return ((u64)hi << 20) + lo;
 }
 
 template <typename T> __device__ __forceinline__ float value_at(const void *row, uint32_t i);
@@ -81,7 +87,22 @@ __device__ __forceinline__ float residual(float p, float q, int32_t i, const Rej
   return r;
 }
 
-template <typename T, bool POINT>
+// Four consecutive values, in one load.
+template <typename T>
+__device__ __forceinline__ void four_at(const void *row, uint32_t i, float (&x)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(row) + i);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(row) + i);
+    x[0] = half_of<T>(v.x, 0), x[1] = half_of<T>(v.x, 1), x[2] = half_of<T>(v.y, 0), x[3] = half_of<T>(v.y, 1);
+  }
+  for (int e = 0; e < 4; ++e) x[e] = clamp01(x[e]);
+}
+
+// EPT: values of a row a lane keeps in registers, so that the rejections at a
+// node and the draw from it read the row once; 0: rows are read each time.
+template <typename T, bool POINT, uint32_t EPT>
 __global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
   const enc_verify_args &a = k.a;
   __shared__ int32_t token[kMaxNodes];
@@ -139,6 +160,52 @@ __global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
   uint32_t round = 0;
   bool solo = false;         // this workgroup no longer waits for the others
 
+  // this lane's values of the current node's row: chunk c of 4 holds elements
+  // seg0 + 256 c + 4 lane .. + 3
+  constexpr uint32_t N = EPT ? EPT : 4;
+  float r[N], q[N], left[N];
+  const uint32_t seg0 = (g * kWaves + wave) * k.segment;
+  int32_t held = -1;         // the node whose row they are
+  auto hold = [&](uint32_t cur, bool with_q) {
+    if (held == (int32_t)cur) return;
+    held = (int32_t)cur;
+    const char *prow = target + cur * trow, *qrow = draft + cur * drow;
+    // 4 values in a load where the wave's part of both rows allows it
+    const bool whole = ((reinterpret_cast<uintptr_t>(prow) | (POINT ? 0 : reinterpret_cast<uintptr_t>(qrow))) &
+                        (4 * sizeof(T) - 1)) == 0 && seg0 + 64 * N <= V;
+    if (whole) {
+#pragma unroll
+      for (uint32_t c = 0; c < N; c += 4) {
+        const uint32_t i = seg0 + 64 * c + 4 * lane;
+        float p4[4], q4[4] = {0.f, 0.f, 0.f, 0.f};
+        four_at<T>(prow, i, p4);
+        if (!POINT && with_q) four_at<T>(qrow, i, q4);
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) r[c + e] = p4[e], q[c + e] = q4[e];
+      }
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < N; ++j) {
+        const uint32_t i = seg0 + 64 * (j & ~3u) + 4 * lane + (j & 3u);
+        r[j] = i < V ? value_at<T>(prow, i) : 0.f;
+        q[j] = !POINT && with_q && i < V ? value_at<T>(qrow, i) : 0.f;
+      }
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < N; ++j) left[j] = r[j];
+  };
+  auto index_of = [&](uint32_t j) { return seg0 + 64 * (j & ~3u) + 4 * lane + (j & 3u); };
+  // the row after one more rejection whose sum was `sum`
+  auto reject = [&](float sum, int32_t x) {
+#pragma unroll
+    for (uint32_t j = 0; j < N; ++j) {
+      const float qk = POINT ? ((int32_t)index_of(j) == x ? 1.f : 0.f) : q[j];
+      left[j] = fmaxf(r[j] - qk, 0.f);
+      r[j] = left[j] / sum;
+      if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // a few quotients at a time: registers
+    }
+  };
+
   // Sums of `left` over every segment of the current node's row, after n
   // rejections, into totals[]; returns their sum. With `pending`, the n-th
   // rejection's own sum is what is being computed: r - q is taken of r.
@@ -170,13 +237,27 @@ __global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
       }
       return wave_sum(acc);
     };
+    auto own_sum = [&]() -> u64 {
+      if (!EPT) return segment_sum(g * kWaves + wave);
+      hold(cur, pending);
+      uint32_t his = 0, los = 0;
+#pragma unroll
+      for (uint32_t j = 0; j < N; ++j) {
+        const float qk = POINT ? ((int32_t)index_of(j) == ptoken ? 1.f : 0.f) : q[j];
+        uint32_t hi, lo;
+        mass_parts(pending ? fmaxf(r[j] - qk, 0.f) : left[j], hi, lo);
+        his += hi, los += lo;
+        if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      }
+      return wave_sum(((u64)his << 20) + los);
+    };
     if (G > 1 && !solo) {
       // a sum and the round it belongs to (modulo 3, plus 1) in one word, so a
       // word is there or not; two slots in turn: nobody writes round r + 2
       // before everybody has published r + 1, and so has read r
       u64 *out = k.totals + ((uint64_t)b * 2 + (round & 1)) * segments;
       const u64 tag = (u64)(round % 3 + 1) << 62;
-      const u64 t = segment_sum(g * kWaves + wave);
+      const u64 t = own_sum();
       if (lane == 0)
         __hip_atomic_store(&out[g * kWaves + wave], t | tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       if (wave * 64 < segments) {
@@ -196,7 +277,10 @@ __global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
       __syncthreads();
       solo = alone;
     }
-    if (G == 1 || solo) {
+    if (G == 1) {
+      const u64 t = own_sum();
+      if (lane == 0) totals[wave] = t;
+    } else if (solo) {
       for (uint32_t s = wave; s < segments; s += kWaves) {
         const u64 t = segment_sum(s);
         if (lane == 0) totals[s] = t;
@@ -229,43 +313,46 @@ __global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
         const uint64_t m = __ballot(parent[j] == (int32_t)cur && i > last);
         if (!c && m) c = 64 * j + (uint32_t)__builtin_ctzll(m);
       }
-      if (!c) break;
-      last = (int32_t)c;
-      const int32_t x = token[c];
-      if (x < 0) continue;
-      float left;
+      if (!c && have) break;
+      const int32_t x = c ? token[c] : -1;
       const uint32_t n = rej.n;
-      const float r = residual<POINT>(pc[c], qc[c], x, rej, n, left);
-      if (u[c] * qc[c] < r) {
-        cur = c;
-        have = false;
-        __syncthreads();
-        if (tid == 0) {
-          path[count] = (int32_t)c;
-          rej.n = 0;
+      if (c) {
+        last = (int32_t)c;
+        if (x < 0) continue;
+        float l;
+        if (u[c] * qc[c] < residual<POINT>(pc[c], qc[c], x, rej, n, l)) {
+          cur = c;
+          have = false;
+          __syncthreads();
+          if (tid == 0) {
+            path[count] = (int32_t)c;
+            rej.n = 0;
+          }
+          ++count;
+          __syncthreads();
+          continue;
         }
-        ++count;
         __syncthreads();
-        continue;
+        if (tid == 0) rej.token[n] = x;
+        __syncthreads();
       }
-      __syncthreads();
-      if (tid == 0) rej.token[n] = x;
-      __syncthreads();
-      const u64 sum = sum_row(cur, n, true);
-      if (sum) {
+      // c was rejected, or there is no child left and no sum yet
+      const u64 sum = sum_row(cur, n, c != 0);
+      if (sum || !c) {
         if (tid < segments) kept[tid] = totals[tid];
         total = sum;
         have = true;
       }
+      if (!c) {
+        __syncthreads();
+        break;
+      }
+      const float sum32 = (float)sum * (1.f / 1099511627776.f);
+      if (EPT && !solo && sum) reject(sum32, x);
       if (tid == 0) {
-        rej.sum[n] = (float)sum * (1.f / 1099511627776.f);
+        rej.sum[n] = sum32;
         rej.n = n + 1;
       }
-      __syncthreads();
-    }
-    if (!have) {
-      total = sum_row(cur, rej.n, false);
-      if (tid < segments) kept[tid] = totals[tid];
       __syncthreads();
     }
   }
@@ -305,14 +392,37 @@ __global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
     }
     __syncthreads();
     const uint32_t seg = hit;
-    if (seg / kWaves == g) {
+    if (EPT && !solo) {
+      if (seg == g * kWaves + wave) {
+        u64 at = hit_before;
+#pragma unroll
+        for (uint32_t c = 0; c < N; c += 4) {
+          u64 w[4], four = 0;
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) four += w[e] = mass(left[c + e]);
+          u64 incl = four;
+          for (uint32_t o = 1; o < 64; o <<= 1) {
+            const u64 t = __shfl_up(incl, o);
+            if (lane >= o) incl += t;
+          }
+          u64 from = at + incl - four;
+          if (from <= goal && goal < from + four) {
+            uint32_t e = 0;
+            while (from + w[e] <= goal) from += w[e++];
+            a.d_token[b] = (int32_t)(index_of(c) + e);
+          }
+          at += __shfl(incl, 63);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    } else if (seg / kWaves == g) {
       const char *prow = target + cur * trow, *qrow = draft + cur * drow;
       const uint32_t lo = seg * k.segment, hi = min(lo + k.segment, V);
       const uint32_t per = (k.segment + kThreadsV - 1) / kThreadsV;
       auto left_at = [&](uint32_t i) -> u64 {
-        float left;
-        residual<POINT>(value_at<T>(prow, i), POINT ? 0.f : value_at<T>(qrow, i), (int32_t)i, rej, rej.n, left);
-        return mass(left);
+        float l;
+        residual<POINT>(value_at<T>(prow, i), POINT ? 0.f : value_at<T>(qrow, i), (int32_t)i, rej, rej.n, l);
+        return mass(l);
       };
       const uint32_t i0 = lo + tid * per;
       u64 sum = 0;
@@ -344,30 +454,46 @@ __global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
   }
 }
 
+template <typename T, bool POINT>
+void launch_kept(const VerifyKernelArgs &k, hipStream_t s) {
+  const dim3 grid(k.a.batch * k.groups), block(kThreadsV);
+  switch (k.segment) {
+    case 64 * 4: hipLaunchKernelGGL((k_verify<T, POINT, 4>), grid, block, 0, s, k); break;
+    case 64 * 8: hipLaunchKernelGGL((k_verify<T, POINT, 8>), grid, block, 0, s, k); break;
+    case 64 * 16: hipLaunchKernelGGL((k_verify<T, POINT, 16>), grid, block, 0, s, k); break;
+    default: hipLaunchKernelGGL((k_verify<T, POINT, 0>), grid, block, 0, s, k); break;
+  }
+}
+
 template <typename T>
 void launch_t(const VerifyKernelArgs &k, hipStream_t s) {
-  const dim3 grid(k.a.batch * k.groups), block(kThreadsV);
   if (k.a.d_draft)
-    hipLaunchKernelGGL((k_verify<T, false>), grid, block, 0, s, k);
+    launch_kept<T, false>(k, s);
   else
-    hipLaunchKernelGGL((k_verify<T, true>), grid, block, 0, s, k);
+    launch_kept<T, true>(k, s);
 }
 
 }  // namespace
 
-// Workgroups per sequence: the device's 256 compute units shared among the
-// sequences, at most 16 (a wave's sums then fit one thread each), and no
-// more than leave a workgroup 4096 elements.
+// A lane keeps 4, 8 or 16 values of a row, a workgroup 4096, 8192 or 16384; of
+// these the smallest with which the workgroups of all sequences find a
+// compute unit each, and a sequence has at most 16 (whose waves' sums then fit
+// a thread each). Rows above 16 x 16384 values are read again each time.
 VerifyPlan plan_verify_tree(uint32_t batch, uint32_t vocab) {
   VerifyPlan p;
-  uint32_t g = batch ? 256 / batch : 1;
-  const uint32_t most = (vocab + 4095) / 4096;
-  if (g > most) g = most;
-  if (g > kMaxGroups) g = kMaxGroups;
-  if (g < 1) g = 1;
-  p.groups = g;
-  const uint32_t segments = g * kWaves;
-  p.segment = ((vocab + segments - 1) / segments + 255) & ~255u;
+  uint32_t ept = 4;
+  while (ept < 16) {
+    const uint32_t g = (vocab + kWaves * 64 * ept - 1) / (kWaves * 64 * ept);
+    if (g <= kMaxGroups && (uint64_t)g * batch <= 256) break;
+    ept *= 2;
+  }
+  p.segment = 64 * ept;
+  p.groups = (vocab + kWaves * p.segment - 1) / (kWaves * p.segment);
+  if (p.groups > kMaxGroups) {
+    p.groups = kMaxGroups;
+    p.segment = ((vocab + kMaxSegments - 1) / kMaxSegments + 255) & ~255u;
+  }
+  const uint32_t segments = p.groups * kWaves;
   p.totals_bytes = align_up(8ull * batch * 2 * segments, 256);
   p.done_bytes = align_up(4ull * batch, 256);
   return p;
