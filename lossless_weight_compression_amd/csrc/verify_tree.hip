@@ -29,21 +29,21 @@ constexpr uint32_t kMaxGroups = 16, kMaxSegments = kMaxGroups * kWaves;
 constexpr uint32_t kMaxNodes = ENC_TREE_MAX_NODES;
 typedef unsigned long long u64;
 
-__device__ __forceinline__ float clamp01(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
+__device__ __forceinline__ float clamp01(float x) { return __builtin_amdgcn_fmed3f(x, 0.f, 1.f); }   // NaN: 0
 
-// x in whole multiples of 2^-40: hi 2^20 + lo. Exact but for lo's rounding;
-// above 2^24 there is nothing to round. Sums of up to 4096 of either fit 32
-// bits.
-__device__ __forceinline__ void mass_parts(float x, uint32_t &hi, uint32_t &lo) {
+// x (up to 1) in whole multiples of 2^-40, ties to even. In steps of 2^-20,
+// whose remainder is exact, and which leave nothing to round above 2^-16.
+__device__ __forceinline__ u64 mass(float x) {
   const float y = x * 1099511627776.f;
   const float h = truncf(y * (1.f / 1048576.f));
-  hi = (uint32_t)h;
-  lo = (uint32_t)rintf(fmaf(-h, 1048576.f, y));
+  return ((u64)(uint32_t)h << 20) + (uint32_t)rintf(fmaf(-h, 1048576.f, y));
 }
-__device__ __forceinline__ u64 mass(float x) {
-  uint32_t hi, lo;
-  mass_parts(x, hi, lo);
-  return ((u64)hi << 20) + lo;
+
+// Four of them; as almost always, none reaches 2^-8, and each fits 32 bits.
+__device__ __forceinline__ u64 mass4(float a, float b, float c, float d) {
+  if (__any(fmaxf(fmaxf(a, b), fmaxf(c, d)) >= 0.00390625f)) return (mass(a) + mass(b)) + (mass(c) + mass(d));
+  auto small = [](float x) { return (u64)(uint32_t)rintf(x * 1099511627776.f); };
+  return (small(a) + small(b)) + (small(c) + small(d));
 }
 
 template <typename T> __device__ __forceinline__ float value_at(const void *row, uint32_t i);
@@ -114,7 +114,11 @@ __global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
   __shared__ uint32_t alone;
 
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const uint32_t G = k.groups, b = blockIdx.x / G, g = blockIdx.x - b * G;
+  // a sequence's workgroups differ by 8, which places them on one compute die
+  // (workgroups go to the 8 dies in turn): their words meet in its L2
+  const uint32_t G = k.groups, id8 = blockIdx.x >> 3, set = id8 / G;
+  const uint32_t b = set * 8 + (blockIdx.x & 7), g = id8 - set * G;
+  if (b >= a.batch) return;
   const uint32_t segments = G * kWaves;
   const uint32_t T_ = a.nodes, V = a.vocab;
   int32_t live = a.d_nodes ? a.d_nodes[b] : (int32_t)T_;
@@ -166,9 +170,13 @@ __global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
   float r[N], q[N], left[N];
   const uint32_t seg0 = (g * kWaves + wave) * k.segment;
   int32_t held = -1;         // the node whose row they are
+  // After a rejection `left` is the difference, and `over` its sum: r becomes
+  // left / over only if another child is rejected here.
+  float over = 0.f;
   auto hold = [&](uint32_t cur, bool with_q) {
     if (held == (int32_t)cur) return;
     held = (int32_t)cur;
+    over = 0.f;
     const char *prow = target + cur * trow, *qrow = draft + cur * drow;
     // 4 values in a load where the wave's part of both rows allows it
     const bool whole = ((reinterpret_cast<uintptr_t>(prow) | (POINT ? 0 : reinterpret_cast<uintptr_t>(qrow))) &
@@ -195,15 +203,20 @@ __global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
     for (uint32_t j = 0; j < N; ++j) left[j] = r[j];
   };
   auto index_of = [&](uint32_t j) { return seg0 + 64 * (j & ~3u) + 4 * lane + (j & 3u); };
-  // the row after one more rejection whose sum was `sum`
-  auto reject = [&](float sum, int32_t x) {
+  auto settle = [&] {
+    if (!(over > 0.f)) return;
 #pragma unroll
     for (uint32_t j = 0; j < N; ++j) {
-      const float qk = POINT ? ((int32_t)index_of(j) == x ? 1.f : 0.f) : q[j];
-      left[j] = fmaxf(r[j] - qk, 0.f);
-      r[j] = left[j] / sum;
+      r[j] = left[j] / over;
       if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // a few quotients at a time: registers
     }
+    over = 0.f;
+  };
+  auto reject = [&](float sum, int32_t x) {
+#pragma unroll
+    for (uint32_t j = 0; j < N; ++j)
+      left[j] = fmaxf(r[j] - (POINT ? ((int32_t)index_of(j) == x ? 1.f : 0.f) : q[j]), 0.f);
+    over = sum;
   };
 
   // Sums of `left` over every segment of the current node's row, after n
@@ -240,16 +253,20 @@ __global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
     auto own_sum = [&]() -> u64 {
       if (!EPT) return segment_sum(g * kWaves + wave);
       hold(cur, pending);
-      uint32_t his = 0, los = 0;
+      if (pending) settle();
+      u64 acc = 0;
 #pragma unroll
-      for (uint32_t j = 0; j < N; ++j) {
-        const float qk = POINT ? ((int32_t)index_of(j) == ptoken ? 1.f : 0.f) : q[j];
-        uint32_t hi, lo;
-        mass_parts(pending ? fmaxf(r[j] - qk, 0.f) : left[j], hi, lo);
-        his += hi, los += lo;
-        if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      for (uint32_t j = 0; j < N; j += 4) {
+        float d[4];
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) {
+          const float qk = POINT ? ((int32_t)index_of(j + e) == ptoken ? 1.f : 0.f) : q[j + e];
+          d[e] = pending ? fmaxf(r[j + e] - qk, 0.f) : left[j + e];
+        }
+        acc += mass4(d[0], d[1], d[2], d[3]);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      return wave_sum(((u64)his << 20) + los);
+      return wave_sum(acc);
     };
     if (G > 1 && !solo) {
       // a sum and the round it belongs to (modulo 3, plus 1) in one word, so a
@@ -456,7 +473,7 @@ __global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
 
 template <typename T, bool POINT>
 void launch_kept(const VerifyKernelArgs &k, hipStream_t s) {
-  const dim3 grid(k.a.batch * k.groups), block(kThreadsV);
+  const dim3 grid((k.a.batch + 7) / 8 * 8 * k.groups), block(kThreadsV);
   switch (k.segment) {
     case 64 * 4: hipLaunchKernelGGL((k_verify<T, POINT, 4>), grid, block, 0, s, k); break;
     case 64 * 8: hipLaunchKernelGGL((k_verify<T, POINT, 8>), grid, block, 0, s, k); break;
