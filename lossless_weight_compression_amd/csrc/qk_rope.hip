@@ -7,8 +7,7 @@
 // a head of D values is held by D/8 lanes (rounded up to a power of two, so
 // its sum is a butterfly inside one wave), 8 consecutive values each, which
 // makes every load and store 16 bytes or more per lane. Values are exchanged
-// between the two halves of a head through LDS, written as the lane holds
-// them. The table row of a token is read by all its heads from cache.
+// between the two halves of a head through LDS, within the wave.
 #include "step_common.h"
 
 namespace enc {
@@ -50,106 +49,174 @@ __device__ __forceinline__ void load_weight(const void *w, uint32_t dtype, uint3
     Eight<float>::load(static_cast<const float *>(w) + d0, x);
 }
 
-template <typename TI, typename TO, uint32_t LANES>
+// R heads of one token to a lane (the same values of each), so the token's
+// angles are read once for them and R rows are on their way at a time. VEC:
+// the angles of a lane's values lie in runs of 4, aligned.
+template <typename TI, typename TO, uint32_t LANES, uint32_t R, bool VEC>
 __global__ __launch_bounds__(kBlock) void k_qk_norm_rope(QkKernelArgs k) {
   const enc_qk_args &a = k.a;
+  constexpr uint32_t kHeads = kBlock / LANES;   // heads of a workgroup, R times
   __shared__ __align__(16) float xs[kBlock * 8];
   const uint32_t chunk = threadIdx.x % LANES, d0 = chunk * 8;
-  const uint32_t item = blockIdx.x * (kBlock / LANES) + threadIdx.x / LANES;
-  const bool live = item < k.items && d0 < a.head_dim;
-  const uint32_t it = item < k.items ? item : k.items - 1;
-  const uint32_t token = k.per_token.quot(it), head = it - token * k.per_token.d;
-  const bool is_q = head < a.q_heads, is_v = head >= a.q_heads + a.kv_heads;
-  const uint32_t h = is_q ? head : is_v ? head - a.q_heads - a.kv_heads : head - a.q_heads;
-  const uint64_t in = is_q   ? token * a.q_token + h * a.q_head
-                      : is_v ? token * a.v_token + h * a.v_head
-                             : token * a.k_token + h * a.k_head;
-  const uint64_t out = is_q   ? token * a.q_out_token + h * a.q_out_head
-                       : is_v ? token * a.v_out_token + h * a.v_out_head
-                              : token * a.k_out_token + h * a.k_out_head;
-  const TI *src = static_cast<const TI *>(is_q ? a.d_q : is_v ? a.d_v : a.d_k) + in;
-  TO *dst = static_cast<TO *>(is_q ? a.d_q_out : is_v ? a.d_v_out : a.d_k_out) + out;
+  const uint32_t token = k.blocks.quot(blockIdx.x), block = blockIdx.x - token * k.blocks.d;
+  const uint32_t first = block * (kHeads * R) + threadIdx.x / LANES;
+  const uint32_t rotated_heads = a.q_heads + a.kv_heads;
+  const bool in_head = d0 < a.head_dim;
 
-  float x[8];
-  for (int i = 0; i < 8; ++i) x[i] = 0.f;
-  if (live) Eight<TI>::load(src + d0, x);
+  float x[R][8];
+#pragma unroll
+  for (uint32_t i = 0; i < R; ++i) {
+    const uint32_t head = first + i * kHeads;
+    const bool is_q = head < a.q_heads, is_v = head >= rotated_heads;
+    const uint32_t h = is_q ? head : is_v ? head - rotated_heads : head - a.q_heads;
+    const uint64_t at = is_q   ? token * a.q_token + h * a.q_head
+                        : is_v ? token * a.v_token + h * a.v_head
+                               : token * a.k_token + h * a.k_head;
+    const TI *src = static_cast<const TI *>(is_q ? a.d_q : is_v ? a.d_v : a.d_k) + at;
+    for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+    if (head < k.heads && in_head) Eight<TI>::load(src + d0, x[i]);
+  }
 
   const uint32_t half = a.rot_dim / 2;
-  const bool rotated = live && !is_v && d0 < a.rot_dim;
-  const bool placed = a.rot_dim && !is_v;
-  int32_t pos = placed ? a.d_positions[token] : 0;
-  const bool lost = placed && (uint32_t)pos >= a.max_pos;
-  if (lost) pos = 0;
-
-  // pair index of value i: adjacent pairs (2p, 2p + 1), else (p, p + half)
+  const bool turns = in_head && d0 < a.rot_dim;
   const bool adjacent = a.flags & ENC_ROPE_ADJACENT;
+  int32_t pos = a.rot_dim ? a.d_positions[token] : 0;
+  const bool lost = a.rot_dim && (uint32_t)pos >= a.max_pos;
+  if (lost) pos = 0;
+  // value e's angle: pair (d0 + e) / 2 if adjacent (4 of them), else d0 + e, less
+  // half in the second half
   float c[8], s[8];
-  for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
-  if (rotated) {
+  for (int e = 0; e < 8; ++e) c[e] = 1.f, s[e] = 0.f;
+  if (turns) {
     const float *row = a.d_table + (uint64_t)pos * a.rot_dim;
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t d = d0 + i;
-      if (d < a.rot_dim) {
-        const uint32_t p = adjacent ? d / 2 : d < half ? d : d - half;
-        c[i] = row[p];
-        s[i] = row[half + p];
+    if constexpr (VEC) {
+      const uint32_t p = adjacent ? d0 / 2 : d0 < half ? d0 : d0 - half;
+      const f32x4 c0 = *reinterpret_cast<const f32x4 *>(row + p), s0 = *reinterpret_cast<const f32x4 *>(row + half + p);
+      f32x4 c1 = c0, s1 = s0;
+      if (!adjacent) {
+        c1 = *reinterpret_cast<const f32x4 *>(row + p + 4);
+        s1 = *reinterpret_cast<const f32x4 *>(row + half + p + 4);
+      }
+      for (int e = 0; e < 4; ++e) {
+        if (adjacent) {
+          c[2 * e] = c[2 * e + 1] = c0[e];
+          s[2 * e] = s[2 * e + 1] = s0[e];
+        } else {
+          c[e] = c0[e], c[4 + e] = c1[e];
+          s[e] = s0[e], s[4 + e] = s1[e];
+        }
+      }
+    } else {
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t d = d0 + e;
+        if (d < a.rot_dim) {
+          const uint32_t p = adjacent ? d / 2 : d < half ? d : d - half;
+          c[e] = row[p];
+          s[e] = row[half + p];
+        }
       }
     }
   }
 
-  if (!(a.flags & ENC_QK_NO_NORM)) {
-    float ss = 0.f;
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-    for (uint32_t o = LANES / 2; o; o >>= 1) ss += __shfl_xor(ss, o);
-    const float scale = 1.0f / sqrtf(ss / (float)a.head_dim + a.eps);
-    if (!is_v)
-      for (int i = 0; i < 8; ++i) x[i] *= scale;
-  }
-  const void *w = is_q ? a.d_q_weight : a.d_k_weight;
-  if (live && !is_v && w) {
-    float wv[8];
-    load_weight(w, a.w_dtype, d0, wv);
-    for (int i = 0; i < 8; ++i) x[i] *= wv[i];
-  }
-
-  if (adjacent) {
-    for (int i = 0; i < 8; i += 2) {
-      const float u = x[i], v = x[i + 1];
-      x[i] = u * c[i] - v * s[i];
-      x[i + 1] = v * c[i] + u * s[i];
+#pragma unroll
+  for (uint32_t i = 0; i < R; ++i) {
+    const uint32_t head = first + i * kHeads;
+    const bool live = head < k.heads && in_head;
+    const bool is_q = head < a.q_heads, is_v = head >= rotated_heads;
+    if (!(a.flags & ENC_QK_NO_NORM)) {
+      float ss = 0.f;
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[i][e], x[i][e], ss);
+#pragma unroll
+      for (uint32_t o = LANES / 2; o; o >>= 1) ss += __shfl_xor(ss, o);
+      const float scale = 1.0f / sqrtf(ss / (float)a.head_dim + a.eps);
+      if (!is_v)
+        for (int e = 0; e < 8; ++e) x[i][e] *= scale;
     }
-  } else if (a.rot_dim) {   // uniform over the launch
-    float *mine = xs + threadIdx.x * 8;
-    reinterpret_cast<f32x4 *>(mine)[0] = f32x4{x[0], x[1], x[2], x[3]};
-    reinterpret_cast<f32x4 *>(mine)[1] = f32x4{x[4], x[5], x[6], x[7]};
-    __syncthreads();
-    if (rotated) {
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t d = d0 + i;
-        if (d < half)
-          x[i] = x[i] * c[i] - mine[i + half] * s[i];
-        else if (d < a.rot_dim)
-          x[i] = x[i] * c[i] + mine[(int)i - (int)half] * s[i];
+    const void *w = is_q ? a.d_q_weight : a.d_k_weight;
+    if (live && !is_v && w) {
+      float wv[8];
+      load_weight(w, a.w_dtype, d0, wv);
+      for (int e = 0; e < 8; ++e) x[i][e] *= wv[e];
+    }
+    if (adjacent) {
+      if (turns && !is_v) {
+        for (int e = 0; e < 8; e += 2) {
+          const float u = x[i][e], v = x[i][e + 1];
+          x[i][e] = u * c[e] - v * s[e];
+          x[i][e + 1] = v * c[e] + u * s[e];
+        }
       }
+    } else if (a.rot_dim) {   // uniform over the launch
+      // the other half's values through LDS; a head's lanes are one wave's, whose
+      // LDS operations keep their order
+      float *mine = xs + threadIdx.x * 8;
+      reinterpret_cast<f32x4 *>(mine)[0] = f32x4{x[i][0], x[i][1], x[i][2], x[i][3]};
+      reinterpret_cast<f32x4 *>(mine)[1] = f32x4{x[i][4], x[i][5], x[i][6], x[i][7]};
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (turns && !is_v) {
+        if constexpr (VEC) {
+          const float *other = d0 < half ? mine + half : mine - half;
+          const f32x4 o0 = reinterpret_cast<const f32x4 *>(other)[0], o1 = reinterpret_cast<const f32x4 *>(other)[1];
+          for (int e = 0; e < 8; ++e) {
+            const float turn = s[e] * (e < 4 ? o0[e & 3] : o1[e & 3]);
+            x[i][e] = d0 < half ? x[i][e] * c[e] - turn : x[i][e] * c[e] + turn;
+          }
+        } else {
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t d = d0 + e;
+            if (d < half)
+              x[i][e] = x[i][e] * c[e] - mine[e + half] * s[e];
+            else if (d < a.rot_dim)
+              x[i][e] = x[i][e] * c[e] + mine[e - (int)half] * s[e];
+          }
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+    if (lost && !is_v)
+      for (int e = 0; e < 8; ++e) x[i][e] = __builtin_nanf("");
+    if (live) {
+      const uint32_t h = is_q ? head : is_v ? head - rotated_heads : head - a.q_heads;
+      const uint64_t at = is_q   ? token * a.q_out_token + h * a.q_out_head
+                          : is_v ? token * a.v_out_token + h * a.v_out_head
+                                 : token * a.k_out_token + h * a.k_out_head;
+      TO *dst = static_cast<TO *>(is_q ? a.d_q_out : is_v ? a.d_v_out : a.d_k_out) + at;
+      Eight<TO>::store(dst + d0, x[i]);
     }
   }
-  if (lost)
-    for (int i = 0; i < 8; ++i) x[i] = __builtin_nanf("");
-  if (live) Eight<TO>::store(dst + d0, x);
+}
+
+// Three heads to a lane once that still gives every compute unit two
+// workgroups; one where latency counts.
+template <typename TI, typename TO, uint32_t LANES>
+void launch_heads(QkKernelArgs k, hipStream_t s) {
+  constexpr uint32_t per = kBlock / LANES;
+  const uint32_t thirds = (k.heads + 3 * per - 1) / (3 * per);
+  const bool many = k.vec && (uint64_t)thirds * k.a.tokens >= 512;
+  const uint32_t blocks = many ? thirds : (k.heads + per - 1) / per;
+  k.blocks = FastDiv::of(blocks);
+  const dim3 grid(blocks * k.a.tokens), block(kBlock);
+  if (many)
+    hipLaunchKernelGGL((k_qk_norm_rope<TI, TO, LANES, 3, true>), grid, block, 0, s, k);
+  else if (k.vec)
+    hipLaunchKernelGGL((k_qk_norm_rope<TI, TO, LANES, 1, true>), grid, block, 0, s, k);
+  else
+    hipLaunchKernelGGL((k_qk_norm_rope<TI, TO, LANES, 1, false>), grid, block, 0, s, k);
 }
 
 template <typename TI, typename TO>
 void launch_lanes(const QkKernelArgs &k, hipStream_t s) {
   const uint32_t need = k.a.head_dim / 8;
-  const uint32_t lanes = need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 64;
-  const uint32_t per = kBlock / lanes;
-  const dim3 grid((k.items + per - 1) / per), block(kBlock);
-  switch (lanes) {
-    case 8: hipLaunchKernelGGL((k_qk_norm_rope<TI, TO, 8>), grid, block, 0, s, k); break;
-    case 16: hipLaunchKernelGGL((k_qk_norm_rope<TI, TO, 16>), grid, block, 0, s, k); break;
-    case 32: hipLaunchKernelGGL((k_qk_norm_rope<TI, TO, 32>), grid, block, 0, s, k); break;
-    default: hipLaunchKernelGGL((k_qk_norm_rope<TI, TO, 64>), grid, block, 0, s, k); break;
-  }
+  if (need <= 8)
+    launch_heads<TI, TO, 8>(k, s);
+  else if (need <= 16)
+    launch_heads<TI, TO, 16>(k, s);
+  else if (need <= 32)
+    launch_heads<TI, TO, 32>(k, s);
+  else
+    launch_heads<TI, TO, 64>(k, s);
 }
 
 template <typename TI>

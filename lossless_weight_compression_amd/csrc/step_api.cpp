@@ -108,8 +108,9 @@ enc_status enc_qk_norm_rope(const enc_qk_args *a, void *stream) {
   if (heads > 65536 || heads * a->tokens > 0x7FFFFFFFull) return unsupported("tokens * heads above 2^31 - 1");
   QkKernelArgs k;
   k.a = *a;
-  k.per_token = FastDiv::of((uint32_t)heads);
-  k.items = (uint32_t)(heads * a->tokens);
+  k.heads = (uint32_t)heads;
+  k.vec = a->rot_dim % (a->flags & ENC_ROPE_ADJACENT ? 8 : 16) == 0 && aligned(a->d_table, 16);
+  k.blocks = FastDiv::of(1);
   return after_launch(launch_qk_norm_rope(k, (hipStream_t)stream), (hipStream_t)stream, "enc_qk_norm_rope");
 }
 

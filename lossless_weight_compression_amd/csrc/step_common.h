@@ -52,8 +52,9 @@ template <> __device__ __forceinline__ float half_of<_Float16>(uint32_t v, int h
 
 struct QkKernelArgs {
   enc_qk_args a;
-  FastDiv per_token;   // heads a token has: q, k and, if given, v
-  uint32_t items;      // tokens * heads
+  uint32_t heads;      // that a token has: q, k and, if given, v
+  uint32_t vec;        // angles in aligned runs of 4
+  FastDiv blocks;      // workgroups to a token
 };
 hipError_t launch_qk_norm_rope(const QkKernelArgs &k, hipStream_t s);
 
