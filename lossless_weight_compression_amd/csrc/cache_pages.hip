@@ -150,8 +150,9 @@ __global__ __launch_bounds__(kPlanThreads) void k_commit_plan(CommitArgs k) {
   __syncthreads();
   const int32_t status = error ? error : found < need ? (int32_t)(need - found) : 0;
   if (tid == 0) *k.status = status;
-  if (status) {
-    for (uint32_t b = tid; b < k.batch; b += kPlanThreads) k.info[4 * b + 1] = 0;   // nothing to move
+  if (status) {   // nothing to move
+    for (uint32_t b = tid; b < k.batch; b += kPlanThreads) k.info[4 * b + 3] = -1;
+    for (uint64_t i = tid; i < (uint64_t)k.batch * k.nodes; i += kPlanThreads) k.to[i] = -1;
     return;
   }
 
@@ -178,48 +179,53 @@ __global__ __launch_bounds__(kPlanThreads) void k_commit_plan(CommitArgs k) {
     }
     k.c.d_lens[seq] = len + rows;
   }
+  __syncthreads();
+  // where each accepted row goes
+  for (uint64_t i = tid; i < (uint64_t)k.batch * k.nodes; i += kPlanThreads) {
+    const uint32_t b = (uint32_t)(i / k.nodes), j = (uint32_t)(i - (uint64_t)b * k.nodes);
+    int32_t to = -1;
+    if ((int32_t)j < k.info[4 * b + 1]) {
+      const uint32_t t = (uint32_t)k.info[4 * b] + j, p = k.page.quot(t);
+      to = (int32_t)((uint32_t)k.c.d_table[(uint64_t)(uint32_t)k.seqs[b] * k.c.max_pages + p] * k.c.page_size +
+                     (t - p * k.c.page_size));
+    }
+    k.to[i] = to;
+  }
 }
 
-// Rows of one (sequence, plane): first the filled rows of a page that is
-// left, then the accepted rows; in 16-byte items, four in flight a lane.
-__global__ __launch_bounds__(kCopyThreads) void k_commit_move(CommitArgs k) {
+// One (sequence, plane)'s rows: a slot for every node of the tree (empty past
+// the accepted ones), in `node_groups` workgroups, one slot to a thread; then
+// the filled rows of a page that is left, by the other workgroups in turn. A
+// slot is `lanes` threads wide, 16 bytes each. The loads in flight come from
+// many small workgroups: with four slots to a thread it took twice as long.
+__global__ __launch_bounds__(kCopyThreads) void k_commit_move(CommitArgs k, FastDiv lanes, uint32_t slots,
+                                                              uint32_t node_groups) {
   const uint32_t b = blockIdx.x;
   const uint64_t plane = blockIdx.y;
-  const int32_t len = k.info[4 * b], rows = k.info[4 * b + 1];
-  if (rows <= 0) return;
-  const int32_t from = k.info[4 * b + 2], to = k.info[4 * b + 3];
-  const uint32_t per = k.c.row_bytes / 16, ps = k.c.page_size;
-  const uint32_t copied = to >= 0 ? (uint32_t)len - k.page.quot(len) * ps : 0;
+  const uint32_t ps = k.c.page_size, row_bytes = k.c.row_bytes;
   uint8_t *base = static_cast<uint8_t *>(k.c.d_data) + plane * k.c.plane_stride;
-  const uint8_t *draft = k.draft + plane * k.draft_plane + (uint64_t)b * k.draft_seq;
-  const int32_t *row = k.c.d_table + (uint64_t)(uint32_t)k.seqs[b] * k.c.max_pages;
-  const int32_t *path = k.path + (uint64_t)b * k.nodes;
-  const uint64_t items = (uint64_t)(copied + (uint32_t)rows) * per;
-  const uint64_t step = (uint64_t)gridDim.z * kCopyThreads;
-  for (uint64_t i0 = blockIdx.z * kCopyThreads + threadIdx.x; i0 < items; i0 += 4 * step) {
-    uint4 v[4];
-    uint8_t *dst[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint64_t i = i0 + u * step;
-      dst[u] = nullptr;
-      if (i < items) {
-        const uint32_t r = (uint32_t)(i / per), o = (uint32_t)(i - (uint64_t)r * per) * 16;
-        const uint8_t *src;
-        if (r < copied) {
-          src = base + ((uint64_t)(uint32_t)from * ps + r) * k.c.row_bytes + o;
-          dst[u] = base + ((uint64_t)(uint32_t)to * ps + r) * k.c.row_bytes + o;
-        } else {
-          const uint32_t j = r - copied, t = (uint32_t)len + j, p = k.page.quot(t);
-          src = draft + (uint64_t)(uint32_t)path[j] * k.c.row_bytes + o;
-          dst[u] = base + ((uint64_t)(uint32_t)row[p] * ps + (t - p * ps)) * k.c.row_bytes + o;
-        }
-        v[u] = *reinterpret_cast<const uint4 *>(src);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (dst[u]) *reinterpret_cast<uint4 *>(dst[u]) = v[u];
+  const uint32_t in = lanes.quot(threadIdx.x), lane = threadIdx.x - in * lanes.d;   // slot of the workgroup, place in it
+  if (in >= slots) return;
+  if (blockIdx.z < node_groups) {
+    const uint32_t slot = blockIdx.z * slots + in;
+    if (slot >= k.nodes) return;
+    const int32_t to = k.to[(uint64_t)b * k.nodes + slot], node = k.path[(uint64_t)b * k.nodes + slot];
+    if (to < 0) return;
+    const uint8_t *src = k.draft + plane * k.draft_plane + (uint64_t)b * k.draft_seq + (uint64_t)(uint32_t)node * row_bytes;
+    uint8_t *dst = base + (uint64_t)(uint32_t)to * row_bytes;
+    for (uint32_t o = lane * 16; o < row_bytes; o += lanes.d * 16)
+      store_nt16(dst + o, *reinterpret_cast<const uint4 *>(src + o));
+    return;
+  }
+  const int32_t len = k.info[4 * b], from = k.info[4 * b + 2], to = k.info[4 * b + 3];
+  if (to < 0) return;
+  const uint32_t filled = (uint32_t)len - k.page.quot((uint32_t)len) * ps;
+  const uint32_t step = (gridDim.z - node_groups) * slots;
+  for (uint32_t r = (blockIdx.z - node_groups) * slots + in; r < filled; r += step) {
+    const uint8_t *src = base + ((uint64_t)(uint32_t)from * ps + r) * row_bytes;
+    uint8_t *dst = base + ((uint64_t)(uint32_t)to * ps + r) * row_bytes;
+    for (uint32_t o = lane * 16; o < row_bytes; o += lanes.d * 16)
+      store_nt16(dst + o, *reinterpret_cast<const uint4 *>(src + o));
   }
 }
 
@@ -262,11 +268,10 @@ __global__ __launch_bounds__(kCopyThreads) void k_truncate(enc_cache c, const in
 
 hipError_t launch_cache_commit(const CommitArgs &k, hipStream_t s) {
   hipLaunchKernelGGL(k_commit_plan, dim3(1), dim3(kPlanThreads), 0, s, k);
-  // slices of about 64 KiB of the most a (sequence, plane) can have to move
-  const uint64_t most = (uint64_t)(k.nodes + k.c.page_size) * k.c.row_bytes;
-  const uint64_t slices = (most + 65535) / 65536;
-  hipLaunchKernelGGL(k_commit_move, dim3(k.batch, k.c.n_planes, (uint32_t)(slices < 64 ? slices : 64)),
-                     dim3(kCopyThreads), 0, s, k);
+  const uint32_t per = k.c.row_bytes / 16, lanes = per < kCopyThreads ? per : kCopyThreads, slots = kCopyThreads / lanes;
+  const uint32_t node_groups = (k.nodes + slots - 1) / slots, copy_groups = (k.c.page_size + slots - 1) / slots;
+  hipLaunchKernelGGL(k_commit_move, dim3(k.batch, k.c.n_planes, node_groups + (copy_groups < 32 ? copy_groups : 32)),
+                     dim3(kCopyThreads), 0, s, k, FastDiv::of(lanes), slots, node_groups);
   return hipGetLastError();
 }
 

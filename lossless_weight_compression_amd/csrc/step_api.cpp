@@ -59,13 +59,14 @@ enc_status check_cache(const enc_cache *c) {
     return unsupported("n_planes above 65535, page_size above 65536, or 2^31 pages or sequences");
   if ((uint64_t)c->max_pages * c->page_size > 0x7FFFFFFFull) return unsupported("max_pages * page_size above 2^31 - 1");
   const uint64_t used = (uint64_t)c->n_pages * c->page_size;
+  if (used > 0x7FFFFFFFull) return unsupported("n_pages * page_size above 2^31 - 1");
   if (used > (1ull << 40) / c->row_bytes) return unsupported("a plane above 2^40 bytes");
   if (c->n_planes > 1 && c->plane_stride < used * c->row_bytes) return invalid("plane_stride below a plane's bytes");
   return ENC_OK;
 }
 
 struct CommitLayout {
-  uint64_t info, first, pick, total;
+  uint64_t info, first, pick, to, total;
 };
 CommitLayout commit_layout(const enc_cache *c, uint32_t batch, uint32_t nodes) {
   CommitLayout l;
@@ -74,7 +75,8 @@ CommitLayout commit_layout(const enc_cache *c, uint32_t batch, uint32_t nodes) {
   l.pick = l.first + align_up(4ull * batch, 256);
   // a sequence's rows reach at most this many pages
   const uint64_t reach = (nodes + c->page_size - 1) / c->page_size + 1;
-  l.total = l.pick + align_up(4ull * batch * reach, 256);
+  l.to = l.pick + align_up(4ull * batch * reach, 256);
+  l.total = l.to + align_up(4ull * batch * nodes, 256);
   return l;
 }
 
@@ -248,6 +250,7 @@ enc_status enc_cache_commit(const enc_cache *c, const int32_t *d_seqs, uint32_t 
   k.info = reinterpret_cast<int32_t *>(ws + l.info);
   k.first = reinterpret_cast<int32_t *>(ws + l.first);
   k.pick = reinterpret_cast<int32_t *>(ws + l.pick);
+  k.to = reinterpret_cast<int32_t *>(ws + l.to);
   return after_launch(launch_cache_commit(k, (hipStream_t)stream), (hipStream_t)stream, "enc_cache_commit");
 }
 

@@ -105,6 +105,7 @@ struct CommitArgs {
   int32_t *info;             // [batch, 4] length before, rows, page copied from (or -1), page copied to
   int32_t *first;            // [batch] rank of the sequence's first new page
   int32_t *pick;             // [pages the call may need] free pages by rank
+  int32_t *to;               // [batch, nodes] cache row of each accepted row, -1 past them
 };
 hipError_t launch_cache_commit(const CommitArgs &k, hipStream_t s);
 hipError_t launch_cache_fork(const enc_cache &c, const int32_t *src, const int32_t *dst, uint32_t pairs,
