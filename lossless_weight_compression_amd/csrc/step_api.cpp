@@ -43,6 +43,8 @@ enc_status check_attention(const enc_tree_attention_args *a) {
   if (rows > 65536) return unsupported("more than 65536 query rows share a KV head");
   if ((uint64_t)a->batch * a->kv_heads * rows > (1ull << 28)) return unsupported("batch * nodes * q_heads above 2^28");
   if ((uint64_t)a->n_pages * a->page_size > 0x7FFFFFFFull) return unsupported("n_pages * page_size above 2^31 - 1");
+  if (((uint64_t)a->max_pages * a->page_size / 32 + 16) * a->batch > 0xFFFFFFFFull)
+    return unsupported("batch * max_pages * page_size above 2^37");
   return ENC_OK;
 }
 
@@ -120,7 +122,7 @@ uint64_t enc_tree_attention_workspace_bytes(const enc_tree_attention_args *a) {
   set_error(ENC_OK, "%s", "");
   if (check_attention(a) != ENC_OK || a->batch == 0) return 0;
   const TreeAttnPlan p = plan_tree_attention(*a);
-  return p.part_bytes + p.ml_bytes;
+  return p.part_bytes + p.ml_bytes + p.share_bytes;
 }
 
 enc_status enc_tree_attention(const enc_tree_attention_args *a, void *d_ws, uint64_t ws_bytes, void *stream) {
@@ -149,7 +151,7 @@ enc_status enc_tree_attention(const enc_tree_attention_args *a, void *d_ws, uint
       a->k_new_node >> 35 || a->v_new_node >> 35)
     return unsupported("k_new or v_new strides above 32 GiB");
   const TreeAttnPlan p = plan_tree_attention(*a);
-  const uint64_t need = p.part_bytes + p.ml_bytes;
+  const uint64_t need = p.part_bytes + p.ml_bytes + p.share_bytes;
   if (need) {
     if (!d_ws || !aligned(d_ws, 16)) return invalid("workspace is NULL or not 16-byte aligned");
     if (ws_bytes < need)
@@ -167,6 +169,7 @@ enc_status enc_tree_attention(const enc_tree_attention_args *a, void *d_ws, uint
   k.mask_words = (a->nodes + 63) / 64 * 2;
   k.part = static_cast<float *>(d_ws);
   k.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(d_ws) + p.part_bytes);
+  k.shares = need ? reinterpret_cast<uint2 *>(static_cast<uint8_t *>(d_ws) + p.part_bytes + p.ml_bytes) : nullptr;
   return after_launch(launch_tree_attention(k, p, (hipStream_t)stream), (hipStream_t)stream, "enc_tree_attention");
 }
 

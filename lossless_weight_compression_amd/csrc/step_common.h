@@ -68,13 +68,14 @@ struct TreeAttnArgs {
   uint32_t mask_words;       // 32-bit mask words per node
   float *part;               // [grid_parts, kv_heads, rows, head_dim] unnormalised sums
   float *part_ml;            // [grid_parts, kv_heads, rows, 2] running maximum and sum
+  uint2 *shares;             // [batch] first part and number of parts; NULL: never more than one
 };
 struct TreeAttnPlan {
   uint32_t wide;             // rows on different waves, keys through LDS
   uint32_t units, waves;     // 16-row units a wave holds; waves of a workgroup
   uint32_t ways, unit;       // waves that take different keys; keys in a unit of work
   uint32_t row_tiles, parts, grid_parts;
-  uint64_t part_bytes, ml_bytes;
+  uint64_t part_bytes, ml_bytes, share_bytes;
 };
 TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a);
 hipError_t launch_tree_attention(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s);

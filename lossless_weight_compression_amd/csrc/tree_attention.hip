@@ -31,6 +31,7 @@
 // kernel, in order. The four waves of a workgroup hold different rows (64
 // each) or different strips, joined through LDS at the end.
 #include "step_common.h"
+#include "group_math.h"
 
 #include <type_traits>
 
@@ -124,35 +125,35 @@ __device__ __forceinline__ uint32_t units_of(const enc_tree_attention_args &a, u
   return (q.len + unit - 1) / unit + (q.live + unit - 1) / unit;
 }
 
-// BY_PART: of part `index`; else of sequence `index`.
-template <bool BY_PART>
-__device__ __forceinline__ Share share_of(const TreeAttnArgs &k, uint32_t unit, uint32_t ways, uint32_t index) {
+__device__ __forceinline__ Share share_of(const TreeAttnArgs &k, uint32_t unit, uint32_t ways, uint32_t part) {
   const enc_tree_attention_args &a = k.a;
   const uint32_t lane = threadIdx.x & 63;
-  const uint32_t mine = units_of(a, lane, unit);
-  uint64_t total = 0;
-  for (uint32_t b0 = 0; b0 < a.batch; b0 += 64) {
-    uint64_t u = b0 ? units_of(a, b0 + lane, unit) : mine;
-    for (uint32_t o = 32; o; o >>= 1) u += __shfl_xor(u, o);
-    total += u;
-  }
-  const uint64_t each = (total + k.parts - 1) / k.parts;
+  auto size_of = [&](uint32_t total) {
+    const uint32_t each = (uint32_t)(((uint64_t)total + k.parts - 1) >> 32) ? total : (total + k.parts - 1) / k.parts;
+    return max((each + ways - 1) / ways * ways, ways);
+  };
   Share s;
-  s.size = max((uint32_t)((each + ways - 1) / ways * ways), ways);
+  if (a.batch == 1) {
+    const uint32_t u = units_of(a, 0, unit);
+    s.size = size_of(u);
+    s.b = s.first = 0;
+    s.parts = max((u + s.size - 1) / s.size, 1u);
+    s.found = part < s.parts;
+    return s;
+  }
+  const uint32_t mine = units_of(a, lane, unit);
+  uint32_t total = 0;   // fits: checked on the host for the longest sequences the table holds
+  for (uint32_t b0 = 0; b0 < a.batch; b0 += 64)
+    total += __builtin_amdgcn_readlane(wave_incl_scan(b0 ? units_of(a, b0 + lane, unit) : mine), 63);
+  s.size = size_of(total);
   s.found = false;
   s.b = s.first = s.parts = 0;
   uint32_t before = 0;
   for (uint32_t b0 = 0; b0 < a.batch; b0 += 64) {
     const uint32_t u = b0 ? units_of(a, b0 + lane, unit) : mine;
     const uint32_t n = b0 + lane < a.batch ? max((u + s.size - 1) / s.size, 1u) : 0;
-    uint32_t incl = n;
-    for (uint32_t o = 1; o < 64; o <<= 1) {
-      const uint32_t t = __shfl_up(incl, o);
-      if (lane >= o) incl += t;
-    }
-    const uint32_t from = before + incl - n;
-    const uint64_t hit = BY_PART ? __ballot(n && index >= from && index < from + n)
-                                 : __ballot(b0 + lane == index);
+    const uint32_t incl = wave_incl_scan(n), from = before + incl - n;
+    const uint64_t hit = __ballot(n && part >= from && part < from + n);
     if (hit) {
       const int at = __builtin_ctzll(hit);
       s.b = b0 + at;
@@ -164,6 +165,11 @@ __device__ __forceinline__ Share share_of(const TreeAttnArgs &k, uint32_t unit, 
     before += __builtin_amdgcn_readlane(incl, 63);
   }
   return s;
+}
+
+// For the join: which parts are a sequence's.
+__device__ __forceinline__ void note_parts(const TreeAttnArgs &k, const Share &s, uint32_t part, bool one) {
+  if (k.shares && one && part == s.first && threadIdx.x == 0) k.shares[s.b] = make_uint2(s.first, s.parts);
 }
 
 // The kernel's arguments, read again where they are used: kept in scalar
@@ -208,8 +214,9 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
   // die sees all heads
   const uint32_t part = blockIdx.x / a.kv_heads, h = (blockIdx.x + part) % a.kv_heads;
   constexpr uint32_t ways = kWavesA;
-  const Share sh = share_of<true>(k, 32, ways, part);
+  const Share sh = share_of(k, 32, ways, part);
   if (!sh.found) return;
+  note_parts(k, sh, part, h == 0);
   const uint32_t b = sh.b, kw = wave;
   const Seq q = sequence_of(a, b);
   const uint32_t strips_ctx = (q.len + 31) / 32, strips = strips_ctx + (q.live + 31) / 32;
@@ -598,8 +605,9 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
   const uint32_t id8 = blockIdx.x >> 3;
   const uint32_t grp = id8 / k.row_tiles * 8 + (blockIdx.x & 7), rt = id8 % k.row_tiles;
   const uint32_t part = grp / a.kv_heads, h = (grp + part) % a.kv_heads;
-  const Share sh = share_of<true>(k, SK, 1, part);
+  const Share sh = share_of(k, SK, 1, part);
   if (!sh.found) return;
+  note_parts(k, sh, part, h == 0 && rt == 0);
   const uint32_t b = sh.b;
   const Seq q = sequence_of(a, b);
   const uint32_t ctx = (q.len + SK - 1) / SK, stages = ctx + (q.live + SK - 1) / SK;
@@ -1061,9 +1069,9 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
 }
 
 // One wave per query row: the parts' sums, brought to their common maximum
-// and added in the order of the splits (64 / LD of them side by side).
+// and added in the order of the parts (64 / LD of them side by side).
 template <typename T, uint32_t LD>
-__global__ __launch_bounds__(256) void k_tree_attention_join(TreeAttnArgs k, uint32_t unit, uint32_t ways) {
+__global__ __launch_bounds__(256) void k_tree_attention_join(TreeAttnArgs k) {
   const enc_tree_attention_args &a = k.a;
   constexpr uint32_t W = 64 / LD;
   const uint32_t lane = threadIdx.x & 63;
@@ -1071,13 +1079,13 @@ __global__ __launch_bounds__(256) void k_tree_attention_join(TreeAttnArgs k, uin
   if (item >= a.batch * a.kv_heads * k.rows) return;
   const uint32_t bh = item / k.rows, r = item - bh * k.rows;
   const uint32_t b = bh / a.kv_heads, h = bh - b * a.kv_heads;
-  const Share sh = share_of<false>(k, unit, ways, b);
-  if (sh.parts <= 1) return;   // written by its only part
+  const uint2 sh = k.shares[b];
+  if (sh.y <= 1) return;   // written by its only part
   const Seq q = sequence_of(a, b);
-  const uint32_t live = sh.parts;
+  const uint32_t live = sh.y;
   const uint32_t node = k.group.quot(r), head = h * k.group.d + (r - node * k.group.d);
 
-  const uint64_t row = ((uint64_t)sh.first * a.kv_heads + h) * k.rows + r, step = (uint64_t)a.kv_heads * k.rows;
+  const uint64_t row = ((uint64_t)sh.x * a.kv_heads + h) * k.rows + r, step = (uint64_t)a.kv_heads * k.rows;
   float m = kLowest;
   for (uint32_t s = lane; s < live; s += 64) m = fmaxf(m, k.part_ml[2 * (row + s * step)]);
   for (uint32_t o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
@@ -1153,11 +1161,11 @@ void launch_type(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
   if (!p.part_bytes) return;
   const dim3 grid((k.a.batch * k.a.kv_heads * k.rows + kWavesA - 1) / kWavesA), block(256);
   if (D <= 64)
-    hipLaunchKernelGGL((k_tree_attention_join<T, 16>), grid, block, 0, s, k, p.unit, p.ways);
+    hipLaunchKernelGGL((k_tree_attention_join<T, 16>), grid, block, 0, s, k);
   else if (D <= 128)
-    hipLaunchKernelGGL((k_tree_attention_join<T, 32>), grid, block, 0, s, k, p.unit, p.ways);
+    hipLaunchKernelGGL((k_tree_attention_join<T, 32>), grid, block, 0, s, k);
   else
-    hipLaunchKernelGGL((k_tree_attention_join<T, 64>), grid, block, 0, s, k, p.unit, p.ways);
+    hipLaunchKernelGGL((k_tree_attention_join<T, 64>), grid, block, 0, s, k);
 }
 
 }  // namespace
@@ -1201,6 +1209,7 @@ TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a) {
   const uint64_t parts = units <= p.ways ? 0 : (uint64_t)p.grid_parts * a.kv_heads * rows;
   p.part_bytes = align_up(4 * parts * a.head_dim, 256);
   p.ml_bytes = align_up(8 * parts, 256);
+  p.share_bytes = parts ? align_up(8ull * a.batch, 256) : 0;
   return p;
 }
 
