@@ -197,27 +197,32 @@ __device__ __forceinline__ uint32_t tree_bits(uint32_t b, uint32_t i, uint32_t f
 
 // DP: head_dim rounded up to what the fragments hold; EXACT: equal to it.
 // U: 16-row units of a wave.
-template <typename T, int DP, int U, bool EXACT>
+// HEADS: the four waves take four neighbouring KV heads of the same keys, so
+// rows of the cache that lie together are read together; else they take
+// different strips of one head, joined through LDS at the end.
+template <typename T, int DP, int U, bool EXACT, bool HEADS>
 __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(TreeAttnArgs k) {
   constexpr int KS = DP / 32;                   // k steps of Q K^T
   constexpr int C = DP >= 128 ? 8 : DP / 16;    // consecutive values a lane transposes
   constexpr int NH = DP / (16 * C);             // groups of 16 C values
   constexpr int NREG = U * NH * C * 4;          // accumulators a lane holds
   const enc_tree_attention_args &a = k.a;
-  __shared__ float joint[2 * (NREG + 2 * U) * 64];
+  __shared__ float joint[HEADS ? 1 : 2 * (NREG + 2 * U) * 64];
 
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t l16 = lane & 15, g4 = lane >> 4;
   const uint32_t D = a.head_dim;
 
   // neighbouring workgroups (on different dies) differ in their head, and each
   // die sees all heads
-  const uint32_t part = blockIdx.x / a.kv_heads, h = (blockIdx.x + part) % a.kv_heads;
-  constexpr uint32_t ways = kWavesA;
+  const uint32_t sets = HEADS ? a.kv_heads / kWavesA : a.kv_heads;
+  const uint32_t part = blockIdx.x / sets, set = (blockIdx.x + part) % sets;
+  const uint32_t h = HEADS ? set * kWavesA + wave : set;
+  constexpr uint32_t ways = HEADS ? 1 : kWavesA;
   const Share sh = share_of(k, 32, ways, part);
   if (!sh.found) return;
-  note_parts(k, sh, part, h == 0);
-  const uint32_t b = sh.b, kw = wave;
+  note_parts(k, sh, part, set == 0);
+  const uint32_t b = sh.b, kw = HEADS ? 0 : wave;
   const Seq q = sequence_of(a, b);
   const uint32_t strips_ctx = (q.len + 31) / 32, strips = strips_ctx + (q.live + 31) / 32;
   const uint32_t lo = (part - sh.first) * sh.size, hi = min(lo + sh.size, strips);
@@ -475,6 +480,7 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
   // ---- join the waves that hold the same rows
 #pragma unroll
   for (int u = 0; u < U; ++u) l[u] = rows_sum(l[u]);
+  if constexpr (!HEADS) {
   __syncthreads();
   for (uint32_t st = ways / 2; st; st >>= 1) {
     const uint32_t slot = kw & (st - 1);
@@ -512,6 +518,7 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
       }
     }
     __syncthreads();
+  }
   }
   if (kw != 0) return;
   const ArgsPtr g = args_again();
@@ -597,7 +604,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
   __shared__ __align__(16) uint4 ks[NB][SK * NCH], vs[NB][SK * PITCH];
   __shared__ uint32_t odd;
 
-  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t l16 = lane & 15, g4 = lane >> 4;
   const uint32_t D = a.head_dim;
   // row tiles of one (part, head) differ in 8, so they meet in one compute die's
@@ -1117,12 +1124,16 @@ __global__ __launch_bounds__(256) void k_tree_attention_join(TreeAttnArgs k) {
 }
 
 template <typename T, int DP, int U>
-void launch_unit(const TreeAttnArgs &k, hipStream_t s) {
-  const dim3 grid(k.grid_parts * k.a.kv_heads), block(256);
-  if (k.a.head_dim == DP)
-    hipLaunchKernelGGL((k_tree_attention<T, DP, U, true>), grid, block, 0, s, k);
+void launch_unit(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
+  const dim3 grid(k.grid_parts * (p.ways == 1 ? k.a.kv_heads / kWavesA : k.a.kv_heads)), block(256);
+  if (p.ways == 1 && k.a.head_dim == DP)
+    hipLaunchKernelGGL((k_tree_attention<T, DP, U, true, true>), grid, block, 0, s, k);
+  else if (p.ways == 1)
+    hipLaunchKernelGGL((k_tree_attention<T, DP, U, false, true>), grid, block, 0, s, k);
+  else if (k.a.head_dim == DP)
+    hipLaunchKernelGGL((k_tree_attention<T, DP, U, true, false>), grid, block, 0, s, k);
   else
-    hipLaunchKernelGGL((k_tree_attention<T, DP, U, false>), grid, block, 0, s, k);
+    hipLaunchKernelGGL((k_tree_attention<T, DP, U, false, false>), grid, block, 0, s, k);
 }
 
 template <typename T, int DP, int U, int W>
@@ -1143,9 +1154,9 @@ void launch_dim(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
       launch_wide<T, DP, 2, 8>(k, s);
     }
   } else if (p.units == 1) {
-    launch_unit<T, DP, 1>(k, s);
+    launch_unit<T, DP, 1>(k, p, s);
   } else if constexpr (DP <= 128) {
-    launch_unit<T, DP, 2>(k, s);
+    launch_unit<T, DP, 2>(k, p, s);
   }
 }
 
@@ -1182,7 +1193,10 @@ TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a) {
   if (rows <= (large ? 16u : 32u)) {
     p.wide = 0;
     p.units = rows <= 16 ? 1 : 2;
-    p.waves = p.ways = 4;
+    p.waves = 4;
+    // four heads to a workgroup where that leaves two waves to a compute unit
+    // before any history is split
+    p.ways = a.kv_heads % 4 == 0 && (uint64_t)a.batch * a.kv_heads >= 512 ? 1 : 4;
     p.unit = 32;
     p.row_tiles = 1;
     fill = 2048;
