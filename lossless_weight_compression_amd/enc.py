@@ -186,19 +186,22 @@ def _check(status):
 _raw_stream = None
 
 
+def _current_stream(index):
+    """Handle of device `index`'s current stream: where torch offers it, the
+    handle alone (a Stream object costs as much as a launch: 2.6 against 0.1 us)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if _raw_stream is None:
+            _raw_stream = lambda i: torch.cuda.current_stream(i).cuda_stream  # noqa: E731
+    return _raw_stream(index)
+
+
 def _stream(stream):
     if stream is None:
-        global _raw_stream
-        if _raw_stream is None:
-            import torch
-            # the handle alone, where torch offers it: a Stream object costs as
-            # much as a kernel launch (2.6 us against 0.1 us)
-            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-            if raw is not None:
-                _raw_stream = lambda: raw(torch.cuda.current_device())  # noqa: E731
-            else:
-                _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
-        return ctypes.c_void_p(_raw_stream())
+        import torch
+        return ctypes.c_void_p(_current_stream(torch.cuda.current_device()))
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -584,6 +587,18 @@ def enc_stream_probe(src, dst, items_per_thread=1, threads_per_workgroup=256, st
 ENC_TREE_MAX_NODES = 256
 ENC_ROPE_ADJACENT, ENC_QK_NO_NORM = 1, 2
 _codes = {}
+_I32 = _I64 = _F32 = _BF16 = _current_device = None
+
+
+def _load_types():
+    """What the calls below need of torch, looked up once."""
+    global _I32, _I64, _F32, _BF16, _current_device
+    import torch
+    _I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
+    _current_device = torch.cuda.current_device
+    _codes.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+
+
 # the argument structs in one go (field by field costs about 0.1 us each)
 _QK_PACK = struct.Struct("=22Q10IfI").pack
 _ATTN_PACK = struct.Struct("=27Q10IfI").pack
@@ -593,32 +608,17 @@ _VERIFY_PACK = struct.Struct("=13Q4I").pack
 def _code(dtype):
     """Header element type of a floating torch type."""
     if not _codes:
-        import torch
-        _codes.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+        _load_types()
     code = _codes.get(dtype)
     if code is None:
         raise TypeError("%s: values must be bfloat16, float16 or float32" % dtype)
     return code
 
 
-class _Here:
-    """Allocations for the current stream need no context."""
-
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_here = _Here()
-
-
 def _on(stream):
-    """Context in which torch allocates for `stream`, so that memory of a
-    tensor made in a call is not handed out again before the call's work."""
-    if stream is None:
-        return _here
+    """Context in which torch allocates for `stream` (not the current one), so
+    that memory of a tensor made in a call is not handed out again before the
+    call's work."""
     import torch
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
@@ -653,13 +653,21 @@ def _scratch(ws, index):
 
 def _device_of(t):
     """Index of the CUDA device a call works on: the current one, and its tensors'."""
-    import torch
+    if _I32 is None:
+        _load_types()
     index = t.get_device()
     if index < 0:
         raise ValueError("expected CUDA tensors")
-    if index != torch.cuda.current_device():
-        raise ValueError("tensors are on %s, the current device is %d" % (t.device, torch.cuda.current_device()))
+    if index != _current_device():
+        raise ValueError("tensors are on %s, the current device is %d" % (t.device, _current_device()))
     return index
+
+
+def _handle(stream, index):
+    """A stream argument as the C calls take it."""
+    if stream is None:
+        return _current_stream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def enc_qk_norm_rope(q, k, v, positions, table, q_weight=None, k_weight=None, eps=1e-6, adjacent=False, norm=True,
@@ -670,26 +678,32 @@ def enc_qk_norm_rope(q, k, v, positions, table, q_weight=None, k_weight=None, ep
     fp32 [max_pos, rot_dim], rot_dim/2 cosines then as many sines (None: no
     rotation). out: (q, k, v) tensors, allocated in out_dtype (bfloat16) if
     None; an out tensor may be its input. Returns (q, k, v)."""
-    import torch
     device = _device_of(q)
     tokens, q_heads, dim = shape = q.shape
     kv_shape = (tokens, k.shape[1], dim)
     qs = _values(q, "q", q.dtype, shape, device)
     ks = _values(k, "k", q.dtype, kv_shape, device)
     if out is None:
-        dtype = out_dtype or torch.bfloat16
-        with _on(stream):
+        dtype = out_dtype or _BF16
+        if stream is not None:
+            with _on(stream):
+                qo, ko = q.new_empty(shape, dtype=dtype), q.new_empty(kv_shape, dtype=dtype)
+                vo = q.new_empty(kv_shape, dtype=dtype) if v is not None else None
+        else:
             qo, ko = q.new_empty(shape, dtype=dtype), q.new_empty(kv_shape, dtype=dtype)
             vo = q.new_empty(kv_shape, dtype=dtype) if v is not None else None
+        qos, kos = (q_heads * dim, dim), (kv_shape[1] * dim, dim)
+        vos = kos
     else:
         qo, ko, vo = out
-    dtype = qo.dtype
-    qos = _values(qo, "q output", dtype, shape, device)
-    kos = _values(ko, "k output", dtype, kv_shape, device)
-    vs = vos = (0, 0)
+        dtype = qo.dtype
+        qos = _values(qo, "q output", dtype, shape, device)
+        kos = _values(ko, "k output", dtype, kv_shape, device)
+        vos = _values(vo, "v output", dtype, kv_shape, device) if v is not None else (0, 0)
+    vs = (0, 0)
     vp = vop = 0
     if v is not None:
-        vs, vos = _values(v, "v", q.dtype, kv_shape, device), _values(vo, "v output", dtype, kv_shape, device)
+        vs = _values(v, "v", q.dtype, kv_shape, device)
         vp, vop = v.data_ptr(), vo.data_ptr()
     qw = kw = tp = pp = max_pos = rot = 0
     w_code = FP32
@@ -700,15 +714,15 @@ def enc_qk_norm_rope(q, k, v, positions, table, q_weight=None, k_weight=None, ep
         if q_weight is not None and q_weight.dtype is not k_weight.dtype:
             raise TypeError("the weights must have one type")
     if table is not None:
-        pp, tp = _plain(positions, "positions", torch.int32, (tokens,), device), _plain(table, "table", torch.float32, None,
-                                                                                        device)
+        pp = _plain(positions, "positions", _I32, (tokens,), device)
+        tp = _plain(table, "table", _F32, None, device)
         max_pos, rot = table.shape
     flags = (ENC_ROPE_ADJACENT if adjacent else 0) | (0 if norm else ENC_QK_NO_NORM)
     a = EncQkArgs.from_buffer_copy(_QK_PACK(
         q.data_ptr(), k.data_ptr(), vp, qo.data_ptr(), ko.data_ptr(), vop, qw, kw, pp, tp,
         qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], qos[0], qos[1], kos[0], kos[1], vos[0], vos[1],
         tokens, q_heads, kv_shape[1], dim, rot, max_pos, _code(q.dtype), _code(dtype), w_code, flags, eps, 0))
-    _check(lib().enc_qk_norm_rope(ctypes.byref(a), _stream(stream)))
+    _check(lib().enc_qk_norm_rope(ctypes.byref(a), _handle(stream, device)))
     return qo, ko, vo
 
 
@@ -735,7 +749,6 @@ def enc_tree_attention(q, k_new, v_new, k_cache, v_cache, table, lens, mask=None
     for nodes j <= i; seqs: int32 [batch] rows of the table, or None; nodes:
     int32 [batch] live nodes, or None. scale: 1 / sqrt(head_dim) if None.
     Returns (out, lse or None)."""
-    import torch
     device = _device_of(q)
     dtype = q.dtype
     batch, n, q_heads, dim = shape = q.shape
@@ -747,20 +760,22 @@ def enc_tree_attention(q, k_new, v_new, k_cache, v_cache, table, lens, mask=None
     cs = _values(k_cache, "k_cache", dtype, (pages, page, kv_heads, dim), device)
     if _values(v_cache, "v_cache", dtype, k_cache.shape, device) != cs:
         raise ValueError("k_cache and v_cache must have the same strides")
-    tp = _plain(table, "table", torch.int32, None, device)
+    tp = _plain(table, "table", _I32, None, device)
     max_seqs, max_pages = table.shape
-    lp = _plain(lens, "lens", torch.int32, (max_seqs,), device)
-    mp = _plain(mask, "mask", torch.int64, (batch, n, (n + 63) // 64), device) if mask is not None else 0
-    sp = _plain(seqs, "seqs", torch.int32, (batch,), device) if seqs is not None else 0
-    np_ = _plain(nodes, "nodes", torch.int32, (batch,), device) if nodes is not None else 0
-    lse = None
-    with _on(stream):
-        if out is None:
-            out = q.new_empty(shape)
-        if return_lse:
-            lse = q.new_empty((batch, n, q_heads), dtype=torch.float32)
-        if ws is None:
-            ws = tree_attention_workspace(q, k_new, table, k_cache)
+    lp = _plain(lens, "lens", _I32, (max_seqs,), device)
+    mp = _plain(mask, "mask", _I64, (batch, n, (n + 63) // 64), device) if mask is not None else 0
+    sp = _plain(seqs, "seqs", _I32, (batch,), device) if seqs is not None else 0
+    np_ = _plain(nodes, "nodes", _I32, (batch,), device) if nodes is not None else 0
+    def room():
+        return (q.new_empty(shape) if out is None else out,
+                q.new_empty((batch, n, q_heads), dtype=_F32) if return_lse else None,
+                tree_attention_workspace(q, k_new, table, k_cache) if ws is None else ws)
+
+    if stream is None:
+        out, lse, ws = room()
+    else:
+        with _on(stream):
+            out, lse, ws = room()
     os = _values(out, "out", dtype, shape, device)
     a = EncTreeAttentionArgs.from_buffer_copy(_ATTN_PACK(
         q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
@@ -768,7 +783,7 @@ def enc_tree_attention(q, k_new, v_new, k_cache, v_cache, table, lens, mask=None
         qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], cs[0], cs[1], cs[2], os[0], os[1], os[2],
         batch, n, q_heads, kv_heads, dim, _code(dtype), pages, page, max_pages, max_seqs,
         dim ** -0.5 if scale is None else scale, 0))
-    _check(lib().enc_tree_attention(ctypes.byref(a), *_scratch(ws, device), _stream(stream)))
+    _check(lib().enc_tree_attention(ctypes.byref(a), *_scratch(ws, device), _handle(stream, device)))
     return out, lse
 
 
@@ -790,28 +805,31 @@ def enc_verify_tree(parents, tokens, target, draft, u, nodes=None, ws=None, stre
     target, draft (or None): [batch, nodes, vocab] probabilities of one type;
     u: fp32 [batch, nodes] random numbers in [0, 1): u[:, i] decides on node i,
     u[:, 0] draws the next token. Returns (path, count, token), int32."""
-    import torch
     device = _device_of(tokens)
     batch, n = shape = tokens.shape
     vocab = target.shape[2]
     dtype = target.dtype
-    pp = _plain(parents, "parents", torch.int32, shape, device)
-    xp = _plain(tokens, "tokens", torch.int32, shape, device)
-    up = _plain(u, "u", torch.float32, shape, device)
+    pp = _plain(parents, "parents", _I32, shape, device)
+    xp = _plain(tokens, "tokens", _I32, shape, device)
+    up = _plain(u, "u", _F32, shape, device)
     ts = _values(target, "target", dtype, (batch, n, vocab), device)
     ds, dp = (0, 0), 0
     if draft is not None:
         ds, dp = _values(draft, "draft", dtype, (batch, n, vocab), device), draft.data_ptr()
-    np_ = _plain(nodes, "nodes", torch.int32, (batch,), device) if nodes is not None else 0
-    with _on(stream):
-        path = tokens.new_empty(shape)
-        count, token = tokens.new_empty(batch), tokens.new_empty(batch)
-        if ws is None:
-            ws = verify_tree_workspace(tokens, target)
+    np_ = _plain(nodes, "nodes", _I32, (batch,), device) if nodes is not None else 0
+    def room():
+        return (tokens.new_empty(shape), tokens.new_empty(batch), tokens.new_empty(batch),
+                verify_tree_workspace(tokens, target) if ws is None else ws)
+
+    if stream is None:
+        path, count, token, ws = room()
+    else:
+        with _on(stream):
+            path, count, token, ws = room()
     a = EncVerifyArgs.from_buffer_copy(_VERIFY_PACK(
         pp, xp, target.data_ptr(), dp, up, np_, path.data_ptr(), count.data_ptr(), token.data_ptr(),
         ts[0], ts[1], ds[0], ds[1], batch, n, vocab, _code(dtype)))
-    _check(lib().enc_verify_tree(ctypes.byref(a), *_scratch(ws, device), _stream(stream)))
+    _check(lib().enc_verify_tree(ctypes.byref(a), *_scratch(ws, device), _handle(stream, device)))
     return path, count, token
 
 
@@ -833,15 +851,15 @@ class Cache:
         size = data.element_size()
         c = EncCache()
         c.d_data = data.data_ptr()
-        c.d_table = _plain(table, "table", torch.int32, None, device)
-        c.d_lens = _plain(lens, "lens", torch.int32, (table.shape[0],), device)
-        c.d_refs = _plain(refs, "refs", torch.int32, (pages,), device)
+        c.d_table = _plain(table, "table", _I32, None, device)
+        c.d_lens = _plain(lens, "lens", _I32, (table.shape[0],), device)
+        c.d_refs = _plain(refs, "refs", _I32, (pages,), device)
         c.plane_stride = st[0] * size
         c.n_planes, c.n_pages, c.page_size, c.row_bytes = planes, pages, page, row * size
         c.max_seqs, c.max_pages = table.shape
         self.c, self.data, self.table, self.lens, self.refs = c, data, table, lens, refs
         self.row_shape, self.planes = tuple(data.shape[3:]), planes
-        self.status = torch.zeros(1, dtype=torch.int32, device=data.device)
+        self.status = torch.zeros(1, dtype=_I32, device=data.device)
         self.ref = ctypes.byref(c)
 
     @classmethod
@@ -868,7 +886,6 @@ def enc_cache_commit(cache, seqs, draft, path, count, ws=None, stream=None):
     """Append rows path[b, :count[b]] of draft [planes, batch, nodes, ...] to
     sequence seqs[b] of the cache. Returns cache.status (on the device: 0, or
     why nothing was changed)."""
-    import torch
     device = _device_of(cache.data)
     batch, nodes = shape = path.shape
     if draft.dtype is not cache.data.dtype or draft.get_device() != device:
@@ -879,32 +896,33 @@ def enc_cache_commit(cache, seqs, draft, path, count, ws=None, stream=None):
         raise ValueError("a sequence's draft rows must be contiguous")
     st, size = draft.stride(), draft.element_size()
     if ws is None:
-        with _on(stream):
+        if stream is None:
             ws = cache_workspace(cache, path)
+        else:
+            with _on(stream):
+                ws = cache_workspace(cache, path)
     _check(lib().enc_cache_commit(
-        cache.ref, _plain(seqs, "seqs", torch.int32, (batch,), device), batch, draft.data_ptr(),
-        st[0] * size, st[1] * size, _plain(path, "path", torch.int32, shape, device),
-        _plain(count, "count", torch.int32, (batch,), device), nodes, cache.status.data_ptr(),
-        *_scratch(ws, device), _stream(stream)))
+        cache.ref, _plain(seqs, "seqs", _I32, (batch,), device), batch, draft.data_ptr(),
+        st[0] * size, st[1] * size, _plain(path, "path", _I32, shape, device),
+        _plain(count, "count", _I32, (batch,), device), nodes, cache.status.data_ptr(),
+        *_scratch(ws, device), _handle(stream, device)))
     return cache.status
 
 
 def enc_cache_fork(cache, src, dst, stream=None):
     """Sequence dst[i] lets go of its pages and shares those of src[i]."""
-    import torch
     device = _device_of(cache.data)
     _check(lib().enc_cache_fork(
-        cache.ref, _plain(src, "src", torch.int32, (src.numel(),), device),
-        _plain(dst, "dst", torch.int32, src.shape, device), src.shape[0], _stream(stream)))
+        cache.ref, _plain(src, "src", _I32, (src.numel(),), device),
+        _plain(dst, "dst", _I32, src.shape, device), src.shape[0], _handle(stream, device)))
 
 
 def enc_cache_truncate(cache, seqs, lens, stream=None):
     """Cut sequence seqs[i] to lens[i] tokens and free the pages past its end."""
-    import torch
     device = _device_of(cache.data)
     _check(lib().enc_cache_truncate(
-        cache.ref, _plain(seqs, "seqs", torch.int32, (seqs.numel(),), device),
-        _plain(lens, "lens", torch.int32, seqs.shape, device), seqs.shape[0], _stream(stream)))
+        cache.ref, _plain(seqs, "seqs", _I32, (seqs.numel(),), device),
+        _plain(lens, "lens", _I32, seqs.shape, device), seqs.shape[0], _handle(stream, device)))
 
 
 def enc_status_string(status):
