@@ -1075,52 +1075,67 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
   }
 }
 
-// One wave per query row: the parts' sums, brought to their common maximum
-// and added in the order of the parts (64 / LD of them side by side).
-template <typename T, uint32_t LD>
+// One query row to WAVES waves: the parts' sums, brought to their common
+// maximum and added in a fixed order, WAVES 64 / LD of them side by side. The
+// loads of a part do not depend on another's, so many are in flight.
+template <typename T, uint32_t LD, uint32_t WAVES>
 __global__ __launch_bounds__(256) void k_tree_attention_join(TreeAttnArgs k) {
   const enc_tree_attention_args &a = k.a;
-  constexpr uint32_t W = 64 / LD;
-  const uint32_t lane = threadIdx.x & 63;
-  const uint32_t item = blockIdx.x * kWavesA + (threadIdx.x >> 6);
+  constexpr uint32_t W = WAVES * 64 / LD;
+  __shared__ float side[WAVES == 1 ? 1 : 4 * 5 * 64];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t item = WAVES == 1 ? blockIdx.x * kWavesA + wave : blockIdx.x;
   if (item >= a.batch * a.kv_heads * k.rows) return;
   const uint32_t bh = item / k.rows, r = item - bh * k.rows;
   const uint32_t b = bh / a.kv_heads, h = bh - b * a.kv_heads;
   const uint2 sh = k.shares[b];
   if (sh.y <= 1) return;   // written by its only part
   const Seq q = sequence_of(a, b);
-  const uint32_t live = sh.y;
+  const uint32_t parts = sh.y;
   const uint32_t node = k.group.quot(r), head = h * k.group.d + (r - node * k.group.d);
 
   const uint64_t row = ((uint64_t)sh.x * a.kv_heads + h) * k.rows + r, step = (uint64_t)a.kv_heads * k.rows;
+  const float2 *ml = reinterpret_cast<const float2 *>(k.part_ml) + row;
   float m = kLowest;
-  for (uint32_t s = lane; s < live; s += 64) m = fmaxf(m, k.part_ml[2 * (row + s * step)]);
+  for (uint32_t s = lane; s < parts; s += 64) m = fmaxf(m, ml[s * step].x);
   for (uint32_t o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  const uint32_t way = lane / LD, d = lane % LD * 4;
+  const uint32_t way = (WAVES == 1 ? 0 : wave * (64 / LD)) + lane / LD, d = lane % LD * 4;
+  const float *sums = k.part + row * a.head_dim + (d < a.head_dim ? d : 0);
   float l = 0.f;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (uint32_t s = way; s < live; s += W) {
-    const uint64_t at = row + s * step;
-    const float w = exp_of(k.part_ml[2 * at] - m);
-    l += w * k.part_ml[2 * at + 1];
-    if (d < a.head_dim) acc += *reinterpret_cast<const f32x4 *>(k.part + at * a.head_dim + d) * w;
+#pragma unroll 8
+  for (uint32_t s = way; s < parts; s += W) {
+    const float2 part = ml[s * step];
+    const f32x4 o = *reinterpret_cast<const f32x4 *>(sums + s * step * a.head_dim);
+    const float w = exp_of(part.x - m);
+    l += w * part.y;
+    acc += o * w;
   }
   for (uint32_t o = 32; o >= LD; o >>= 1) {
     l += __shfl_xor(l, o);
     for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], o);
   }
+  if constexpr (WAVES > 1) {
+    float *mine = side + wave * 5 * 64 + lane;
+    mine[0] = l;
+    for (int e = 0; e < 4; ++e) mine[64 * (e + 1)] = acc[e];
+    __syncthreads();
+    if (wave != 0) return;
+    for (uint32_t w = 1; w < WAVES; ++w) {
+      l += side[w * 5 * 64 + lane];
+      for (int e = 0; e < 4; ++e) acc[e] += side[w * 5 * 64 + 64 * (e + 1) + lane];
+    }
+  }
   const bool any = node < q.live && l != 0.f;
   const float inv = any ? 1.0f / l : 0.f;
-  if (way == 0 && d < a.head_dim) {
+  if (lane < LD && d < a.head_dim) {
     T *dst = static_cast<T *>(a.d_out) + b * a.out_batch + node * a.out_node + head * a.out_head + d;
     const uint2 w = any ? make_uint2(pack2<T>(acc[0] * inv, acc[1] * inv), pack2<T>(acc[2] * inv, acc[3] * inv))
                         : make_uint2(0u, 0u);
     *reinterpret_cast<uint2 *>(dst) = w;
   }
   if (a.d_lse && lane == 0)
-    a.d_lse[((uint64_t)b * a.nodes + node) * a.q_heads + head] =
-        any ? m + __log2f(l) * kLn2 : -__builtin_inff();
+    a.d_lse[((uint64_t)b * a.nodes + node) * a.q_heads + head] = any ? m + __log2f(l) * kLn2 : -__builtin_inff();
 }
 
 template <typename T, int DP, int U>
@@ -1160,6 +1175,16 @@ void launch_dim(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
   }
 }
 
+// Four waves to a row while the rows alone do not fill the device.
+template <typename T, uint32_t LD>
+void launch_join(const TreeAttnArgs &k, hipStream_t s) {
+  const uint32_t rows = k.a.batch * k.a.kv_heads * k.rows;
+  if (rows <= 4096)
+    hipLaunchKernelGGL((k_tree_attention_join<T, LD, 4>), dim3(rows), dim3(256), 0, s, k);
+  else
+    hipLaunchKernelGGL((k_tree_attention_join<T, LD, 1>), dim3((rows + kWavesA - 1) / kWavesA), dim3(256), 0, s, k);
+}
+
 template <typename T>
 void launch_type(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
   const uint32_t D = k.a.head_dim;
@@ -1170,13 +1195,12 @@ void launch_type(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
   else
     launch_dim<T, 256>(k, p, s);
   if (!p.part_bytes) return;
-  const dim3 grid((k.a.batch * k.a.kv_heads * k.rows + kWavesA - 1) / kWavesA), block(256);
   if (D <= 64)
-    hipLaunchKernelGGL((k_tree_attention_join<T, 16>), grid, block, 0, s, k);
+    launch_join<T, 16>(k, s);
   else if (D <= 128)
-    hipLaunchKernelGGL((k_tree_attention_join<T, 32>), grid, block, 0, s, k);
+    launch_join<T, 32>(k, s);
   else
-    hipLaunchKernelGGL((k_tree_attention_join<T, 64>), grid, block, 0, s, k);
+    launch_join<T, 64>(k, s);
 }
 
 }  // namespace
@@ -1199,7 +1223,8 @@ TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a) {
     p.ways = a.kv_heads % 4 == 0 && (uint64_t)a.batch * a.kv_heads >= 512 ? 1 : 4;
     p.unit = 32;
     p.row_tiles = 1;
-    fill = 2048;
+    // workgroups that 256 compute units hold at once, by the registers of a wave
+    fill = 256 * (a.head_dim <= 64 ? 5 - p.units : large ? 1 : 4 - p.units) * (4 / p.ways);
   } else {
     p.wide = 1;
     p.units = large || rows <= 128 ? 1 : 2;
