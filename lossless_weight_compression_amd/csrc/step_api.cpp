@@ -166,6 +166,7 @@ enc_status enc_tree_attention(const enc_tree_attention_args *a, void *d_ws, uint
   k.row_tiles = p.row_tiles;
   k.parts = p.parts;
   k.grid_parts = p.grid_parts;
+  k.least = p.least;
   k.mask_words = (a->nodes + 63) / 64 * 2;
   k.part = static_cast<float *>(d_ws);
   k.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(d_ws) + p.part_bytes);

@@ -65,6 +65,7 @@ struct TreeAttnArgs {
   uint32_t row_tiles;        // tiles of rows, each one workgroup's
   uint32_t parts;            // equal parts the call's keys are cut into
   uint32_t grid_parts;       // and the most there are, with short last ones
+  uint32_t least;            // units in the smallest part
   uint32_t mask_words;       // 32-bit mask words per node
   float *part;               // [grid_parts, kv_heads, rows, head_dim] unnormalised sums
   float *part_ml;            // [grid_parts, kv_heads, rows, 2] running maximum and sum
@@ -74,7 +75,7 @@ struct TreeAttnPlan {
   uint32_t wide;             // rows on different waves, keys through LDS
   uint32_t units, waves;     // 16-row units a wave holds; waves of a workgroup
   uint32_t ways, unit;       // waves that take different keys; keys in a unit of work
-  uint32_t row_tiles, parts, grid_parts;
+  uint32_t row_tiles, parts, grid_parts, least;
   uint64_t part_bytes, ml_bytes, share_bytes;
 };
 TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a);

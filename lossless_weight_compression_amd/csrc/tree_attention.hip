@@ -130,7 +130,7 @@ __device__ __forceinline__ Share share_of(const TreeAttnArgs &k, uint32_t unit, 
   const uint32_t lane = threadIdx.x & 63;
   auto size_of = [&](uint32_t total) {
     const uint32_t each = (uint32_t)(((uint64_t)total + k.parts - 1) >> 32) ? total : (total + k.parts - 1) / k.parts;
-    return max((each + ways - 1) / ways * ways, ways);
+    return max((each + ways - 1) / ways * ways, k.least);
   };
   Share s;
   if (a.batch == 1) {
@@ -1244,8 +1244,11 @@ TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a) {
   const uint64_t most = (units + p.ways - 1) / p.ways * a.batch;
   p.parts = (uint32_t)(want < most ? want : most);
   p.grid_parts = p.parts + a.batch;
-  // a sequence never has two parts if all its units fit one wave each
-  const uint64_t parts = units <= p.ways ? 0 : (uint64_t)p.grid_parts * a.kv_heads * rows;
+  // a part is at least a round of the ways; where no history is longer than
+  // three rounds, one part without a join is quicker (300 tokens, 32 sequences:
+  // 11.5 against 15.2 us; at 1000 tokens the join wins, 10.7 against 18.7)
+  p.least = units <= 3 * p.ways ? 3 * p.ways : p.ways;
+  const uint64_t parts = units <= p.least ? 0 : (uint64_t)p.grid_parts * a.kv_heads * rows;
   p.part_bytes = align_up(4 * parts * a.head_dim, 256);
   p.ml_bytes = align_up(8 * parts, 256);
   p.share_bytes = parts ? align_up(8ull * a.batch, 256) : 0;
