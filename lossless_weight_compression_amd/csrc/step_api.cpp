@@ -41,7 +41,9 @@ enc_status check_attention(const enc_tree_attention_args *a) {
   if ((uint64_t)a->max_pages * a->page_size > 0x7FFFFFFFull) return unsupported("max_pages * page_size above 2^31 - 1");
   const uint64_t rows = (uint64_t)a->nodes * (a->q_heads / a->kv_heads);
   if (rows > 65536) return unsupported("more than 65536 query rows share a KV head");
-  if ((uint64_t)a->batch * a->kv_heads * rows > (1ull << 28)) return unsupported("batch * nodes * q_heads above 2^28");
+  // a grid holds fewer than 2^32 threads
+  if ((uint64_t)a->batch * a->kv_heads * rows > (1ull << 25) || (uint64_t)a->batch * a->kv_heads > (1ull << 23))
+    return unsupported("batch * nodes * q_heads above 2^25, or batch * kv_heads above 2^23");
   if ((uint64_t)a->n_pages * a->page_size > 0x7FFFFFFFull) return unsupported("n_pages * page_size above 2^31 - 1");
   if (((uint64_t)a->max_pages * a->page_size / 32 + 16) * a->batch > 0xFFFFFFFFull)
     return unsupported("batch * max_pages * page_size above 2^37");
@@ -109,7 +111,7 @@ enc_status enc_qk_norm_rope(const enc_qk_args *a, void *stream) {
     return invalid("rotation needs positions and a table");
   if (a->max_pos > 0x7FFFFFFFu) return unsupported("max_pos above 2^31 - 1");
   const uint64_t heads = (uint64_t)a->q_heads + a->kv_heads * (a->d_v ? 2ull : 1ull);
-  if (heads > 65536 || heads * a->tokens > 0x7FFFFFFFull) return unsupported("tokens * heads above 2^31 - 1");
+  if (heads > 65536 || heads * a->tokens > 0x7FFFFFFFull) return unsupported("more than 65536 heads, or tokens * heads above 2^31 - 1");
   QkKernelArgs k;
   k.a = *a;
   k.heads = (uint32_t)heads;
@@ -197,6 +199,8 @@ enc_status enc_verify_tree(const enc_verify_args *a, void *d_ws, uint64_t ws_byt
       !aligned(a->d_token, 4))
     return invalid("a misaligned array");
   const VerifyPlan p = plan_verify_tree(a->batch, a->vocab);
+  if ((a->batch + 7ull) / 8 * 8 * p.groups > (1u << 21))   // a grid holds fewer than 2^32 threads
+    return unsupported("batch * vocab: more than 2^21 workgroups");
   const uint64_t need = p.totals_bytes + p.done_bytes;
   if (!d_ws || !aligned(d_ws, 16)) return invalid("workspace is NULL or not 16-byte aligned");
   if (ws_bytes < need)

@@ -55,6 +55,7 @@ struct QkKernelArgs {
   uint32_t heads;      // that a token has: q, k and, if given, v
   uint32_t vec;        // angles in aligned runs of 4
   FastDiv blocks;      // workgroups to a token
+  uint32_t token0;     // this launch's first
 };
 hipError_t launch_qk_norm_rope(const QkKernelArgs &k, hipStream_t s);
 

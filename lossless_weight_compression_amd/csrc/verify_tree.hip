@@ -16,7 +16,9 @@
 // sums of its waves' segments and takes those of the others. A workgroup that
 // waits too long for the others (which may not have been scheduled) computes
 // all segments by itself from then on, so no wait is unbounded. The
-// workgroup whose segment holds the drawn token finds it.
+// workgroup whose segment holds the drawn token finds it. A sequence's
+// workgroups are on one compute die, so that the words they exchange meet in
+// its L2.
 #include "step_common.h"
 
 #include <cstdlib>

@@ -144,3 +144,17 @@ def test_another_stream_and_empty(E):
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
     E.enc_qk_norm_rope(x[:0], x[:0], x[:0], pos[:0], table)
+
+
+def test_more_tokens_than_one_grid_holds(E):
+    say("2^24 + 5 tokens of three heads of 8 values")
+    tokens, big = 2 ** 24 + 5, 2 ** 23
+    q = torch.randn(tokens, 2, 8, device="cuda", dtype=torch.bfloat16)
+    k = torch.randn(tokens, 1, 8, device="cuda", dtype=torch.bfloat16)
+    table = torch.from_numpy(rope_table(64, 8)).cuda()
+    pos = (torch.arange(tokens, device="cuda") % 64).int()
+    qo, ko, _ = E.enc_qk_norm_rope(q, k, None, pos, table)
+    for at in (0, big - 2, 2 * big - 2, tokens - 5):
+        part = slice(at, at + 5)
+        one_q, one_k, _ = E.enc_qk_norm_rope(q[part], k[part], None, pos[part], table)
+        assert torch.equal(qo[part], one_q) and torch.equal(ko[part], one_k)

@@ -199,3 +199,16 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(ValueError):
         enc.enc_verify_tree(torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32),
                             torch.zeros(1, 1, 4), None, torch.zeros(1, 1))
+
+
+@pytest.mark.parametrize("kw", [dict(batch=2 ** 23, nodes=1, q_heads=8, kv_heads=2), dict(batch=2 ** 24, nodes=1, q_heads=1, kv_heads=1)])
+def test_attention_grids_above_32_bits_of_threads(L, kw):
+    a = attention(max_pages=1, **kw)
+    assert L.enc_tree_attention(ctypes.byref(a), P, 1 << 40, None) == -2
+    assert L.enc_tree_attention_workspace_bytes(ctypes.byref(a)) == 0
+
+
+def test_verify_grids_above_32_bits_of_threads(L):
+    a = verify(batch=2 ** 18, vocab=2 ** 20, target_batch=0, target_node=0)
+    assert L.enc_verify_tree(ctypes.byref(a), P, 1 << 40, None) == -2
+    assert enc.enc_last_error()
