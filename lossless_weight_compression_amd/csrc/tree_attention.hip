@@ -2,34 +2,46 @@
 // the tree itself (enc_tree_attention).
 //
 // One pass over the keys with a running maximum m and sum l per query row:
-// o = sum_j e^(s_j - m) v_j / l, s_j = scale q.k_j. The query rows
-// that share a KV head (nodes x heads of its group) are one matrix, so every
-// key and value is read once for all of them: HBM traffic of the cache is the
-// bound, until some 200 rows share a KV head.
+// o = sum_j e^(s_j - m) v_j / l, s_j = scale q.k_j. The query rows that share a
+// KV head (nodes x heads of its group) are one matrix, so every key and value
+// is read once for all of them: HBM traffic of the cache is the bound, until
+// some 200 rows share a KV head.
 //
-// Nothing of K or V passes through LDS. A wave takes strips of 32 keys and
-// computes S^T = K Q^T and O^T += V^T P^T with v_mfma 16x16x32:
-//  * K: lane l holds 8 consecutive values of key l % 16, so fragments are
-//    loaded from the rows as they lie, 16 bytes a lane.
-//  * S^T leaves lane l with keys 4 (l / 16) + i of query row l % 16. The sum
-//    over keys in P V may run in any order, so key 16 t + 4 g + i is made
-//    contraction index 8 g + 4 t + i: then these registers, rounded, are the
-//    P^T fragment, with no exchange between lanes.
-//  * V: lane l loads, of its group's 8 keys, values (l % 16) C .. + C - 1
-//    (C = 8 for 128 values: whole rows per 16 lanes) and transposes them in
-//    registers, one byte permute per output dword. Row m of V^T fragment f
-//    then stands for value m C + f, and lane l's accumulators hold runs of
-//    C consecutive values of its row, stored 16 bytes at a time.
-//  * m and l belong to the lane's own query row; rescaling needs no exchange.
-// P is rounded to the values' type (its relative error, 2^-9 for BF16, is
-// that of the result's own rounding); sums, m, l and o are fp32. A row's m
-// only moves when a strip exceeds it by more than 8 (a factor of 2^8, far
-// inside fp32 and both 16-bit ranges), which makes rescaling rare.
+// Both kernels compute S^T = K Q^T and O^T += V^T P^T with v_mfma 16x16x32 on
+// strips of 32 keys. S^T leaves lane l with keys 4 (l / 16) + i of query row
+// l % 16. The sum over keys in P V may run in any order, so key 16 t + 4 g + i
+// is made contraction index 8 g + 4 t + i: these registers, rounded, are then
+// the P^T fragment, with no exchange between lanes. m and l belong to the
+// lane's own query row; rescaling needs no exchange either.
+//  * k_tree_attention, rows up to 16 (up to 32 in large batches): a wave holds
+//    all rows, and K and V go from memory straight into its registers.
+//    K: lane l holds 8 consecutive values of key l % 16, so fragments are
+//    loaded from the rows as they lie, 16 bytes a lane. V: lane l loads, of its
+//    group's 8 keys, values (l % 16) C .. + C - 1 (C = 8 for 128 values: whole
+//    rows per 16 lanes) and transposes them in registers, one byte permute per
+//    output dword. Row m of V^T fragment f then stands for value m C + f, and
+//    lane l's accumulators hold runs of C consecutive values of its row, stored
+//    16 bytes at a time.
+//  * k_tree_attention_wide, more rows: 4 or 8 waves hold different rows and
+//    share the keys through LDS.
 //
-// The keys of a (sequence, KV head) are split over workgroups so that a few
-// long sequences fill the device too; the parts are joined by a second
-// kernel, in order. The four waves of a workgroup hold different rows (64
-// each) or different strips, joined through LDS at the end.
+// P is rounded to the values' type (its relative error, 2^-9 for BF16, is that
+// of the result's own rounding); sums, m, l and o are fp32. A row's m only
+// moves when a strip exceeds it by more than 8 (a factor of 2^8, far inside
+// fp32 and both 16-bit ranges), which makes rescaling rare.
+//
+// The work is cut into equal parts over all sequences (share_of), so that one
+// long history fills the device as well as many short ones do; a second kernel
+// joins the parts of a row in their order.
+//
+// Measured (BF16, 8 KV heads of 128 under 32 query heads, pages of 16; us on
+// the device with the join): one sequence of 131072 tokens, one node: 113, 4.8
+// TB/s; 16384 tokens: 21; 1024: 10.6. 64 sequences of up to 8192 tokens with 8
+// nodes: 216 + 12, 5.0 TB/s, where a large copy reaches 4.9. 64 nodes over
+// 131072 tokens (256 rows to a KV head): 185 to 220 with the clock, 620 to 740
+// TFLOP/s, where a large library matrix product reaches 1190: the vector unit
+// (exponentials, maxima, packing) is busy 40% of the cycles, the matrix unit
+// 37%, LDS 23%; without the loads it takes 183, the loads alone 107.
 #include "step_common.h"
 #include "group_math.h"
 
@@ -198,8 +210,9 @@ __device__ __forceinline__ uint32_t tree_bits(uint32_t b, uint32_t i, uint32_t f
 // DP: head_dim rounded up to what the fragments hold; EXACT: equal to it.
 // U: 16-row units of a wave.
 // HEADS: the four waves take four neighbouring KV heads of the same keys, so
-// rows of the cache that lie together are read together; else they take
-// different strips of one head, joined through LDS at the end.
+// rows of the cache that lie together are read together (64 sequences of up to
+// 8192 tokens: 230 us, 251 without); else they take different strips of one
+// head, joined through LDS at the end, and U is 1.
 template <typename T, int DP, int U, bool EXACT, bool HEADS>
 __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(TreeAttnArgs k) {
   constexpr int KS = DP / 32;                   // k steps of Q K^T
@@ -576,8 +589,10 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
 // ---- many rows: K and V through LDS
 //
 // W waves of U units each hold W U 16 different rows and go through the same
-// keys, a stage of SK at a time, held twice in LDS (the next stage is on its
-// way into registers while one is computed). Banks: a wave reads one 16-byte
+// keys, a stage of SK at a time. Heads up to 128 values: three stages lie in
+// LDS (the one computed, the next, whose first K fragments are read early, and
+// the one a slower wave may still be in), a fourth is on its way into
+// registers. Above: two, for want of registers and LDS. Banks: a wave reads one 16-byte
 // chunk of 16 rows of K at a time, in groups of lanes that mix neighbouring
 // chunks, so chunk c of row r lies at c ^ k_turn(r); of V it reads 32 bytes of
 // 8 rows, so rows lie 32 bytes further apart than they are long. V^T fragments
@@ -1145,10 +1160,12 @@ void launch_unit(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
     hipLaunchKernelGGL((k_tree_attention<T, DP, U, true, true>), grid, block, 0, s, k);
   else if (p.ways == 1)
     hipLaunchKernelGGL((k_tree_attention<T, DP, U, false, true>), grid, block, 0, s, k);
-  else if (k.a.head_dim == DP)
-    hipLaunchKernelGGL((k_tree_attention<T, DP, U, true, false>), grid, block, 0, s, k);
-  else
-    hipLaunchKernelGGL((k_tree_attention<T, DP, U, false, false>), grid, block, 0, s, k);
+  else if constexpr (U == 1) {
+    if (k.a.head_dim == DP)
+      hipLaunchKernelGGL((k_tree_attention<T, DP, 1, true, false>), grid, block, 0, s, k);
+    else
+      hipLaunchKernelGGL((k_tree_attention<T, DP, 1, false, false>), grid, block, 0, s, k);
+  }
 }
 
 template <typename T, int DP, int U, int W>
@@ -1161,8 +1178,10 @@ void launch_wide(const TreeAttnArgs &k, hipStream_t s) {
 template <typename T, int DP>
 void launch_dim(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
   if (p.wide) {
-    if (p.waves == 4) {
+    if (p.waves == 4 && p.units == 1) {
       launch_wide<T, DP, 1, 4>(k, s);
+    } else if (p.waves == 4) {
+      if constexpr (DP <= 128) launch_wide<T, DP, 2, 4>(k, s);
     } else if (p.units == 1) {
       launch_wide<T, DP, 1, 8>(k, s);
     } else if constexpr (DP <= 128) {
@@ -1175,7 +1194,8 @@ void launch_dim(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
   }
 }
 
-// Four waves to a row while the rows alone do not fill the device.
+// Four waves to a row while the rows alone do not fill the device (131072
+// tokens, one node: 113 us in all, 166 with one wave to a row).
 template <typename T, uint32_t LD>
 void launch_join(const TreeAttnArgs &k, hipStream_t s) {
   const uint32_t rows = k.a.batch * k.a.kv_heads * k.rows;
@@ -1205,30 +1225,42 @@ void launch_type(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
 
 }  // namespace
 
-// Up to 32 rows (16 for heads above 128): one wave holds them all, and the four
-// of a workgroup take different keys. More: waves hold different rows, 16 or
-// 32 each, 4 or 8 to a workgroup, then tiles. Splits: workgroups to fill 256
-// compute units, with a stage (or a strip for every wave) each at least.
+// Parts: as many as workgroups fit the device at once by their registers, with
+// a stage (or a strip for every wave) each at least: 16384 tokens and one node
+// took 50 us with 256 workgroups and 21 so; twice as many for the wide kernel
+// were slower at 64 nodes over 131072 tokens.
 TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a) {
   TreeAttnPlan p;
   const uint32_t rows = a.nodes * (a.q_heads / a.kv_heads);
+  const uint64_t heads = (uint64_t)a.batch * a.kv_heads;
   const bool large = a.head_dim > 128;
+  // Four heads to a workgroup where that leaves two waves to a compute unit
+  // before any history is split. 8 nodes of 4 heads, 64 sequences of up to 8192
+  // tokens: 228 us, in the wide kernel 264; 32 sequences of up to 4096: 87, wide
+  // 84; one of 65536: 58, wide 52.
+  const bool by_heads = a.kv_heads % 4 == 0 && heads >= 512;
   uint64_t fill;
-  if (rows <= (large ? 16u : 32u)) {
+  if (rows <= 16 || (rows <= 32 && !large && by_heads)) {
     p.wide = 0;
     p.units = rows <= 16 ? 1 : 2;
     p.waves = 4;
-    // four heads to a workgroup where that leaves two waves to a compute unit
-    // before any history is split
-    p.ways = a.kv_heads % 4 == 0 && (uint64_t)a.batch * a.kv_heads >= 512 ? 1 : 4;
+    p.ways = by_heads ? 1 : 4;
     p.unit = 32;
     p.row_tiles = 1;
     // workgroups that 256 compute units hold at once, by the registers of a wave
     fill = 256 * (a.head_dim <= 64 ? 5 - p.units : large ? 1 : 4 - p.units) * (4 / p.ways);
   } else {
+    // Waves hold different rows, 16 or 32 each, 4 or 8 to a workgroup, then
+    // tiles. With 32 a wave reads each fragment from LDS once for two products
+    // (132 rows: 83 us against 154). 65 to 128 rows: four waves of 32 where
+    // there are many sequences and heads (16 sequences of up to 4096 tokens, 100
+    // rows: 56 us against 70 with eight of 16); eight of 16 where histories are
+    // split more, whose parts are then half as many (1024 tokens: 13.5 against
+    // 16.7; 65536: 72 against 77).
     p.wide = 1;
-    p.units = large || rows <= 128 ? 1 : 2;
-    p.waves = rows <= 64 ? 4 : 8;
+    const bool four = rows <= 64 || (rows <= 128 && !large && heads >= 128);
+    p.units = large || rows <= 64 || (rows <= 128 && !four) ? 1 : 2;
+    p.waves = four ? 4 : 8;
     p.ways = 1;
     p.unit = stage_keys(large ? 256 : a.head_dim > 64 ? 128 : 64, p.waves);
     const uint32_t tile = 16 * p.units * p.waves;

@@ -301,3 +301,35 @@ def test_offsets_past_32_bits(E):
     wide[0][t2[0].long()], wide[1][t2[0].long()] = small_k, small_v
     got = E.enc_tree_attention(q, kn, vn, wide[0], wide[1], t2, lens)[0]
     assert torch.equal(got, want)
+
+
+MANY = [(128, 3, 8, 4, 128, torch.bfloat16),    # 6 rows to a KV head, four heads to a workgroup
+        (128, 5, 8, 4, 72, torch.float16),      # 10, heads of 72
+        (128, 7, 16, 4, 128, torch.bfloat16),   # 28
+        (130, 8, 12, 4, 64, torch.float16),     # 24, a batch that ends inside a wave
+        (128, 2, 8, 4, 200, torch.bfloat16),    # 4, heads of 200
+        (128, 4, 20, 5, 128, torch.bfloat16),   # five KV heads: not in fours
+        (32, 25, 16, 4, 128, torch.bfloat16),   # 100, two to a wave's fragments
+        (32, 25, 16, 4, 40, torch.float16),
+        (40, 30, 16, 4, 64, torch.bfloat16)]    # 120
+
+
+@pytest.mark.parametrize("B,T,H,G,D,dt", MANY)
+def test_many_sequences(E, B, T, H, G, D, dt):
+    say("attention, many sequences", B, T, H, G, D, dt)
+    c = Case(B, T, H, G, D, [700 if b == 5 else b * 7 % 90 for b in range(B)], 16, dt, seed=5)
+    live = [(b * 5) % (T + 1) for b in range(B)]
+    c.check(E)
+    c.check(E, nodes=live)
+
+
+@pytest.mark.parametrize("B,T,H,G,D,dt", MANY)
+def test_many_sequences_nonfinite_where_a_row_may_not_look(E, B, T, H, G, D, dt):
+    say("attention, many sequences, NaN", B, T, H, G, D, dt)
+    c = Case(B, T, H, G, D, [700 if b == 5 else b * 7 % 90 for b in range(B)], 16, dt, seed=6)
+    c.seen[:, :T - 1, T - 1] = False
+    clean, clean_lse = c.run(E)
+    c.kn[:, T - 1], c.vn[:, T - 1] = float("nan"), float("inf")
+    out, lse = c.run(E)
+    assert torch.equal(out[:, :T - 1], clean[:, :T - 1]) and torch.equal(lse[:, :T - 1], clean_lse[:, :T - 1])
+    assert torch.isnan(out[:, T - 1].float()).all()
