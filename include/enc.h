@@ -434,7 +434,8 @@ typedef struct enc_qk_args {
 
 /* head_dim: a multiple of 8 up to 512; rot_dim: even, at most head_dim.
  * An output may be its input itself (same pointer, type and strides);
- * otherwise they must not overlap. tokens = 0 does nothing. Asynchronous. */
+ * otherwise they must not overlap. tokens = 0 does nothing; tokens * heads is
+ * at most 2^31 - 1. Asynchronous. */
 enc_status enc_qk_norm_rope(const enc_qk_args *h_args, void *stream);
 
 /* Attention of a tree's nodes over a paged cache and the tree itself:
@@ -470,8 +471,10 @@ typedef struct enc_tree_attention_args {
 
 /* Rows of nodes past a tree's live ones are 0 (lse -infinity). head_dim: a
  * multiple of 8 up to 256; nodes up to ENC_TREE_MAX_NODES; q_heads a multiple
- * of kv_heads; page_size up to 65536. A table entry outside [0, n_pages)
- * reads some page of the cache. The workspace (any contents) holds the parts
+ * of kv_heads; page_size up to 65536; max_pages * page_size and n_pages *
+ * page_size up to 2^31 - 1; a cache (K or V) below 64 GiB; batch * nodes *
+ * q_heads up to 2^25, batch * kv_heads up to 2^23. A table entry outside
+ * [0, n_pages) reads some page of the cache. The workspace (any contents) holds the parts
  * of rows whose history is split over workgroups, joined in a fixed order by
  * a second kernel: equal inputs give equal bits. Its size depends on batch,
  * nodes, heads, head_dim and max_pages * page_size. Asynchronous. */
@@ -512,7 +515,8 @@ typedef struct enc_verify_args {
   uint32_t batch, nodes, vocab, dtype; /* dtype of both distributions: 1 BF16, 2 FP16, 3 FP32 */
 } enc_verify_args;
 
-/* nodes up to ENC_TREE_MAX_NODES, vocab up to 2^22. Rows need no alignment
+/* nodes up to ENC_TREE_MAX_NODES, vocab up to 2^22, batch up to 2^20 (2^17
+ * for the largest vocabularies: 2^21 workgroups). Rows need no alignment
  * beyond their type's. The workspace must be zero-filled before its first use
  * with this entry point; every call leaves it ready for the next; calls
  * sharing one must not overlap. Asynchronous. */

@@ -9,7 +9,12 @@
 // number it was given, counts needs and free pages and either updates the
 // table, the counts and the lengths or leaves everything as it was. The
 // second moves the rows, and is bound by HBM traffic: a workgroup per
-// (sequence, plane, slice), 16 bytes a lane, several loads in flight.
+// (sequence, plane, slice), 16 bytes a lane.
+//
+// Measured (us on the device): one sequence, 64 planes of 2048-byte rows: plan
+// 3.9, move 2.9; 64 sequences of 32 nodes, 16 planes (65 MB): plan 7.8, move 15,
+// 4.3 TB/s; 16 forks of one prompt that then append, copying 63 rows of their
+// last page in 16 planes (71 MB): fork 2.7, move 10.
 #include "step_common.h"
 
 namespace enc {
