@@ -37,7 +37,7 @@
 // Measured (BF16, 8 KV heads of 128 under 32 query heads, pages of 16; us on
 // the device with the join): one sequence of 131072 tokens, one node: 113, 4.8
 // TB/s; 16384 tokens: 21; 1024: 10.6. 64 sequences of up to 8192 tokens with 8
-// nodes: 216 + 12, 5.0 TB/s, where a large copy reaches 4.9. 64 nodes over
+// nodes: 222 + 10, 4.8 TB/s, where a large copy reaches 4.9. 64 nodes over
 // 131072 tokens (256 rows to a KV head): 185 to 220 with the clock, 620 to 740
 // TFLOP/s, where a large library matrix product reaches 1190: the vector unit
 // (exponentials, maxima, packing) is busy 40% of the cycles, the matrix unit
