@@ -846,6 +846,13 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[u][j] = __builtin_amdgcn_exp2f(fmaf(p[u][j], c2, -mc[u]));
     }
+    if constexpr (SPECIAL) {   // -infinity times a scale of 0 is no number
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (!(seen[u] >> (16 * (j >> 2) + 4 * g4 + (j & 3)) & 1u)) p[u][j] = 0.f;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       l[u] += ((p[u][0] + p[u][1]) + (p[u][2] + p[u][3])) + ((p[u][4] + p[u][5]) + (p[u][6] + p[u][7]));
