@@ -71,6 +71,9 @@ struct TreeAttnArgs {
   float *part;               // [grid_parts, kv_heads, rows, head_dim] unnormalised sums
   float *part_ml;            // [grid_parts, kv_heads, rows, 2] running maximum and sum
   uint2 *shares;             // [batch] first part and number of parts; NULL: never more than one
+  uint32_t raw;              // maxima are of q.k times the scale's sign, not yet scaled
+  float unit;                // powers of two to a unit of a maximum
+  float slack;               // how far a strip may exceed it before it moves
 };
 struct TreeAttnPlan {
   uint32_t wide;             // rows on different waves, keys through LDS
@@ -80,7 +83,7 @@ struct TreeAttnPlan {
   uint64_t part_bytes, ml_bytes, share_bytes;
 };
 TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a);
-hipError_t launch_tree_attention(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s);
+hipError_t launch_tree_attention(TreeAttnArgs k, const TreeAttnPlan &p, hipStream_t s);
 
 struct VerifyKernelArgs {
   enc_verify_args a;

@@ -23,7 +23,7 @@
 //    lane l's accumulators hold runs of C consecutive values of its row, stored
 //    16 bytes at a time.
 //  * k_tree_attention_wide, more rows: 4 or 8 waves hold different rows and
-//    share the keys through LDS.
+//    share the keys through LDS. Its maxima are of q.k, before the scale.
 //
 // P is rounded to the values' type (its relative error, 2^-9 for BF16, is that
 // of the result's own rounding); sums, m, l and o are fp32. A row's m only
@@ -45,6 +45,8 @@
 #include "step_common.h"
 #include "group_math.h"
 
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 namespace enc {
@@ -52,17 +54,18 @@ namespace {
 
 constexpr float kLowest = -3.402823466e38f;   // finite: differences with it are not NaN
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr float kSlack = 8.0f * kLn2;
+constexpr float kSlack2 = 8.0f, kSlack = kSlack2 * kLn2;
 
 // e^x. Scores stay in natural units until here: the difference of two finite
 // scores does not overflow, a score times log2(e) may.
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 constexpr uint32_t kWavesA = 4;
+constexpr float kFar = 65536.f;   // see the wide kernel
 
 template <typename T> struct Half;
 template <> struct Half<__bf16> {
   static constexpr uint32_t kExp = 0x7F80u;
-  static constexpr float kLift = 0.f;
+  static constexpr float kLift2 = 0.f, kLift = 0.f;
   static __device__ __forceinline__ f32x4 mfma(uint4 a, uint4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
@@ -72,7 +75,7 @@ template <> struct Half<_Float16> {
   static constexpr uint32_t kExp = 0x7C00u;
   // P is held 2^6 larger (at most 2^14): FP16 loses precision below 2^-14, and
   // many keys of little weight together still count
-  static constexpr float kLift = 6.f * kLn2;
+  static constexpr float kLift2 = 6.f, kLift = kLift2 * kLn2;
   static __device__ __forceinline__ f32x4 mfma(uint4 a, uint4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
                                                   0);
@@ -641,7 +644,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
   uint32_t node[U];
   bool alive[U];
   const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;   // -scale (-q).k
-  const float scale = fabsf(a.scale), c2 = scale * kLog2e;
+  const float c2 = k.unit, slack = k.slack;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const uint32_t r = row0 + 16 * u;
@@ -658,17 +661,22 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
       qf[u][s] = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
     }
   }
+  // A key's weight is 2^(p c2 - mc), p = q.k: one fma, exact until it is
+  // rounded, so that mc, the row's maximum mr times c2 (less the lift), may be
+  // rounded as it likes. From kFar on the rounding of mc alone is no longer
+  // small beside 1: there it is 2^((p - mr) c2), whose difference is exact where
+  // it is small.
   f32x4 o[U][NF];
-  float m[U], mc[U], l[U];
+  float mr[U], mc[U], l[U];   // mr: -infinity until the row has seen a key
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    m[u] = kLowest;
+    mr[u] = -__builtin_inff();
     mc[u] = kLowest;
     l[u] = 0.f;
 #pragma unroll
     for (int f = 0; f < NF; ++f) o[u][f] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  uint32_t far = 0;   // some row's maximum times log2(e) leaves fp32 (the same in all lanes)
+  uint32_t far = 0;   // some row's maximum has got there (the same in all lanes, and for all rows)
 
   // ---- bringing a stage in: thread's chunk i is chunk ch of row r0 + i kRowStep
   const uint32_t ch = tid % NCH, r0 = tid / NCH;
@@ -764,31 +772,32 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
 
   // New maxima, and what is summed so far brought to them.
   auto grow = [&](const float (&top)[U]) {
+    const uint32_t was = far;
+    float up[U], at[U];
     uint32_t out = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float up = fmaxf(top[u] - Half<T>::kLift, m[u]), shrink = exp_of(m[u] - up);
-      m[u] = up;
-      mc[u] = fmaxf(up * kLog2e, kLowest);   // a row that has seen nothing keeps a finite one
-      out |= !(fabsf(up) < 1e38f) && up != kLowest;
+      up[u] = fmaxf(top[u], mr[u]);
+      at[u] = fmaf(up[u], c2, -Half<T>::kLift2);
+      out |= up[u] > -__builtin_inff() && !(fabsf(at[u]) < kFar);
+    }
+    far |= (uint32_t)(__ballot(out) != 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float by = was ? (mr[u] - up[u]) * c2 : far ? fmaf(-up[u], c2, mc[u]) + Half<T>::kLift2 : mc[u] - at[u];
+      const float shrink = mr[u] > -__builtin_inff() ? __builtin_amdgcn_exp2f(by) : 0.f;
+      mr[u] = up[u];
+      mc[u] = fmaxf(at[u], kLowest);
       l[u] *= shrink;
 #pragma unroll
       for (int f = 0; f < NF; ++f) o[u][f] *= shrink;
     }
-    far |= (uint32_t)(__ballot(out) != 0);
   };
 
   // ---- one strip of 32 keys of a stage
   auto compute = [&](auto special_, uint32_t st, uint32_t half, uint32_t buf) {
     constexpr bool SPECIAL = decltype(special_)::value;
-    uint4 kf[2][KS];
-    {
-      const uint4 *row = ks[buf] + (half * 32 + l16) * NCH;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int e = 0; e < KS; ++e) kf[t][e] = row[16 * t * NCH + ((4 * e + g4) ^ k_turn<NCH>(l16))];
-    }
+    const uint4 *row = ks[buf] + (half * 32 + l16) * NCH;
     const char *vb = reinterpret_cast<const char *>(vs[buf] + (half * 32 + 4 * g4 + (l16 >> 2)) * PITCH) + (l16 & 3) * 8;
     float p[U][8];
 #pragma unroll
@@ -798,13 +807,15 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
       for (int u = 0; u < U; ++u) s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < KS; ++e) {
+        const uint4 kf = row[16 * t * NCH + ((4 * e + g4) ^ k_turn<NCH>(l16))];
 #pragma unroll
-        for (int u = 0; u < U; ++u) s[u] = Half<T>::mfma(kf[t][e], qf[u][e], s[u]);
+        for (int u = 0; u < U; ++u) s[u] = Half<T>::mfma(kf, qf[u][e], s[u]);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[u][4 * t + e] = s[u][e];
+      if constexpr (!PIPE) __builtin_amdgcn_sched_barrier(0);   // half of K at a time: registers
     }
 
     const bool tree = SPECIAL && st >= ctx;
@@ -831,15 +842,16 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
       float t = p[u][0];
 #pragma unroll
       for (int j = 1; j < 8; ++j) t = fmaxf(t, p[u][j]);
-      top[u] = rows_max(t) * scale;
-      grown = grown || top[u] > m[u] + (kSlack + Half<T>::kLift);
+      top[u] = rows_max(t);
+      grown = grown || top[u] - mr[u] > slack;
     }
     if (__any(grown)) grow(top);
     if (far) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[u][j] = exp_of(fmaf(p[u][j], scale, -m[u]));
+        for (int j = 0; j < 8; ++j)
+          p[u][j] = __builtin_amdgcn_exp2f(fmaf(p[u][j] - fmaxf(mr[u], kLowest), c2, Half<T>::kLift2));
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -886,7 +898,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
       float t = p[u][0];
 #pragma unroll
       for (int j = 1; j < 8; ++j) t = fmaxf(t, p[u][j]);
-      top[u] = rows_max(t) * scale;
+      top[u] = rows_max(t);
     }
   };
   auto scores = [&](float (&x)[U][8]) {
@@ -919,16 +931,16 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
     }
     bool grown = false;
 #pragma unroll
-    for (int u = 0; u < U; ++u) grown = grown || top[u] > m[u] + (kSlack + Half<T>::kLift);
+    for (int u = 0; u < U; ++u) grown = grown || top[u] - mr[u] > slack;
     if (__any(grown)) grow(top);
     float off[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) off[u] = mc[u];
-    if (far) {   // scores less their maximum first, so that nothing overflows
+    if (far) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float less = m[u] / scale;
-        off[u] = 0.f;
+        const float less = fmaxf(mr[u], kLowest);
+        off[u] = -Half<T>::kLift2;
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[u][j] -= less;
       }
@@ -1065,6 +1077,9 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
     l[u] = rows_sum(l[u]);
     const uint32_t r = row0 + 16 * u;
     if (r >= g->rows) continue;
+    // sums of weights 2^((p - mr) c2 + lift), whichever way they were taken
+    const float fix = far || !(mr[u] > -__builtin_inff())
+                          ? 1.f : __builtin_amdgcn_exp2f(fmaf(-mr[u], c2, mc[u]) + Half<T>::kLift2);
     if (sh.parts == 1) {
       const uint32_t head = h * group + (r - node[u] * group);
       T *dst = static_cast<T *>(g->a.d_out) + b * g->a.out_batch + node[u] * g->a.out_node + head * g->a.out_head;
@@ -1080,18 +1095,18 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
       }
       if (g->a.d_lse && g4 == 0)
         g->a.d_lse[((uint64_t)b * g->a.nodes + node[u]) * g->a.q_heads + head] =
-            any ? m[u] + __log2f(l[u]) * kLn2 : -__builtin_inff();
+            any ? mr[u] * fabsf(g->a.scale) + (__log2f(l[u] * fix) - Half<T>::kLift2) * kLn2 : -__builtin_inff();
     } else {
       const uint64_t at = ((uint64_t)part * g->a.kv_heads + h) * g->rows + r;
       if (g4 == 0) {
-        g->part_ml[2 * at] = m[u];
-        g->part_ml[2 * at + 1] = l[u];
+        g->part_ml[2 * at] = fmaxf(mr[u], kLowest);
+        g->part_ml[2 * at + 1] = l[u] * fix;
       }
       float *dst = g->part + at * D;
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
         const uint32_t d = 16 * f + 4 * g4;
-        if (d < D) *reinterpret_cast<f32x4 *>(dst + d) = o[u][f];
+        if (d < D) *reinterpret_cast<f32x4 *>(dst + d) = o[u][f] * fix;
       }
     }
   }
@@ -1129,7 +1144,7 @@ __global__ __launch_bounds__(256) void k_tree_attention_join(TreeAttnArgs k) {
   for (uint32_t s = way; s < parts; s += W) {
     const float2 part = ml[s * step];
     const f32x4 o = *reinterpret_cast<const f32x4 *>(sums + s * step * a.head_dim);
-    const float w = exp_of(part.x - m);
+    const float w = __builtin_amdgcn_exp2f(fmaxf(part.x - m, kLowest) * k.unit);
     l += w * part.y;
     acc += o * w;
   }
@@ -1157,7 +1172,8 @@ __global__ __launch_bounds__(256) void k_tree_attention_join(TreeAttnArgs k) {
     *reinterpret_cast<uint2 *>(dst) = w;
   }
   if (a.d_lse && lane == 0)
-    a.d_lse[((uint64_t)b * a.nodes + node) * a.q_heads + head] = any ? m + __log2f(l) * kLn2 : -__builtin_inff();
+    a.d_lse[((uint64_t)b * a.nodes + node) * a.q_heads + head] =
+        any ? (k.raw ? m * fabsf(a.scale) - Half<T>::kLift : m) + __log2f(l) * kLn2 : -__builtin_inff();
 }
 
 template <typename T, int DP, int U>
@@ -1294,7 +1310,10 @@ TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a) {
   return p;
 }
 
-hipError_t launch_tree_attention(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
+hipError_t launch_tree_attention(TreeAttnArgs k, const TreeAttnPlan &p, hipStream_t s) {
+  k.raw = p.wide;
+  k.unit = p.wide ? std::min(std::fabs(k.a.scale) * kLog2e, -kLowest) : kLog2e;
+  k.slack = std::min(kSlack2 / k.unit, -kLowest);
   if (k.a.dtype == 1)
     launch_type<__bf16>(k, p, s);
   else

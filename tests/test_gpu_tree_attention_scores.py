@@ -57,3 +57,143 @@ def test_scale_zero_or_negative(E, shape, dt, scale):
     c.check(E)
     c.seen[:, c.T // 2] = False                     # a node that sees no other, nor itself
     c.check(E, nodes=[c.T - b % 2 for b in range(c.B)])
+
+
+# ------------------------------------------------------------------ large scores
+# Queries and keys are small whole numbers times powers of two, so that q.k is
+# exact in 32 bits and the kernels' scores are the definition's but for the
+# product with the scale. Rows up to 16 (32 in large batches) round that
+# product, by 2^-24 of the score at most, in each weight: |err| grows by 2^-23
+# max |score| sum p |v|. The wide kernel does not.
+WIDE = [s for s in SHAPES if "waves" in s or "256" in s]
+NARROW = [s for s in SHAPES if s not in WIDE]
+
+
+class Whole(Case):
+    """q.k = 2^exp n + at, n whole and small; `at` a column of its own."""
+
+    def __init__(self, shape, dt, seed, exp=0):
+        super().__init__(*SHAPES[shape], dt, seed=seed)
+        g = torch.Generator().manual_seed(seed)
+        small = lambda x: torch.randint(-1, 2, x.shape, generator=g).to(x.dtype).cuda()  # noqa: E731
+        self.a, self.b = exp // 2, exp - exp // 2
+        self.q, self.kn, self.kc = small(self.q) * 2.0 ** self.a, small(self.kn) * 2.0 ** self.b, small(self.kc) * 2.0 ** self.b
+        self.g = g
+
+    def column(self, d, q, k, spread=0, step=1):
+        """Column d of every query q, of every key k - step {0 .. spread}."""
+        for x in (self.kn, self.kc):
+            x[..., d] = k - step * torch.randint(0, spread + 1, x.shape[:-1], generator=self.g).to(x.dtype).cuda()
+        self.q[..., d] = q
+
+    def verdict(self, E, slack=0.0, **kw):
+        """As Case.check, with `slack` more for the weights."""
+        out, lse = self.run(E, **kw)
+        want, wl, size = self.want(**kw)
+        u = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}[out.dtype]
+        g, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        bad = ~(abs(g - want) <= u * abs(want) + (u + 2.0 ** -10 + slack) * size + 1e-30)
+        assert not bad.any(), "%d of %d outside" % (bad.sum(), bad.size)
+        fin = abs(wl) < float("inf")
+        assert (abs(gl - wl)[fin] <= 2.0 ** -11 + 2.0 ** -20 * abs(wl[fin])).all()
+        assert (gl[~fin] == -float("inf")).all() and (g[~fin] == 0).all()
+
+
+def extra(shape, top):
+    return 0.0 if shape in WIDE else 2.0 ** -23 * top
+
+
+@pytest.mark.parametrize("dt,exp", [(torch.bfloat16, e) for e in (20, 27, 30, 100, 120)]
+                         + [(torch.float16, e) for e in (20, 27, 30)])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_large_scores(E, shape, dt, exp):
+    """n is some 10 and the scale near 0.1: scores about 1e6, 1e8, 1e9, 1e30,
+    1e36. The largest outweighs all others; equal ones share."""
+    say("attention large scores", shape, dt, exp)
+    c = Whole(shape, dt, 41, exp)
+    c.verdict(E)
+    c.scale *= -1
+    c.verdict(E)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("bits", [14, 18, 20, 22])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_smooth_weights_far_from_zero(E, shape, bits, sign, dt):
+    """All scores far from 0 together, their differences ordinary ones."""
+    say("attention scores far from 0", shape, bits, sign, dt)
+    c = Whole(shape, dt, 42)
+    c.column(0, 2.0 ** (bits // 2), sign * 2.0 ** (bits - bits // 2))
+    c.verdict(E, extra(shape, (2.0 ** bits + 300) * c.scale))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_where_the_arithmetic_changes(E, shape, sign, dt):
+    """Scores of 2^16 powers of two, some keys on each side, in every part."""
+    say("attention scores around 2^16", shape, sign, dt)
+    c = Whole(shape, dt, 43)
+    c.scale = 128 ** -0.5                          # 2^16 at q.k = 513935
+    c.column(0, 512.0, sign * 1004.0)              # 514048
+    c.column(1, 1.0, 0.0, 127, sign * 2)           # down to 513794
+    c.verdict(E, extra(shape, 514348 * c.scale))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("down", [False, True])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_scores_that_grow_along_the_history(E, shape, down, dt):
+    """Each page's keys outweigh the page's before (or after) by far, from
+    ordinary scores to 2^22."""
+    say("attention growing scores", shape, down, dt)
+    c = Whole(shape, dt, 44)
+    c.q[..., 0] = 2.0 ** 11
+    c.kn[..., 0] = 0 if down else 2.0 ** 11
+    for row, n in zip(c.table, c.lens):
+        held = row[:-(-n // c.page)]
+        for i, page in enumerate(held):
+            at = len(held) - 1 - i if down else i
+            c.kc[int(page), :, :, 0] = 2.0 ** min(at, 11) if at else 0
+    c.verdict(E, extra(shape, (2.0 ** 22 + 300) * c.scale))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_lowest_values(E, shape, dt):
+    """Scores at the type's lowest value, all of them: the mean of what is seen."""
+    say("attention lowest values", shape, dt)
+    c = Case(*SHAPES[shape], dt, seed=45)
+    c.q[:] = 0
+    c.q[..., 0] = 1
+    c.kc[..., 0] = torch.finfo(dt).min
+    c.kn[..., 0] = torch.finfo(dt).min
+    c.scale = 1.0
+    Whole.verdict(c, E)
+    c.q[..., 0] = -1                               # and at the highest
+    Whole.verdict(c, E)
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e30, 3.4e38])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_scales_at_the_ends(E, shape, scale):
+    say("attention scale", scale, shape)
+    c = Whole(shape, torch.bfloat16, 46, 0 if scale < 1 else -120)
+    c.scale = scale
+    c.verdict(E)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_one_key_that_outweighs_all(E, shape, dt):
+    say("attention sharp", shape, dt)
+    for part in (0.0, 0.3, 0.99):
+        c = Case(*SHAPES[shape], dt, seed=47)
+        b = int(c.lens.argmax())
+        at = int(part * c.lens[b])
+        page, row = int(c.table[b, at // c.page]), at % c.page
+        c.kc[page, row, 0] = 30 * c.q[b, 0, 0]
+        out, _ = c.run(E)
+        # every other score is 30 |q|^2 scale - 6 |q| or more below, far past 2^-24
+        assert (out[b, 0, 0].float() - c.vc[page, row, 0].float()).abs().max() <= 2.0 ** -7 * 4
