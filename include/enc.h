@@ -535,7 +535,7 @@ typedef struct enc_cache {
   int32_t *d_lens;                 /* [max_seqs] */
   int32_t *d_refs;                 /* [n_pages] */
   uint64_t plane_stride;           /* bytes, a multiple of 16 */
-  uint32_t n_planes, n_pages, page_size, row_bytes; /* row_bytes: a multiple of 16 */
+  uint32_t n_planes, n_pages, page_size, row_bytes; /* row_bytes: a multiple of 16, up to 2^31 */
   uint32_t max_seqs, max_pages;
 } enc_cache;
 

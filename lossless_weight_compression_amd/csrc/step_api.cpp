@@ -62,6 +62,8 @@ enc_status check_cache(const enc_cache *c) {
   if (c->n_planes > 65535 || c->page_size > 65536 || c->n_pages > 0x7FFFFFFFu || c->max_seqs > 0x7FFFFFFFu)
     return unsupported("n_planes above 65535, page_size above 65536, or 2^31 pages or sequences");
   if ((uint64_t)c->max_pages * c->page_size > 0x7FFFFFFFull) return unsupported("max_pages * page_size above 2^31 - 1");
+  // a row is copied by steps of up to 4096 bytes, counted in 32 bits
+  if (c->row_bytes > (1u << 31)) return unsupported("row_bytes above 2^31");
   const uint64_t used = (uint64_t)c->n_pages * c->page_size;
   if (used > 0x7FFFFFFFull) return unsupported("n_pages * page_size above 2^31 - 1");
   if (used > (1ull << 40) / c->row_bytes) return unsupported("a plane above 2^40 bytes");
