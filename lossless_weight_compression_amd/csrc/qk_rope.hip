@@ -149,6 +149,7 @@ __global__ __launch_bounds__(kBlock) void k_qk_norm_rope(QkKernelArgs k) {
     if (adjacent) {
       if (turns && !is_v) {
         for (int e = 0; e < 8; e += 2) {
+          if (!VEC && d0 + e >= a.rot_dim) continue;   // 0 times an infinity is no number
           const float u = x[i][e], v = x[i][e + 1];
           x[i][e] = u * c[e] - v * s[e];
           x[i][e + 1] = v * c[e] + u * s[e];
