@@ -550,7 +550,8 @@ typedef struct enc_cache {
  * *d_status (device) becomes 0, or, with nothing changed: the number of pages
  * missing, -1 (a sequence outside the table), -2 (a count or path entry
  * outside the nodes), -3 (a length past max_pages * page_size), -4 (a table
- * entry or length that no call of this group left). The workspace may hold
+ * entry, a last page's count or a length that no call of this group left); of
+ * several reasons the lowest. batch is at least 1. The workspace may hold
  * anything. Asynchronous. */
 uint64_t enc_cache_workspace_bytes(const enc_cache *h_cache, uint32_t batch, uint32_t nodes);
 enc_status enc_cache_commit(const enc_cache *h_cache, const int32_t *d_seqs, uint32_t batch,

@@ -80,7 +80,9 @@ __device__ __forceinline__ Need need_of(const CommitArgs &k, uint32_t b) {
     const int32_t e = row[p];
     if (partly && p == p0) {
       if ((uint32_t)e >= k.c.n_pages) { n.error = kBadTable; return n; }
-      if (k.c.d_refs[e] > 1) {
+      const int32_t refs = k.c.d_refs[e];
+      if (refs < 1) { n.error = kBadTable; return n; }   // held, yet free for others
+      if (refs > 1) {
         n.last = e;
         ++n.pages;
       }
