@@ -466,6 +466,10 @@ __global__ __launch_bounds__(kThreadsV) void k_verify(VerifyKernelArgs k) {
   // the last workgroup of a sequence leaves its words at zero for the next call
   if (G > 1) {
     __shared__ uint32_t order;
+    // A workgroup that waited to the end has read its own words back. One that
+    // gave up has not: they must have arrived before it counts as through, or
+    // the last one's zeros could be overtaken.
+    if (solo) __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
     __syncthreads();
     if (tid == 0) order = __hip_atomic_fetch_add(&k.done[b], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();

@@ -53,3 +53,21 @@ def test_vocabularies_above_the_registers(E, monkeypatch, B, T, V, dt, point, sp
         u0[:, 0] = [0.0, 0.9999999, 0.25][:B]
         compare(E, parents, tokens, p, None if point else q, u0, ws=ws)
     assert rejected and not ws.any()
+
+
+@pytest.mark.parametrize("spins", ["0", "2"])
+def test_workgroups_that_give_up_leave_the_workspace_zero(E, monkeypatch, spins):
+    """Many sequences whose workgroups stop waiting at their first sum, then the
+    same workspace with all the patience there is, in turn."""
+    say("verify, impatient then patient", spins)
+    parents, tokens, p, q, u = make(24, 3, 66000, torch.float32, 60, near=1.5)
+    c = [torch.from_numpy(a).cuda() for a in (parents, tokens)] + [p.cuda(), q.cuda(), torch.from_numpy(u).cuda()]
+    ws = E.verify_tree_workspace(c[1], c[2])
+    want = [t.clone() for t in E.enc_verify_tree(*c)]
+    for _ in range(20):
+        monkeypatch.setenv("ENC_VERIFY_SPINS", spins)
+        got = E.enc_verify_tree(*c, ws=ws)
+        monkeypatch.delenv("ENC_VERIFY_SPINS")
+        again = E.enc_verify_tree(*c, ws=ws)
+        assert all(torch.equal(a, b) for a, b in zip(want, got)) and all(torch.equal(a, b) for a, b in zip(want, again))
+    assert not ws.any()
