@@ -115,6 +115,8 @@ class Decoder:
             order = torch.arange(n, dtype=torch.int32, device="cuda").repeat(self.batch, 1)
             _, rows = self.forward(part, order, None, self.model.layers)
             self.commit(rows, order, torch.full((self.batch,), n, dtype=torch.int32, device="cuda"))
+            if int(self.cache.status):
+                raise RuntimeError("the cache refused the prompt's rows: %d" % int(self.cache.status))
         return prompt[:, -1].contiguous()
 
     def plain_step(self, pending):
@@ -179,6 +181,8 @@ def generate(decoder, prompt, n, speculate=True):
             pending = decoder.plain_step(pending)
         for b, t in enumerate(pending.tolist()):
             out[b].append(t)
+        if int(decoder.cache.status):               # nothing was appended: what followed would miss these rows
+            raise RuntimeError("the cache refused the step's rows: %d" % int(decoder.cache.status))
     return [o[:n] for o in out], steps
 
 
