@@ -25,8 +25,16 @@
 //  * k_tree_attention_wide, more rows: 4 or 8 waves hold different rows and
 //    share the keys through LDS. Its maxima are of q.k, before the scale.
 //
-// P is rounded to the values' type (its relative error, 2^-9 for BF16, is that
-// of the result's own rounding); sums, m, l and o are fp32. A row's m only
+// The matrix unit takes P in the values' type. k_tree_attention, which waits
+// for memory, gives it P in two, the rounding and the rounded rest, so that the
+// result's own rounding is what is left (BF16, against 64 bits: 1.66e-3 of the
+// result's norm, 2.2e-3 with the rounding alone; one node over 1021 tokens 11.9
+// us, 11.4 without, 16384 22.0 and 21.5, 131072 117.2 and 116.6, 64 sequences
+// the same).
+// In the wide kernel the second product would cost more than half as much again
+// (64 nodes over 131072 tokens: 197 us, 306 with it): there P is rounded, an
+// error of 2^-9 of each weight for BF16, as large as the result's rounding. Sums,
+// m, l and o are fp32. A row's m only
 // moves when a strip exceeds it by more than 8 (a factor of 2^8, far inside
 // fp32 and both 16-bit ranges), which makes rescaling rare.
 //
@@ -211,13 +219,14 @@ __device__ __forceinline__ uint32_t tree_bits(uint32_t b, uint32_t i, uint32_t f
 }
 
 // DP: head_dim rounded up to what the fragments hold; EXACT: equal to it.
-// U: 16-row units of a wave.
+// U: 16-row units of a wave. Three workgroups to a compute unit are asked for
+// where they just fit (heads of 96, 32768 tokens: 32.6 us, 37.0 with two).
 // HEADS: the four waves take four neighbouring KV heads of the same keys, so
 // rows of the cache that lie together are read together (64 sequences of up to
 // 8192 tokens: 230 us, 251 without); else they take different strips of one
 // head, joined through LDS at the end, and U is 1.
 template <typename T, int DP, int U, bool EXACT, bool HEADS>
-__global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(TreeAttnArgs k) {
+__global__ __launch_bounds__(256, (DP == 256 ? 1 : DP == 128 && U == 1 ? 3 : 2)) void k_tree_attention(TreeAttnArgs k) {
   constexpr int KS = DP / 32;                   // k steps of Q K^T
   constexpr int C = DP >= 128 ? 8 : DP / 16;    // consecutive values a lane transposes
   constexpr int NH = DP / (16 * C);             // groups of 16 C values
@@ -266,15 +275,6 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
 
   f32x4 o[U][NH][C];
   float m[U], l[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    m[u] = kLowest;
-    l[u] = 0.f;
-#pragma unroll
-    for (int x = 0; x < NH; ++x)
-#pragma unroll
-      for (int f = 0; f < C; ++f) o[u][x][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
 
   // ---- strips: cached keys, then the tree's own; one strip's registers, each
   // half loaded again as soon as it has been used
@@ -342,11 +342,11 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
 
   // One strip, its K and V on the way into the registers. SPECIAL: a last strip
   // that is not full, and the tree's: keys that a row may not see score
-  // -infinity, values that are no keys' or (tree) not finite become 0. `after_k`
-  // and `after_v` load the next strip's halves.
+  // -infinity, values that are no keys' or (tree) not finite become 0. SPLIT: P
+  // in two parts. `after_k` and `after_v` load the next strip's halves.
   bool strange = false;   // infinities or NaN were among the tree's values
-  auto compute = [&](auto special_, uint32_t strip, auto after_k, auto after_v) {
-    constexpr bool SPECIAL = decltype(special_)::value;
+  auto compute = [&](auto special_, auto split_, uint32_t strip, auto after_k, auto after_v) {
+    constexpr bool SPECIAL = decltype(special_)::value, SPLIT = decltype(split_)::value;
     float p[U][8];
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -387,7 +387,7 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
       }
     }
 
-    uint4 pf[U];
+    uint4 pf[U], pl[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float top = kLowest;
@@ -414,8 +414,14 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
         p[u][j] = exp_of(p[u][j] - m[u]);
         l[u] += p[u][j];
       }
-      pf[u] = make_uint4(pack2<T>(p[u][0], p[u][1]), pack2<T>(p[u][2], p[u][3]), pack2<T>(p[u][4], p[u][5]),
-                         pack2<T>(p[u][6], p[u][7]));
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        hi[j] = pack2<T>(p[u][2 * j], p[u][2 * j + 1]);
+        if (SPLIT) lo[j] = pack2<T>(p[u][2 * j] - half_of<T>(hi[j], 0), p[u][2 * j + 1] - half_of<T>(hi[j], 1));
+      }
+      pf[u] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if (SPLIT) pl[u] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
 #pragma unroll
     for (int n = 0; n < NH; ++n)
@@ -428,48 +434,79 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : 2)) void k_tree_attention(Tre
                                        f & 1 ? 0x07060302u : 0x05040100u);
         const uint4 vf = make_uint4(w[0], w[1], w[2], w[3]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) o[u][n][f] = Half<T>::mfma(vf, pf[u], o[u][n][f]);
+        for (int u = 0; u < U; ++u) {
+          o[u][n][f] = Half<T>::mfma(vf, pf[u], o[u][n][f]);
+          if (SPLIT) o[u][n][f] = Half<T>::mfma(vf, pl[u], o[u][n][f]);
+        }
       }
 
     after_v();
   };
 
-  uint32_t strip = lo + kw;
   const uint32_t whole = min(hi, q.len / 32);     // strips of 32 cached keys
-  uint32_t ko, vo;
-  if (strip < whole) {
-    offsets_of(strip, entry_of(strip), ko, vo);
-    load_k(strip, ko);
-    load_v(strip, vo);
-    int32_t entry = strip + ways < whole ? entry_of(strip + ways) : 0;
-    while (true) {
-      const uint32_t next = strip + ways;
-      const bool more = next < whole;
-      if (more) offsets_of(next, entry, ko, vo);
-      compute(
-          std::false_type{}, strip,
-          [&] {
-            if (!more) return;
-            load_k(next, ko);
-            entry = next + ways < whole ? entry_of(next + ways) : 0;
-          },
-          [&] {
-            if (more) load_v(next, vo);
-          });
-      strip = next;
-      if (!more) break;
+  auto pass = [&](auto split_) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      m[u] = kLowest;
+      l[u] = 0.f;
+#pragma unroll
+      for (int x = 0; x < NH; ++x)
+#pragma unroll
+        for (int f = 0; f < C; ++f) o[u][x][f] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    uint32_t strip = lo + kw;
+    uint32_t ko, vo;
+    if (strip < whole) {
+      offsets_of(strip, entry_of(strip), ko, vo);
+      load_k(strip, ko);
+      load_v(strip, vo);
+      int32_t entry = strip + ways < whole ? entry_of(strip + ways) : 0;
+      while (true) {
+        const uint32_t next = strip + ways;
+        const bool more = next < whole;
+        if (more) offsets_of(next, entry, ko, vo);
+        compute(
+            std::false_type{}, split_, strip,
+            [&] {
+              if (!more) return;
+              load_k(next, ko);
+              entry = next + ways < whole ? entry_of(next + ways) : 0;
+            },
+            [&] {
+              if (more) load_v(next, vo);
+            });
+        strip = next;
+        if (!more) break;
+      }
+    }
+    for (; strip < hi; strip += ways) {
+      offsets_of(strip, entry_of(strip), ko, vo);
+      load_k(strip, ko);
+      load_v(strip, vo);
+      compute(std::true_type{}, split_, strip, [] {}, [] {});
+    }
+  };
+  // The rest of a weight may be 0 or below, and then no number, or the wrong
+  // infinity, comes of an infinite cached value. Every row sees that: where no
+  // row is finite, once more without the rest.
+  pass(std::true_type{});
+  bool lost = true;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float zero = 0.f;
+#pragma unroll
+    for (int n = 0; n < NH; ++n)
+#pragma unroll
+      for (int f = 0; f < C; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) zero = fmaf(o[u][n][f][e], 0.f, zero);
+    lost = lost && rows_sum(zero) != 0.f;
   }
-  for (; strip < hi; strip += ways) {
-    offsets_of(strip, entry_of(strip), ko, vo);
-    load_k(strip, ko);
-    load_v(strip, vo);
-    compute(std::true_type{}, strip, [] {}, [] {});
-  }
+  if (__all(lost)) pass(std::false_type{});
   // Infinities and NaN went in as zeros, since 0 times them would reach rows
   // that do not see them: add them to the rows that do.
   if (__any(strange)) {
-    for (strip = lo + kw; strip < hi; strip += ways) {
+    for (uint32_t strip = lo + kw; strip < hi; strip += ways) {
       if (strip < strips_ctx) continue;
       const uint32_t first = (strip - strips_ctx) * 32;
 #pragma unroll

@@ -197,3 +197,50 @@ def test_one_key_that_outweighs_all(E, shape, dt):
         out, _ = c.run(E)
         # every other score is 30 |q|^2 scale - 6 |q| or more below, far past 2^-24
         assert (out[b, 0, 0].float() - c.vc[page, row, 0].float()).abs().max() <= 2.0 ** -7 * 4
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("shape", NARROW)
+def test_only_the_result_is_rounded(E, shape, dt):
+    """Up to 16 rows (32 in large batches) weights count in more than 16 bits.
+    Scores are exact here, exponentials good to 2^-19 of themselves, what is
+    left of a weight in two parts is 2^-18, and a sum of n fp32 terms is off by
+    n 2^-24 at most (130 keys): 2^-15 of sum p |v| bounds them all, beside the
+    result's own rounding, 2^-8 (BF16) or 2^-11 of it, or 2^-25 in FP16."""
+    say("attention rounding", shape, dt)
+    c = Whole(shape, dt, 48)
+    out, _ = c.run(E)
+    want, _, size = c.want()
+    u = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}[dt]
+    g = out.double().cpu().numpy()
+    bad = ~(abs(g - want) <= u * abs(want) + 2.0 ** -15 * size + (2.0 ** -25 if dt == torch.float16 else 0))
+    assert not bad.any(), "%d of %d outside" % (bad.sum(), bad.size)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_infinite_cached_values(E, shape, dt):
+    """Every row of the sequence sees them: infinities of the value's sign, no
+    number where both meet or a value is none, and nothing anywhere else."""
+    say("attention infinite cached values", shape, dt)
+    c = Case(*SHAPES[shape], dt, seed=49)
+    base, lse = c.run(E)
+    b = int(c.lens.argmax())
+    n = int(c.lens[b])
+    inf = float("inf")
+    at = lambda t: (int(c.table[b, t // c.page]), t % c.page)  # noqa: E731
+    for t, d, x in ((0, 1, inf), (n // 2, 3, -inf), (n - 1, 6, inf), (3, 9, inf), (n - 2, 9, -inf), (n // 3, 12, float("nan"))):
+        c.vc[at(t) + (slice(None), d)] = x
+    out, l2 = c.run(E)
+    assert torch.equal(lse, l2)
+    got = out[b].float()
+    assert (got[..., 1] == inf).all() and (got[..., 3] == -inf).all() and (got[..., 6] == inf).all()
+    assert got[..., [9, 12]].isnan().all()
+    rest = [d for d in range(c.D) if d not in (1, 3, 6, 9, 12)]
+    # finite places differ at most by what rounding the weights does
+    u = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}[dt]
+    want, _, size = c.want()
+    bad = ~(abs(out.double().cpu().numpy() - want) <= u * abs(want) + (u + 2.0 ** -10) * size + 1e-30)
+    assert not bad[b][..., rest].any()
+    others = [i for i in range(c.B) if i != b]
+    assert torch.equal(out[others], base[others])
