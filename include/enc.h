@@ -447,7 +447,9 @@ enc_status enc_qk_norm_rope(const enc_qk_args *h_args, void *stream);
  * in page d_table[s][t / page_size], row t % page_size. Infinities and NaN
  * in rows that a node does not see leave its output alone. A node that sees
  * nothing has output 0 and lse -infinity. d_lse: log sum exp of the scaled
- * scores (natural logarithm). */
+ * scores (natural logarithm). scale is any finite number. With up to 16 query
+ * rows to a KV head (up to 32 in some large batches) the result is all that is
+ * rounded to the values' type; with more, so is each softmax weight. */
 typedef struct enc_tree_attention_args {
   const void *d_q;                 /* [batch, nodes, q_heads, head_dim] */
   const void *d_k_new, *d_v_new;   /* the nodes' own rows, [batch, nodes, kv_heads, head_dim] */
@@ -499,7 +501,8 @@ enc_status enc_tree_attention(const enc_tree_attention_args *h_args, void *d_ws,
  * probabilities are read as fp32 and clamped to [0, 1] (NaN: 0); products,
  * differences and quotients are rounded to fp32 one by one; sums are exact
  * sums of whole multiples of 2^-40 (each term rounded to nearest, ties to
- * even); u counts in units of 2^-24, rounded down, clamped to [0, 1).
+ * even); u[0] counts in units of 2^-24, rounded down, clamped to [0, 1) (NaN: 0),
+ * the others as they are (NaN: rejected).
  * A child whose token lies outside [0, vocab) is rejected without changing
  * r. If r is 0 everywhere token is -1. A sequence without live nodes has
  * count 0 and token -1. */

@@ -12,9 +12,14 @@
 // (sequence, plane, slice), 16 bytes a lane.
 //
 // Measured (us on the device): one sequence, 64 planes of 2048-byte rows: plan
-// 3.9, move 2.9; 64 sequences of 32 nodes, 16 planes (65 MB): plan 7.8, move 15,
-// 4.3 TB/s; 16 forks of one prompt that then append, copying 63 rows of their
-// last page in 16 planes (71 MB): fork 2.7, move 10.
+// 4.1, move 2.9; 64 sequences of 32 nodes, 16 planes (65 MB): plan 8 to 9, move
+// 15, 4.3 TB/s; 16 forks of one prompt that then append, copying 63 rows of their
+// last page in 16 planes (71 MB): fork 2.6, plan 8.0, move 10.
+//
+// The plan counts the free pages of the whole pool, 64 counts a wave at a time,
+// and then walks them again up to the last one needed: a call that needs one
+// page takes 1 us more with 10000 pages than with 100, 12 with 100000 (32 if
+// the first free one comes after nine tenths of them), 142 (320) with a million.
 #include "step_common.h"
 
 namespace enc {

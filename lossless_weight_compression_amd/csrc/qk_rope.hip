@@ -10,8 +10,8 @@
 // between the two halves of a head through LDS, within the wave.
 //
 // Measured (us on the device): 8192 tokens of 48 heads of 128, fp32 in, BF16
-// out (306 MB): 61, 5.0 TB/s, where a large copy reaches 4.9; 792 tokens of 24
-// heads of 64 in BF16: 4.9; one token: 3.2 of a call's 12 (the rest is the
+// out (306 MB): 60, 5.1 TB/s, where a large copy reaches 4.9; 792 tokens of 24
+// heads of 64 in BF16: 4.6; one token: 3.1 of a call's 12 (the rest is the
 // host's).
 #include "step_common.h"
 
@@ -198,9 +198,9 @@ __global__ __launch_bounds__(kBlock) void k_qk_norm_rope(QkKernelArgs k) {
 }
 
 // Three heads to a lane once that still gives every compute unit eight
-// workgroups, one below, where latency counts (us, three and one: 8192 tokens of
-// 48 heads of 128 65.4, 67.6; 1024: 10.4, 10.3; 792 of 24 heads of 64 5.6, 4.9;
-// 256 of 48 heads of 128 6.3, 4.6).
+// workgroups, one below, where latency counts (us a call of ten in a graph, three
+// and one: 8192 tokens of 48 heads of 128 65.4, 67.6; 1024: 10.4, 10.3; 792 of 24
+// heads of 64 5.6, 4.9; 256 of 48 heads of 128 6.3, 4.6).
 template <typename TI, typename TO, uint32_t LANES>
 void launch_heads(QkKernelArgs k, hipStream_t s) {
   constexpr uint32_t per = kBlock / LANES;

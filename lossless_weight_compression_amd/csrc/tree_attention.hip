@@ -42,14 +42,16 @@
 // long history fills the device as well as many short ones do; a second kernel
 // joins the parts of a row in their order.
 //
-// Measured (BF16, 8 KV heads of 128 under 32 query heads, pages of 16; us on
-// the device with the join): one sequence of 131072 tokens, one node: 113, 4.8
-// TB/s; 16384 tokens: 21; 1024: 10.6. 64 sequences of up to 8192 tokens with 8
-// nodes: 222 + 10, 4.8 TB/s, where a large copy reaches 4.9. 64 nodes over
-// 131072 tokens (256 rows to a KV head): 185 to 220 with the clock, 620 to 740
-// TFLOP/s, where a large library matrix product reaches 1190: the vector unit
-// (exponentials, maxima, packing) is busy 40% of the cycles, the matrix unit
-// 37%, LDS 23%; without the loads it takes 183, the loads alone 107.
+// Measured (BF16, 8 KV heads of 128 under 32 query heads; us on the device with
+// the join): one sequence of 131072 tokens, pages of 64, one node: 117, 4.6 TB/s;
+// 16384 tokens: 22; 1021, pages of 16: 11.9. 64 sequences of up to 8192 tokens
+// with 8 nodes: 219 + 11, 4.8 TB/s, where a large copy reaches 4.9; pages of 32
+// to 256 take 230 as well. 64 nodes over 131072 tokens (256 rows to a KV head):
+// 185 to 220 with the clock, 620 to 740 TFLOP/s, where a large library matrix
+// product reaches 1190: the vector unit (exponentials, maxima, packing) is busy
+// 40% of the cycles, the matrix unit 37%, LDS 23%; without the loads it takes
+// 183, the loads alone 107. So no unit is the bound there: two waves to a SIMD,
+// behind one barrier a stage, do not cover each other's dependent steps.
 #include "step_common.h"
 #include "group_math.h"
 
@@ -414,14 +416,15 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : DP == 128 && U == 1 ? 3 : 2))
         p[u][j] = exp_of(p[u][j] - m[u]);
         l[u] += p[u][j];
       }
-      uint32_t hi[4], lo[4];
+      uint32_t round[4], rest[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        hi[j] = pack2<T>(p[u][2 * j], p[u][2 * j + 1]);
-        if (SPLIT) lo[j] = pack2<T>(p[u][2 * j] - half_of<T>(hi[j], 0), p[u][2 * j + 1] - half_of<T>(hi[j], 1));
+        const float a0 = p[u][2 * j], a1 = p[u][2 * j + 1];
+        round[j] = pack2<T>(a0, a1);
+        if (SPLIT) rest[j] = pack2<T>(a0 - half_of<T>(round[j], 0), a1 - half_of<T>(round[j], 1));
       }
-      pf[u] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if (SPLIT) pl[u] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      pf[u] = make_uint4(round[0], round[1], round[2], round[3]);
+      if (SPLIT) pl[u] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
     }
 #pragma unroll
     for (int n = 0; n < NH; ++n)
@@ -1255,7 +1258,7 @@ void launch_dim(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
 }
 
 // Four waves to a row while the rows alone do not fill the device (131072
-// tokens, one node: 113 us in all, 166 with one wave to a row).
+// tokens, one node: 117 us in all, 166 with one wave to a row).
 template <typename T, uint32_t LD>
 void launch_join(const TreeAttnArgs &k, hipStream_t s) {
   const uint32_t rows = k.a.batch * k.a.kv_heads * k.rows;
@@ -1287,7 +1290,7 @@ void launch_type(const TreeAttnArgs &k, const TreeAttnPlan &p, hipStream_t s) {
 
 // Parts: as many as workgroups fit the device at once by their registers, with
 // a stage (or a strip for every wave) each at least: 16384 tokens and one node
-// took 50 us with 256 workgroups and 21 so; twice as many for the wide kernel
+// took 50 us with 256 workgroups and 22 so; twice as many for the wide kernel
 // were slower at 64 nodes over 131072 tokens.
 TreeAttnPlan plan_tree_attention(const enc_tree_attention_args &a) {
   TreeAttnPlan p;
