@@ -28,9 +28,10 @@
 // The matrix unit takes P in the values' type. k_tree_attention, which waits
 // for memory, gives it P in two, the rounding and the rounded rest, so that the
 // result's own rounding is what is left (BF16, against 64 bits: 1.66e-3 of the
-// result's norm, 2.2e-3 with the rounding alone; one node over 1021 tokens 11.9
-// us, 11.4 without, 16384 22.0 and 21.5, 131072 117.2 and 116.6, 64 sequences
-// the same).
+// result's norm, 2.2e-3 with the rounding alone; one node over 1021 tokens 11.8
+// us, 11.4 without, 16384 21.8 and 21.4, 131072 116.6 and 116.4, 64 sequences
+// the same; at most 5% more, 64 sequences of up to 2000 tokens with 28 rows of
+// 80 values).
 // In the wide kernel the second product would cost more than half as much again
 // (64 nodes over 131072 tokens: 197 us, 306 with it): there P is rounded, an
 // error of 2^-9 of each weight for BF16, as large as the result's rounding. Sums,
@@ -44,7 +45,7 @@
 //
 // Measured (BF16, 8 KV heads of 128 under 32 query heads; us on the device with
 // the join): one sequence of 131072 tokens, pages of 64, one node: 117, 4.6 TB/s;
-// 16384 tokens: 22; 1021, pages of 16: 11.9. 64 sequences of up to 8192 tokens
+// 16384 tokens: 22; 1021, pages of 16: 11.8. 64 sequences of up to 8192 tokens
 // with 8 nodes: 219 + 11, 4.8 TB/s, where a large copy reaches 4.9; pages of 32
 // to 256 take 230 as well. 64 nodes over 131072 tokens (256 rows to a KV head):
 // 185 to 220 with the clock, 620 to 740 TFLOP/s, where a large library matrix
@@ -459,7 +460,7 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : DP == 128 && U == 1 ? 3 : 2))
     }
     uint32_t strip = lo + kw;
     uint32_t ko, vo;
-    if (strip < whole) {
+    if (decltype(split_)::value && strip < whole) {
       offsets_of(strip, entry_of(strip), ko, vo);
       load_k(strip, ko);
       load_v(strip, vo);
@@ -491,7 +492,8 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : DP == 128 && U == 1 ? 3 : 2))
   };
   // The rest of a weight may be 0 or below, and then no number, or the wrong
   // infinity, comes of an infinite cached value. Every row sees that: where no
-  // row is finite, once more without the rest.
+  // row is finite, once more without the rest, the simple way (the loop above a
+  // second time, never run, cost 2% of every call).
   pass(std::true_type{});
   bool lost = true;
 #pragma unroll
