@@ -404,7 +404,8 @@ __global__ __launch_bounds__(256, (DP == 256 ? 1 : DP == 128 && U == 1 ? 3 : 2))
       for (int j = 0; j < 8; ++j) top = fmaxf(top, p[u][j]);
       top = rows_max(top);
       if (__any(top > m[u] + (kSlack + Half<T>::kLift))) {
-        const float up = fmaxf(top - Half<T>::kLift, m[u]), shrink = exp_of(m[u] - up);
+        // only the rows concerned: what a row gives does not depend on the others
+        const float up = top > m[u] + (kSlack + Half<T>::kLift) ? top - Half<T>::kLift : m[u], shrink = exp_of(m[u] - up);
         m[u] = up;
         l[u] *= shrink;
 #pragma unroll
@@ -718,7 +719,8 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
 #pragma unroll
     for (int f = 0; f < NF; ++f) o[u][f] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  uint32_t far = 0;   // some row's maximum has got there (the same in all lanes, and for all rows)
+  bool far = false;   // some row of the wave has got there
+  auto beyond = [&](int u) { return !(fabsf(mc[u]) < kFar); };   // this one (or it has seen nothing)
 
   // ---- bringing a stage in: thread's chunk i is chunk ch of row r0 + i kRowStep
   const uint32_t ch = tid % NCH, r0 = tid / NCH;
@@ -812,28 +814,25 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
     }
   };
 
-  // New maxima, and what is summed so far brought to them.
+  // New maxima where a strip exceeds the old ones, and what is summed so far
+  // brought to them; other rows stay as they are, to the bit.
   auto grow = [&](const float (&top)[U]) {
-    const uint32_t was = far;
-    float up[U], at[U];
-    uint32_t out = 0;
+    bool out = false;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      up[u] = fmaxf(top[u], mr[u]);
-      at[u] = fmaf(up[u], c2, -Half<T>::kLift2);
-      out |= up[u] > -__builtin_inff() && !(fabsf(at[u]) < kFar);
-    }
-    far |= (uint32_t)(__ballot(out) != 0);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float by = was ? (mr[u] - up[u]) * c2 : far ? fmaf(-up[u], c2, mc[u]) + Half<T>::kLift2 : mc[u] - at[u];
+      const float up = top[u] - mr[u] > slack ? top[u] : mr[u], at = fmaf(up, c2, -Half<T>::kLift2);
+      const bool was = beyond(u), is = !(fabsf(at) < kFar);
+      const float by = was ? is ? (mr[u] - up) * c2 : fmaf(mr[u], c2, -at) - Half<T>::kLift2
+                           : is ? fmaf(-up, c2, mc[u]) + Half<T>::kLift2 : mc[u] - at;
       const float shrink = mr[u] > -__builtin_inff() ? __builtin_amdgcn_exp2f(by) : 0.f;
-      mr[u] = up[u];
-      mc[u] = fmaxf(at[u], kLowest);
+      mr[u] = up;
+      mc[u] = fmaxf(at, kLowest);
+      out = out || (is && up > -__builtin_inff());
       l[u] *= shrink;
 #pragma unroll
       for (int f = 0; f < NF; ++f) o[u][f] *= shrink;
     }
+    far = __any(out);
   };
 
   // ---- one strip of 32 keys of a stage
@@ -890,10 +889,11 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
     if (__any(grown)) grow(top);
     if (far) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u) {
+        const float less = beyond(u) ? fmaxf(mr[u], kLowest) : 0.f, off = beyond(u) ? -Half<T>::kLift2 : mc[u];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          p[u][j] = __builtin_amdgcn_exp2f(fmaf(p[u][j] - fmaxf(mr[u], kLowest), c2, Half<T>::kLift2));
+        for (int j = 0; j < 8; ++j) p[u][j] = __builtin_amdgcn_exp2f(fmaf(p[u][j] - less, c2, -off));
+      }
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -981,8 +981,8 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
     if (far) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float less = fmaxf(mr[u], kLowest);
-        off[u] = -Half<T>::kLift2;
+        const float less = beyond(u) ? fmaxf(mr[u], kLowest) : 0.f;
+        if (beyond(u)) off[u] = -Half<T>::kLift2;
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[u][j] -= less;
       }
@@ -1120,8 +1120,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_tree_attention_wide(TreeAttnArgs 
     const uint32_t r = row0 + 16 * u;
     if (r >= g->rows) continue;
     // sums of weights 2^((p - mr) c2 + lift), whichever way they were taken
-    const float fix = far || !(mr[u] > -__builtin_inff())
-                          ? 1.f : __builtin_amdgcn_exp2f(fmaf(-mr[u], c2, mc[u]) + Half<T>::kLift2);
+    const float fix = beyond(u) ? 1.f : __builtin_amdgcn_exp2f(fmaf(-mr[u], c2, mc[u]) + Half<T>::kLift2);
     if (sh.parts == 1) {
       const uint32_t head = h * group + (r - node[u] * group);
       T *dst = static_cast<T *>(g->a.d_out) + b * g->a.out_batch + node[u] * g->a.out_node + head * g->a.out_head;

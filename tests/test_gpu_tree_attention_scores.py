@@ -244,3 +244,20 @@ def test_infinite_cached_values(E, shape, dt):
     assert not bad[b][..., rest].any()
     others = [i for i in range(c.B) if i != b]
     assert torch.equal(out[others], base[others])
+
+
+@pytest.mark.parametrize("x", [float("inf"), 1e4])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("shape", [s for s in SHAPES if SHAPES[s][1] > 1])
+def test_keys_that_a_row_does_not_see(E, shape, dt, x):
+    """Scores of infinity, or large ones, in other rows change nothing, to the bit."""
+    say("attention, keys of other rows", shape, dt, x)
+    c = Case(*SHAPES[shape], dt, seed=50)
+    j = c.T // 2
+    c.seen[:, j, j] = True
+    base, lse = c.run(E)
+    c.kn[:, j, :, 5] = x
+    out, l2 = c.run(E)
+    sees = torch.from_numpy(c.seen[:, :, j]).cuda()
+    assert bool(sees.any()) and not bool(sees.all())
+    assert torch.equal(out[~sees], base[~sees]) and torch.equal(l2[~sees], lse[~sees])
