@@ -34,10 +34,10 @@
 // 80 values).
 // In the wide kernel the second product would cost more than half as much again
 // (64 nodes over 131072 tokens: 197 us, 306 with it): there P is rounded, an
-// error of 2^-9 of each weight for BF16, as large as the result's rounding. Sums,
-// m, l and o are fp32. A row's m only
-// moves when a strip exceeds it by more than 8 (a factor of 2^8, far inside
-// fp32 and both 16-bit ranges), which makes rescaling rare.
+// error of up to 2^-8 of each weight for BF16, like the result's rounding. Sums,
+// m, l and o are fp32. A row's m only moves when a strip of its own scores exceeds
+// it by more than 8 (a factor of 2^8, far inside fp32 and both 16-bit ranges),
+// which makes rescaling rare.
 //
 // The work is cut into equal parts over all sequences (share_of), so that one
 // long history fills the device as well as many short ones do; a second kernel
