@@ -438,6 +438,43 @@ typedef struct enc_qk_args {
  * at most 2^31 - 1. Asynchronous. */
 enc_status enc_qk_norm_rope(const enc_qk_args *h_args, void *stream);
 
+/* What lies between a block's last product and the next one's first, one
+ * launch; for every row, of `width` values:
+ *   z  = y                                          (the block's result)
+ *   z  = y * rsqrt(mean(y^2) + eps) * w_post        (with ENC_BLOCK_POST_NORM)
+ *   h' = h_scale * h + y_scale * g * z              (the residual stream)
+ *   x  = h' * rsqrt(mean(h'^2) + eps) * w_pre       (the next block's input)
+ * g is row token / gate_every of the gates: gate_every = 1 for a gate of each
+ * token, the tokens of a sequence for one of each sequence, at least `tokens`
+ * for one of each channel alone. Weights that are NULL count as ones, with
+ * ENC_BLOCK_UNIT_OFFSET a weight w counts as 1 + w, without gates g is 1, and
+ * without d_y z is 0. Everything is computed in fp32 (squares too: a row whose
+ * squares pass fp32 has an infinite mean), h' and x are rounded once, each to
+ * its own type, and x is taken from h' before that rounding. */
+enum { ENC_BLOCK_POST_NORM = 1, ENC_BLOCK_UNIT_OFFSET = 2 };
+typedef struct enc_block_norm_args {
+  const void *d_y;                 /* [tokens, width] of y_dtype, or NULL */
+  const void *d_h;                 /* [tokens, width] of h_dtype */
+  const void *d_gate;              /* [ceil(tokens / gate_every), width] of g_dtype, or NULL */
+  const void *d_w_post, *d_w_pre;  /* [width] of w_dtype, or NULL */
+  void *d_h_out;                   /* h', [tokens, width] of h_dtype, or NULL */
+  void *d_out;                     /* x, [tokens, width] of out_dtype, or NULL */
+  uint64_t y_token, h_token, gate_row, h_out_token, out_token; /* strides */
+  uint32_t tokens, width, gate_every;
+  uint32_t y_dtype, h_dtype, g_dtype, w_dtype, out_dtype; /* 1 BF16, 2 FP16, 3 FP32; of absent arrays not read */
+  uint32_t flags;
+  float eps, h_scale, y_scale;
+} enc_block_norm_args;
+
+/* width up to 32768, any number; rows need no alignment beyond their type's
+ * (they are read in 16-byte pieces where bases, strides and width allow it).
+ * d_h_out may be d_h itself (same strides); otherwise outputs must not overlap
+ * inputs or each other. A norm's weight or a gate without what it belongs to
+ * (d_w_post without the flag, d_gate or the flag without d_y, d_w_pre without
+ * d_out) is ENC_ERR_INVALID_ARG. tokens = 0 does nothing; at most 2^31 - 1.
+ * Asynchronous. */
+enc_status enc_block_norm(const enc_block_norm_args *h_args, void *stream);
+
 /* Attention of a tree's nodes over a paged cache and the tree itself:
  *   out[b,i,h] = sum_j softmax_j(scale * q[b,i,h] . k_j) v_j
  * where j runs over the sequence's cached tokens and over the nodes that

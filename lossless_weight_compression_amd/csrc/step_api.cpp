@@ -122,6 +122,47 @@ enc_status enc_qk_norm_rope(const enc_qk_args *a, void *stream) {
   return after_launch(launch_qk_norm_rope(k, (hipStream_t)stream), (hipStream_t)stream, "enc_qk_norm_rope");
 }
 
+enc_status enc_block_norm(const enc_block_norm_args *a, void *stream) {
+  set_error(ENC_OK, "%s", "");
+  if (!a) return invalid("args is NULL");
+  if (a->flags & ~(ENC_BLOCK_POST_NORM | ENC_BLOCK_UNIT_OFFSET)) return invalid("unknown flags");
+  if (!a->width) return invalid("width is 0");
+  if (a->width > 32768) return unsupported("width above 32768");
+  if (!(a->eps >= 0.f && std::isfinite(a->eps))) return invalid("eps must be finite and >= 0");
+  if (!std::isfinite(a->h_scale) || !std::isfinite(a->y_scale)) return invalid("h_scale and y_scale must be finite");
+  if (a->tokens == 0) return ENC_OK;
+  if (a->tokens > 0x7FFFFFFFu) return unsupported("tokens above 2^31 - 1");
+  if (!a->d_h || (!a->d_h_out && !a->d_out)) return invalid("h is NULL, or no output is asked for");
+  if (!a->d_y && (a->d_gate || (a->flags & ENC_BLOCK_POST_NORM))) return invalid("a gate or a norm of y without y");
+  if (a->d_w_post && !(a->flags & ENC_BLOCK_POST_NORM)) return invalid("w_post without ENC_BLOCK_POST_NORM");
+  if (a->d_w_pre && !a->d_out) return invalid("w_pre without out");
+  if (a->d_gate && !a->gate_every) return invalid("gate_every is 0");
+  const struct {
+    const void *p;
+    uint32_t dtype;
+    uint64_t stride;
+    bool out;
+  } arrays[] = {{a->d_y, a->y_dtype, a->y_token, false},        {a->d_h, a->h_dtype, a->h_token, false},
+                {a->d_gate, a->g_dtype, a->gate_row, false},    {a->d_w_post, a->w_dtype, 0, false},
+                {a->d_w_pre, a->w_dtype, 0, false},             {a->d_h_out, a->h_dtype, a->h_out_token, true},
+                {a->d_out, a->out_dtype, a->out_token, true}};
+  bool vec = a->width % 8 == 0;
+  for (const auto &x : arrays) {
+    if (!x.p) continue;
+    if (x.dtype - 1u > 2u) return unsupported("unknown dtype");
+    if (!aligned(x.p, value_bytes(x.dtype))) return invalid("a misaligned array");
+    if (x.stride >> 40) return unsupported("a stride of 2^40 or more");
+    if (x.out && a->tokens > 1 && x.stride < a->width) return invalid("rows of an output overlap");
+    vec = vec && aligned(x.p, 16) && x.stride % (16 / value_bytes(x.dtype)) == 0;
+  }
+  BlockNormKernelArgs k;
+  k.a = *a;
+  k.gate = FastDiv::of(a->d_gate ? a->gate_every < 0x80000000u ? a->gate_every : 0x7FFFFFFFu : 1);
+  k.vec = vec;
+  k.token0 = 0;
+  return after_launch(launch_block_norm(k, (hipStream_t)stream), (hipStream_t)stream, "enc_block_norm");
+}
+
 uint64_t enc_tree_attention_workspace_bytes(const enc_tree_attention_args *a) {
   set_error(ENC_OK, "%s", "");
   if (check_attention(a) != ENC_OK || a->batch == 0) return 0;

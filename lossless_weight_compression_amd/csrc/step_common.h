@@ -1,5 +1,5 @@
 // step_common.h -- definitions shared by the kernels of one decoding step
-// (qk_rope, tree_attention, verify_tree, cache_pages) and their host side.
+// (qk_rope, block_norm, tree_attention, verify_tree, cache_pages) and their host side.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -58,6 +58,14 @@ struct QkKernelArgs {
   uint32_t token0;     // this launch's first
 };
 hipError_t launch_qk_norm_rope(const QkKernelArgs &k, hipStream_t s);
+
+struct BlockNormKernelArgs {
+  enc_block_norm_args a;
+  FastDiv gate;        // tokens to a row of gates
+  uint32_t vec;        // all rows and weights 16-byte aligned, width a multiple of 8
+  uint32_t token0;     // this launch's first
+};
+hipError_t launch_block_norm(const BlockNormKernelArgs &k, hipStream_t s);
 
 struct TreeAttnArgs {
   enc_tree_attention_args a;

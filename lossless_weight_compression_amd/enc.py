@@ -80,6 +80,15 @@ class EncQkArgs(ctypes.Structure):
         + [("eps", ctypes.c_float), ("reserved", ctypes.c_uint32)])
 
 
+class EncBlockNormArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in (
+        "d_y", "d_h", "d_gate", "d_w_post", "d_w_pre", "d_h_out", "d_out")]
+        + [(n, ctypes.c_uint64) for n in ("y_token", "h_token", "gate_row", "h_out_token", "out_token")]
+        + [(n, ctypes.c_uint32) for n in (
+            "tokens", "width", "gate_every", "y_dtype", "h_dtype", "g_dtype", "w_dtype", "out_dtype", "flags")]
+        + [(n, ctypes.c_float) for n in ("eps", "h_scale", "y_scale")])
+
+
 class EncTreeAttentionArgs(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in (
         "d_q", "d_k_new", "d_v_new", "d_k_cache", "d_v_cache", "d_out", "d_lse", "d_table", "d_lens",
@@ -146,6 +155,7 @@ SIGNATURES = {
     "enc_gemm_dense_nt": (_ST, [_VP, _U32, _U32, _VP, _U32, _VP, _VP, _U64, _VP]),
     "enc_stream_probe": (_ST, [_VP, _U64, _VP, _U64, _U32, _U32, _VP]),
     "enc_qk_norm_rope": (_ST, [ctypes.POINTER(EncQkArgs), _VP]),
+    "enc_block_norm": (_ST, [ctypes.POINTER(EncBlockNormArgs), _VP]),
     "enc_tree_attention_workspace_bytes": (_U64, [ctypes.POINTER(EncTreeAttentionArgs)]),
     "enc_tree_attention": (_ST, [ctypes.POINTER(EncTreeAttentionArgs), _VP, _U64, _VP]),
     "enc_verify_tree_workspace_bytes": (_U64, [_U32, _U32, _U32]),
@@ -586,6 +596,7 @@ def enc_stream_probe(src, dst, items_per_thread=1, threads_per_workgroup=256, st
 # ------------------------------------------------------ one decoding step
 ENC_TREE_MAX_NODES = 256
 ENC_ROPE_ADJACENT, ENC_QK_NO_NORM = 1, 2
+ENC_BLOCK_POST_NORM, ENC_BLOCK_UNIT_OFFSET = 1, 2
 _codes = {}
 _I32 = _I64 = _F32 = _BF16 = _current_device = None
 
@@ -601,6 +612,7 @@ def _load_types():
 
 # the argument structs in one go (field by field costs about 0.1 us each)
 _QK_PACK = struct.Struct("=22Q10IfI").pack
+_BLOCK_PACK = struct.Struct("=12Q9I3f").pack
 _ATTN_PACK = struct.Struct("=27Q10IfI").pack
 _VERIFY_PACK = struct.Struct("=13Q4I").pack
 
@@ -724,6 +736,68 @@ def enc_qk_norm_rope(q, k, v, positions, table, q_weight=None, k_weight=None, ep
         tokens, q_heads, kv_shape[1], dim, rot, max_pos, _code(q.dtype), _code(dtype), w_code, flags, eps, 0))
     _check(lib().enc_qk_norm_rope(ctypes.byref(a), _handle(stream, device)))
     return qo, ko, vo
+
+
+def enc_block_norm(h, y=None, gate=None, w_post=None, w_pre=None, post_norm=False, pre_norm=True, h_scale=1.0,
+                   y_scale=1.0, eps=1e-6, unit_offset=False, h_out=None, out=None, out_dtype=None, stream=None):
+    """Residual sum and norms between two blocks. h: [tokens, width] residual
+    stream; y: [tokens, width] the last block's rows, or None; gate: [width] or
+    [rows, width], rows dividing tokens (row i for tokens i * tokens / rows on),
+    or None; w_post (with post_norm), w_pre: [width] of one type, or None for
+    ones. Each of its own floating type, any row stride. Returns (h', x): h' =
+    h_scale h + y_scale gate norm(y) in h's type (h_out, which may be h; h
+    itself where y is None and h_scale 1, unless h_out is given), x = norm(h')
+    in out_dtype (out; bfloat16 if neither is given), None without pre_norm."""
+    device = _device_of(h)
+    tokens, width = shape = h.shape
+    h_code = _code(h.dtype)
+    hs = _values(h, "h", h.dtype, shape, device)
+    yp = gp = qp = pp = hop = op = 0
+    ys, gs, hos, os = 0, 0, 0, 0
+    y_code = g_code = w_code = out_code = 0
+    every = 1
+    if y is not None:
+        ys, yp, y_code = _values(y, "y", y.dtype, shape, device)[0], y.data_ptr(), _code(y.dtype)
+    if gate is not None:
+        g = gate if gate.dim() == 2 else gate[None]
+        rows = g.shape[0]
+        gs = _values(g, "gate", g.dtype, (rows, width), device)[0]
+        if rows == 0 and tokens or rows and tokens % rows:
+            raise ValueError("%d rows of gates for %d tokens" % (rows, tokens))
+        gp, g_code, every = g.data_ptr(), _code(g.dtype), max(tokens // max(rows, 1), 1)
+    if w_post is not None:
+        qp, w_code = _plain(w_post, "w_post", w_post.dtype, (width,), device), _code(w_post.dtype)
+    if w_pre is not None:
+        pp, w_code = _plain(w_pre, "w_pre", w_pre.dtype, (width,), device), _code(w_pre.dtype)
+        if w_post is not None and w_post.dtype is not w_pre.dtype:
+            raise TypeError("the weights must have one type")
+    if not pre_norm and (out is not None or w_pre is not None):
+        raise ValueError("out or w_pre without pre_norm")
+    writes_h = y is not None or h_scale != 1.0 or h_out is not None
+
+    def room():
+        return (h.new_empty(shape) if writes_h and h_out is None else h_out,
+                h.new_empty(shape, dtype=out_dtype or _BF16) if pre_norm and out is None else out)
+
+    if stream is None:
+        ho, x = room()
+    else:
+        with _on(stream):
+            ho, x = room()
+    if writes_h:
+        hos, hop = _values(ho, "h_out", h.dtype, shape, device)[0], ho.data_ptr()
+    else:
+        ho = h
+    if x is not None:
+        os, op, out_code = _values(x, "out", x.dtype, shape, device)[0], x.data_ptr(), _code(x.dtype)
+    if not writes_h and x is None:
+        return ho, None
+    flags = (ENC_BLOCK_POST_NORM if post_norm else 0) | (ENC_BLOCK_UNIT_OFFSET if unit_offset else 0)
+    a = EncBlockNormArgs.from_buffer_copy(_BLOCK_PACK(
+        yp, h.data_ptr(), gp, qp, pp, hop, op, ys, hs[0], gs, hos, os, tokens, width, every, y_code, h_code, g_code,
+        w_code, out_code, flags, eps, h_scale, y_scale))
+    _check(lib().enc_block_norm(ctypes.byref(a), _handle(stream, device)))
+    return ho, x
 
 
 def enc_tree_attention_workspace_bytes(q, k_new, table, k_cache):
