@@ -563,6 +563,45 @@ typedef struct enc_verify_args {
 uint64_t enc_verify_tree_workspace_bytes(uint32_t batch, uint32_t nodes, uint32_t vocab);
 enc_status enc_verify_tree(const enc_verify_args *h_args, void *d_ws, uint64_t ws_bytes, void *stream);
 
+/* Temperature, top-k, top-p and min-p on rows of logits l, the next token from
+ * a given random number, and the filtered probabilities. For each row, with
+ * weights e_i = exp(l_i / T - max_j l_j / T) and the tokens in the order of
+ * their logits (descending, ties by index):
+ *   top-k  keeps the first k of the order;
+ *   top-p  keeps, of those, the shortest front part whose weights reach p times
+ *          the sum of those weights;
+ *   min-p  keeps those with e_i >= min_p;
+ * what all three keep is kept, and the first of the order always is.
+ *   d_probs: e_i / (sum of the kept e), 0 for what is not kept
+ *   d_token: the smallest t with sum_{i <= t, kept} e_i > u * (sum of the kept e)
+ * A setting that is NULL is off; so are top_k <= 0 or >= vocab, top_p >= 1 or
+ * NaN, min_p <= 0 or NaN. Temperature NULL counts as 1; 0, below or NaN keeps the
+ * first of the order alone. u is clamped to [0, 1] (NaN: 0; if no t is left by
+ * rounding or with 1, the last kept one). Logits of NaN or -infinity are never
+ * kept; with +infinity among them those weigh 1 and all others nothing; a row
+ * with nothing to keep has token -1 and probabilities 0. Weights below e^-47
+ * may count as 0. Sums are taken in fp64, in bins whole numbers of 2^-32 of a
+ * weight, always in the same order: equal rows give equal bits. */
+typedef struct enc_sample_args {
+  const void *d_logits;            /* [rows, vocab] of dtype */
+  const float *d_u;                /* [rows], may be NULL without d_token */
+  const float *d_temperature, *d_top_p, *d_min_p; /* [ceil(rows / rows_per_setting)], or NULL */
+  const int32_t *d_top_k;          /* the same */
+  int32_t *d_token;                /* [rows], or NULL */
+  void *d_probs;                   /* [rows, vocab] of probs_dtype, or NULL */
+  uint64_t logits_row, probs_row;  /* strides */
+  uint32_t rows, vocab, rows_per_setting; /* row r has setting r / rows_per_setting */
+  uint32_t dtype, probs_dtype;     /* 1 BF16, 2 FP16, 3 FP32 */
+  uint32_t reserved;               /* 0 */
+} enc_sample_args;
+
+/* vocab up to 2^22, rows up to 2^20; rows need no alignment beyond their
+ * type's. d_probs must not overlap d_logits. The workspace may hold anything;
+ * its size does not depend on the settings and stops growing at 1024 rows.
+ * Asynchronous. */
+uint64_t enc_sample_workspace_bytes(uint32_t rows, uint32_t vocab);
+enc_status enc_sample(const enc_sample_args *h_args, void *d_ws, uint64_t ws_bytes, void *stream);
+
 /* Pages of a cache. n_planes arrays of pages (2 per layer, K and V; any
  * element type) share one table: token t of sequence s is row t % page_size
  * of page d_table[s][t / page_size] in every plane. d_refs counts the

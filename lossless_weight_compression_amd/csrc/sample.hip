@@ -1,0 +1,824 @@
+// sample.hip -- temperature, top-k, top-p and min-p on rows of logits, the next
+// token from a given random number, and the filtered probabilities
+// (enc_sample).
+//
+// With x = l / T and the tokens of a row in the order of their logits
+// (descending, ties by index), each filter keeps a front part of the order, so
+// what is kept ends at one token: the cut. Nothing is sorted. A first pass puts
+// every token into one of 768 bins of 1/16 in x below the row's greatest, counts
+// them and sums their weights e^x; cumulative counts and sums name the bins in
+// which the cuts lie; only those bins' tokens (some hundred) are gathered, by a
+// second pass, and selected from.
+//
+// Sums: bin edges are whole multiples of 1/16 in x itself, not below the
+// greatest, so that segments of a row, which do not know the row's greatest,
+// count into the same bins. Within a bin a weight is taken relative to the
+// bin's lower edge, 1 <= w < 1.065, and held as a whole number of 2^-32: sums in a bin
+// are exact in any order (in fp64 too, for 2^20 tokens, so that borders between
+// equal logits are met exactly), and a count and a sum fit one 64-bit word of
+// LDS. Across bins sums are fp64, always in the same order. The borders between
+// tokens are finer than fp32: in 128256 tokens a cumulative sum that is off by
+// 1e-8 draws another token once in a thousand calls; here it is some 1e-12.
+//
+// Steps, each a launch: k_scan (rows x segments), k_plan (rows), k_collect (rows
+// x segments with something to gather), k_resolve (rows; the cut, the draw),
+// k_probs (rows x segments). Where more than 4096 tokens lie in a cut's bins
+// (many equal logits, a high temperature), k_resolve reads the row itself.
+#include "step_common.h"
+
+#include "group_math.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace enc {
+namespace {
+
+typedef unsigned long long u64;
+constexpr uint32_t kBins = kSampleBins, kList = kSampleList, kWide = 1024;
+constexpr double kUnit = 1.0 / 4294967296.0;   // 2^-32
+constexpr u64 kOne = 1ull << 32, kSumMask = (1ull << 49) - 1;
+constexpr uint32_t kNoBin = ~0u;
+
+// Keys: greater for tokens earlier in the order; never 0.
+__device__ __forceinline__ u64 key_of(float l, uint32_t i) {
+  const uint32_t u = __float_as_uint(l + 0.f);   // -0 counts as 0
+  return (u64)(u & 0x80000000u ? ~u : u | 0x80000000u) << 32 | (uint32_t)~i;
+}
+__device__ __forceinline__ float logit_of(u64 key) {
+  const uint32_t u = (uint32_t)(key >> 32);
+  return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+__device__ __forceinline__ uint32_t index_of(u64 key) { return ~(uint32_t)key; }
+// NaN and -infinity are never kept.
+__device__ __forceinline__ bool counts(float l) { return l > -__builtin_inff(); }
+
+// Place in units of 1/16 of x, rounded to a multiple of 2^-30 (2^-35 of a weight):
+// logits that differ by less, around 0 on both sides of a bin's edge, weigh the
+// same to the bit. +infinity lies above everything finite.
+__device__ __forceinline__ double place_of(float l, double r16) {
+  constexpr double kRound = 6291456.0;   // 3 2^21: one unit in its last place is 2^-30
+  return l == __builtin_inff() ? 1e300 : fma((double)l, r16, kRound) - kRound;
+}
+// e^(f / 16) - 1 for 0 <= f < 1 in units of 2^-32 (the next term is below 2^-40).
+__device__ __forceinline__ u64 excess_of(double f) {
+  const double z = f * 0.0625;
+  double s = 1.0 / 720.0;
+  s = fma(s, z, 1.0 / 120.0);
+  s = fma(s, z, 1.0 / 24.0);
+  s = fma(s, z, 1.0 / 6.0);
+  s = fma(s, z, 0.5);
+  s = fma(s, z, 1.0);
+  // the low bits of 2^52 + n are n
+  return (u64)__double_as_longlong(fma(s * z, 4294967296.0, 4503599627370496.0)) & ((1ull << 52) - 1);
+}
+
+struct Setting {
+  double r16;        // 16 / temperature
+  double top_p, min_p;
+  uint32_t top_k;    // 0: all
+  bool first;        // only the first of the order
+};
+__device__ __forceinline__ Setting setting_of(const enc_sample_args &a, uint32_t row) {
+  const uint32_t i = row / a.rows_per_setting;
+  Setting s;
+  const float t = a.d_temperature ? a.d_temperature[i] : 1.f;
+  s.first = !(t > 0.f);
+  s.r16 = s.first ? 16.0 : 16.0 / (double)t;
+  const int32_t k = a.d_top_k ? a.d_top_k[i] : 0;
+  s.top_k = k > 0 && (uint32_t)k < a.vocab ? (uint32_t)k : 0;
+  const float p = a.d_top_p ? a.d_top_p[i] : 1.f;
+  s.top_p = p < 1.f ? (double)p : 1.0;
+  const float m = a.d_min_p ? a.d_min_p[i] : 0.f;
+  s.min_p = m > 0.f ? (double)m : 0.0;
+  s.first = s.first || s.top_k == 1 || s.top_p <= 0.0 || s.min_p > 1.0;
+  return s;
+}
+
+// ---- a row in 16-byte pieces: piece boundaries are those of memory, so element
+// i of the row is place i + head of the row's pieces
+template <typename T> constexpr uint32_t kPiece = 16 / sizeof(T);
+template <typename T> __device__ __forceinline__ uint32_t head_of(const T *row) {
+  return (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T);
+}
+template <typename T> __device__ __forceinline__ float value_at(const T *row, uint32_t i) { return (float)row[i]; }
+
+template <typename T>
+__device__ __forceinline__ uint4 load_piece(const T *row, uint32_t head, uint32_t vocab, uint32_t at) {
+  constexpr uint32_t E = kPiece<T>;
+  if (at >= head && at + E <= head + vocab) return *reinterpret_cast<const uint4 *>(row + ((int64_t)at - head));
+  uint32_t w[4];
+#pragma unroll
+  for (uint32_t e = 0; e < 4; ++e) {   // -infinity where there is no element
+    if constexpr (sizeof(T) == 4) {
+      const uint32_t v = at + e;
+      w[e] = v >= head && v < head + vocab ? reinterpret_cast<const uint32_t *>(row)[v - head] : 0xFF800000u;
+    } else {
+      constexpr uint32_t kNone = std::is_same<T, __bf16>::value ? 0xFF80u : 0xFC00u;
+      const uint32_t v = at + 2 * e;
+      const uint16_t *p = reinterpret_cast<const uint16_t *>(row);
+      const uint32_t lo = v >= head && v < head + vocab ? p[v - head] : kNone;
+      const uint32_t hi = v + 1 >= head && v + 1 < head + vocab ? p[v + 1 - head] : kNone;
+      w[e] = lo | hi << 16;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T> __device__ __forceinline__ void values_of(uint4 piece, float (&x)[kPiece<T>]) {
+  const uint32_t w[4] = {piece.x, piece.y, piece.z, piece.w};
+#pragma unroll
+  for (uint32_t e = 0; e < kPiece<T>; ++e) {
+    if constexpr (sizeof(T) == 4)
+      x[e] = __uint_as_float(w[e]);
+    else
+      x[e] = half_of<T>(w[e >> 1], e & 1);
+  }
+}
+
+__device__ __forceinline__ u64 wave_max(u64 v) {
+  for (uint32_t o = 32; o; o >>= 1) {
+    const u64 w = __shfl_xor(v, o);
+    v = w > v ? w : v;
+  }
+  return v;
+}
+
+template <typename V> __device__ __forceinline__ V wave_scan(V v) {   // inclusive
+  const uint32_t lane = threadIdx.x & 63;
+  for (uint32_t o = 1; o < 64; o <<= 1) {
+    const V w = __shfl_up(v, o);
+    if (lane >= o) v += w;
+  }
+  return v;
+}
+// Inclusive scan over a workgroup of kWide; `side` has room for 16 and is free
+// again after the call's last barrier.
+template <typename V> __device__ __forceinline__ V group_scan(V v, V *side) {
+  v = wave_scan(v);
+  const uint32_t wave = threadIdx.x >> 6;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 63) side[wave] = v;
+  __syncthreads();
+  V before = 0;
+  for (uint32_t w = 0; w < wave; ++w) before += side[w];
+  return before + v;
+}
+
+// ---- first pass: a segment's greatest key, and its bins
+template <typename T, uint32_t NT, uint32_t NV>
+__global__ __launch_bounds__(NT) void k_scan(SampleKernelArgs k) {
+  constexpr uint32_t E = kPiece<T>, S = NT * NV * E;
+  const enc_sample_args &a = k.a;
+  __shared__ u64 bins[kBins];
+  __shared__ u64 tops[NT / 64];
+  __shared__ uint32_t last;
+  const uint32_t tid = threadIdx.x, r = blockIdx.x / k.segments, seg = blockIdx.x - r * k.segments;
+  const uint32_t row = k.row0 + r;
+  const T *l = static_cast<const T *>(a.d_logits) + (uint64_t)row * a.logits_row;
+  const uint32_t head = head_of(l);
+  uint4 piece[NV];
+#pragma unroll
+  for (uint32_t j = 0; j < NV; ++j) piece[j] = load_piece(l, head, a.vocab, seg * S + (j * NT + tid) * E);
+  const Setting set = setting_of(a, row);
+  for (uint32_t i = tid; i < kBins; i += NT) bins[i] = 0;
+  if (tid == 0) last = 0;
+
+  u64 top = 0;
+#pragma unroll
+  for (uint32_t j = 0; j < NV; ++j) {
+    float x[E];
+    values_of<T>(piece[j], x);
+#pragma unroll
+    for (uint32_t e = 0; e < E; ++e)
+      if (counts(x[e])) {
+        const u64 key = key_of(x[e], seg * S + (j * NT + tid) * E + e - head);
+        top = key > top ? key : top;
+      }
+  }
+  top = wave_max(top);
+  if ((tid & 63) == 0) tops[tid >> 6] = top;
+  __syncthreads();
+  for (uint32_t w = 0; w < NT / 64; ++w) top = tops[w] > top ? tops[w] : top;
+  SampleSegment *out = k.segs + (uint64_t)r * k.segments + seg;
+  if (tid == 0) {
+    out->top = top;
+    out->bins = 0;
+  }
+  if (top == 0 || set.first) return;   // nothing in it, or nothing but the first is asked for
+  const double edge = floor(place_of(logit_of(top), set.r16));
+#pragma unroll
+  for (uint32_t j = 0; j < NV; ++j) {
+    float x[E];
+    values_of<T>(piece[j], x);
+#pragma unroll
+    for (uint32_t e = 0; e < E; ++e) {
+      const double t = place_of(x[e], set.r16), at = floor(t), below = edge - at;
+      if (counts(x[e]) && below < (double)kBins) atomicAdd(&bins[(uint32_t)below], (1ull << 49) + excess_of(t - at));
+    }
+  }
+  __syncthreads();
+  u64 *dst = k.bins + ((uint64_t)r * k.segments + seg) * kBins;
+  uint32_t used = 0;
+  for (uint32_t i = tid; i < kBins; i += NT) {
+    const u64 v = bins[i];
+    if (v) used = i + 1;
+  }
+  atomicMax(&last, used);
+  __syncthreads();
+  used = last;
+  for (uint32_t i = tid; i < used; i += NT) dst[i] = bins[i];
+  if (tid == 0) {
+    out->edge = edge;
+    out->bins = used;
+  }
+}
+
+// ---- per row: the bins of all segments, and where the cuts lie
+__global__ __launch_bounds__(kWide) void k_plan(SampleKernelArgs k) {
+  const enc_sample_args &a = k.a;
+  __shared__ u64 tops[kWide / 64];
+  __shared__ double sums[kBins], side[kWide / 64];
+  __shared__ uint32_t numbers[kBins], side_n[kWide / 64];
+  __shared__ uint32_t k_bin, p_low, p_high;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = blockIdx.x, row = k.row0 + r;
+  SampleSegment *segs = k.segs + (uint64_t)r * k.segments;
+  const Setting set = setting_of(a, row);
+  SampleRow &out = k.rows[r];
+
+  u64 top = 0;
+  for (uint32_t s = tid; s < k.segments; s += kWide) top = max(top, segs[s].top);
+  top = wave_max(top);
+  if (lane == 0) tops[wave] = top;
+  if (tid == 0) k_bin = p_low = p_high = kBins - 1;
+  __syncthreads();
+  for (uint32_t w = 0; w < kWide / 64; ++w) top = max(top, tops[w]);
+  const double t_max = place_of(logit_of(top), set.r16), edge = floor(t_max);
+  if (tid == 0) {
+    out.edge = edge;
+    out.r16 = set.r16;
+    out.top = top;
+    out.n = 0;
+    out.cut_bin = 0;
+    out.tau = top;
+    out.z = 0.0;
+    out.state = top == 0 ? kSampleEmpty : kSampleFirst;
+  }
+  if (top == 0 || set.first) return;
+
+  u64 sum = 0;
+  uint32_t number = 0;
+  if (tid < kBins)
+    for (uint32_t s = 0; s < k.segments; ++s) {
+      const double by = edge - segs[s].edge;
+      if (!(segs[s].bins && by < (double)kBins)) continue;
+      const uint32_t at = tid - (uint32_t)by;   // wraps where the segment has no such bin
+      if (at < segs[s].bins) {
+        const u64 v = k.bins[((uint64_t)r * k.segments + s) * kBins + at];
+        number += (uint32_t)(v >> 49);
+        sum += v & kSumMask;
+      }
+    }
+  const double mass = tid < kBins ? ((double)number + (double)sum * kUnit) * exp((double)tid * -0.0625) : 0.0;
+  const double upto = group_scan(mass, side);
+  const uint32_t n_upto = group_scan(number, side_n);
+  if (tid < kBins) {
+    sums[tid] = upto;
+    numbers[tid] = n_upto;
+    k.sums[(uint64_t)r * kBins + tid] = upto;
+  }
+  __syncthreads();
+  // the bin that a count or a sum is reached in (sums grow: each test is true once)
+  if (set.top_k && tid < kBins && n_upto >= set.top_k && n_upto - number < set.top_k) k_bin = tid;
+  __syncthreads();
+  const uint32_t kb = k_bin;
+  const bool k_part = set.top_k && numbers[kb] > set.top_k;
+  if (set.top_p < 1.0 && tid < kBins) {
+    const double low = set.top_p * (k_part ? kb ? sums[kb - 1] : 0.0 : sums[kb]), high = set.top_p * sums[kb];
+    const double before = tid ? sums[tid - 1] : 0.0;
+    if (upto >= low && (tid == 0 || before < low)) p_low = tid;
+    if (upto >= high && (tid == 0 || before < high)) p_high = tid;
+  }
+  __syncthreads();
+  uint32_t bk = k_part ? kb : kNoBin, lo = set.top_p < 1.0 ? p_low : kNoBin, hi = set.top_p < 1.0 ? min(p_high, kb) : kb;
+  if (lo != kNoBin) lo = min(lo, hi);
+  double t_min = -1e308;
+  uint32_t bm = kNoBin;
+  if (set.min_p > 0.0) {
+    t_min = t_max + 16.0 * log(set.min_p);
+    const double below = edge - floor(t_min);
+    if (below < (double)kBins) bm = (uint32_t)below;
+    if (bm != kNoBin && bm > min(hi, kb)) bm = kNoBin;                   // another filter ends before it
+    if (bm != kNoBin && bm < min(bk, lo) && (lo != kNoBin || bk != kNoBin)) bk = lo = kNoBin;   // it ends before the others
+    if (bm != kNoBin && bk == kNoBin && lo == kNoBin) hi = bm;
+  }
+  // tokens to gather, and every segment's place in the list
+  const auto wanted = [&](uint32_t i) { return i == bk || i == bm || (lo != kNoBin && i >= lo && i <= hi); };
+  uint32_t total = 0;
+  if (bk != kNoBin || bm != kNoBin || lo != kNoBin) {
+    uint32_t mine = 0;
+    if (tid < kBins && wanted(tid)) mine = number;
+    total = group_scan(mine, side_n);
+    __syncthreads();
+    if (tid == kWide - 1) side_n[0] = total;
+    __syncthreads();
+    total = side_n[0];
+    if (total <= kList) {
+      uint32_t base = 0;
+      for (uint32_t s0 = 0; s0 < k.segments; s0 += kWide) {
+        // a wave counts a segment's wanted bins; then a scan over the segments
+        __syncthreads();
+        for (uint32_t s = s0 + wave; s < min(k.segments, s0 + kWide); s += kWide / 64) {
+          const double by = edge - segs[s].edge;
+          uint32_t c = 0;
+          if (segs[s].bins && by < (double)kBins)
+            for (uint32_t i = lane; i < segs[s].bins; i += 64)
+              if (i + (uint32_t)by < kBins && wanted(i + (uint32_t)by))
+                c += (uint32_t)(k.bins[((uint64_t)r * k.segments + s) * kBins + i] >> 49);
+          c = wave_incl_scan(c);
+          if (lane == 63) segs[s].n = c;
+        }
+        __syncthreads();
+        const uint32_t s = s0 + tid;
+        const uint32_t c = s < k.segments ? segs[s].n : 0;
+        const uint32_t incl = group_scan(c, side_n);
+        if (s < k.segments) segs[s].first = base + incl - c;
+        for (uint32_t w = 0; w < kWide / 64; ++w) base += side_n[w];
+      }
+    }
+  }
+  if (tid == 0) {
+    out.bk = bk;
+    out.lo = lo;
+    out.hi = hi;
+    out.bm = bm;
+    out.kb = kb;
+    out.rank = k_part ? set.top_k - (kb ? numbers[kb - 1] : 0) : 0;   // the last kept one's, from 1
+    out.top_p = set.top_p;
+    out.t_min = t_min;
+    out.n = total;
+    out.cut_bin = hi;   // where no list is needed: a whole bin ends what is kept
+    out.tau = 0;
+    out.z = sums[hi];
+    out.state = total == 0 ? kSampleWhole : total <= kList ? kSampleListed : kSampleRead;
+  }
+}
+
+// ---- second pass: the tokens of the cuts' bins
+template <typename T, uint32_t NT, uint32_t NV>
+__global__ __launch_bounds__(NT) void k_collect(SampleKernelArgs k) {
+  constexpr uint32_t E = kPiece<T>, S = NT * NV * E;
+  const enc_sample_args &a = k.a;
+  __shared__ uint32_t filled;
+  const uint32_t tid = threadIdx.x, r = blockIdx.x / k.segments, seg = blockIdx.x - r * k.segments;
+  const SampleRow &w = k.rows[r];
+  if (w.state != kSampleListed) return;
+  const SampleSegment &me = k.segs[(uint64_t)r * k.segments + seg];
+  if (!me.bins || !me.n) return;
+  const T *l = static_cast<const T *>(a.d_logits) + (uint64_t)(k.row0 + r) * a.logits_row;
+  const uint32_t head = head_of(l);
+  uint4 piece[NV];
+#pragma unroll
+  for (uint32_t j = 0; j < NV; ++j) piece[j] = load_piece(l, head, a.vocab, seg * S + (j * NT + tid) * E);
+  if (tid == 0) filled = 0;
+  __syncthreads();
+  const uint32_t bk = w.bk, lo = w.lo, hi = w.hi, bm = w.bm;
+  const double r16 = w.r16, edge = w.edge;
+  const uint32_t n = me.n;
+  SampleToken *dst = k.list + (uint64_t)r * kList + me.first;
+#pragma unroll
+  for (uint32_t j = 0; j < NV; ++j) {
+    float x[E];
+    values_of<T>(piece[j], x);
+#pragma unroll
+    for (uint32_t e = 0; e < E; ++e) {
+      const double t = place_of(x[e], r16), at = floor(t), below = edge - at;
+      if (!counts(x[e]) || !(below < (double)kBins)) continue;
+      const uint32_t i = (uint32_t)below;
+      if (i == bk || i == bm || (lo != kNoBin && i >= lo && i <= hi)) {
+        const uint32_t slot = atomicAdd(&filled, 1u);   // any order: what is selected does not depend on it
+        if (slot < n) dst[slot] = SampleToken{key_of(x[e], seg * S + (j * NT + tid) * E + e - head), (u64)i << 40 | excess_of(t - at)};
+      }
+    }
+  }
+}
+
+// ---- per row: the cuts among the gathered tokens, then the draw
+
+struct Select {
+  u64 keys[256];        // few enough to compare each with each
+  u64 weights[256];
+  u64 sum[256];         // of a digit's values
+  uint32_t number[256];
+  u64 any, every, tau, skipped_sum;
+  uint32_t filled, digit, skipped;
+};
+
+// Tokens of a row: those gathered, or the row itself. f(key, bin, excess).
+template <typename T> struct Tokens {
+  const SampleToken *list;   // in LDS
+  uint32_t n;
+  const T *row;              // instead, if not NULL
+  uint32_t vocab;
+  double r16, edge;
+  template <typename F> __device__ __forceinline__ void each(F f) const {
+    if (!row) {
+      for (uint32_t i = threadIdx.x; i < n; i += kWide)
+        f(list[i].key, (uint32_t)(list[i].at >> 40), list[i].at & ((1ull << 40) - 1));
+    } else {
+      for (uint32_t i = threadIdx.x; i < vocab; i += kWide) {
+        const float x = value_at(row, i);
+        const double t = place_of(x, r16), at = floor(t), below = edge - at;
+        if (counts(x) && below < (double)kBins) f(key_of(x, i), (uint32_t)below, excess_of(t - at));
+      }
+    }
+  }
+};
+
+// The key of the token of a bin, in the order, at which the count reaches `rank`
+// (from 1), or, with rank 0, the weights' sum reaches `need` (in bin units); the
+// bin's last token if neither does. First a digit of the excess, which spreads a
+// bin's tokens, then digits of the key from its highest bit that differs, until
+// 256 tokens are left, which are compared each with each.
+template <typename T>
+__device__ u64 select(const Tokens<T> &all, uint32_t bin, uint32_t rank, double need, Select &s) {
+  const uint32_t tid = threadIdx.x, lane = tid & 63;
+  u64 low = 0, high = ~0ull;   // keys still in question
+  uint32_t qd = kNoBin;        // their excess' first digit
+  uint32_t skipped = 0;        // tokens and weights before them
+  u64 skipped_sum = 0;
+  const auto live = [&](u64 key, uint32_t i, u64 q) {
+    return i == bin && key >= low && key <= high && (qd == kNoBin || (uint32_t)(q >> 21) == qd);
+  };
+  for (uint32_t round = 0;; ++round) {
+    // how many, and in which bits they differ
+    __syncthreads();
+    if (tid == 0) s.filled = 0, s.any = 0, s.every = ~0ull;
+    __syncthreads();
+    u64 any = 0, every = ~0ull;
+    uint32_t mine = 0;
+    all.each([&](u64 key, uint32_t i, u64 q) {
+      if (!live(key, i, q)) return;
+      any |= key;
+      every &= key;
+      ++mine;
+    });
+    if (mine) {
+      atomicAdd(&s.filled, mine);
+      atomicOr(&s.any, any);
+      atomicAnd(&s.every, every);
+    }
+    __syncthreads();
+    if (s.filled <= 256) break;
+    const u64 common = s.every, differ = s.any & ~common;
+    const uint32_t top_bit = 63 - __clzll((long long)differ);   // keys are distinct: some bit differs
+    const uint32_t shift = top_bit >= 7 ? top_bit - 7 : 0;
+    const bool by_excess = round == 0;
+    if (tid < 256) s.sum[tid] = 0, s.number[tid] = 0;
+    __syncthreads();
+    all.each([&](u64 key, uint32_t i, u64 q) {
+      if (!live(key, i, q)) return;
+      const uint32_t d = by_excess ? (uint32_t)(q >> 21) : (uint32_t)(key >> shift) & 255u;
+      atomicAdd(&s.number[d], 1u);
+      atomicAdd(&s.sum[d], kOne + q);
+    });
+    __syncthreads();
+    if (tid < 64) {   // digits from the highest down, four to a lane
+      uint32_t n4 = 0;
+      u64 m4 = 0;
+      for (uint32_t e = 0; e < 4; ++e) n4 += s.number[255 - 4 * lane - e], m4 += s.sum[255 - 4 * lane - e];
+      uint32_t n_at = skipped + wave_scan(n4) - n4;
+      u64 m_at = skipped_sum + wave_scan(m4) - m4;
+      uint32_t hit = kNoBin, last = kNoBin;
+      for (uint32_t e = 0; e < 4; ++e) {
+        const uint32_t d = 255 - 4 * lane - e;
+        if (!s.number[d]) continue;
+        last = d;
+        const bool reached = rank ? n_at + s.number[d] >= rank : (double)(m_at + s.sum[d]) * kUnit >= need;
+        if (reached && hit == kNoBin) hit = d;
+        if (hit == kNoBin) n_at += s.number[d], m_at += s.sum[d];
+      }
+      const u64 hits = __ballot(hit != kNoBin), lasts = __ballot(last != kNoBin);
+      // the first lane that reaches it; if none does (rounding), the last token
+      const int from = hits ? __builtin_ctzll(hits) : 63 - __builtin_clzll(lasts);
+      uint32_t d = __builtin_amdgcn_readlane(hits ? hit : last, from);
+      if (!hits) {   // everything before the last digit is passed
+        n_at = skipped, m_at = skipped_sum;
+        for (uint32_t e = 255; e > d; --e) n_at += s.number[e], m_at += s.sum[e];
+      } else {
+        n_at = __builtin_amdgcn_readlane(n_at, from);
+        m_at = (u64)(uint32_t)__builtin_amdgcn_readlane((uint32_t)m_at, from) |
+               (u64)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(m_at >> 32), from) << 32;
+      }
+      if (lane == 0) s.digit = d, s.skipped = n_at, s.skipped_sum = m_at;
+    }
+    __syncthreads();
+    skipped = s.skipped;
+    skipped_sum = s.skipped_sum;
+    if (by_excess) {
+      qd = s.digit;
+    } else {
+      const u64 same = shift + 8 < 64 ? common >> (shift + 8) << (shift + 8) : 0;   // bits above the digit
+      low = same | (u64)s.digit << shift;
+      high = low | ((1ull << shift) - 1);
+    }
+  }
+  __syncthreads();
+  if (tid == 0) s.filled = 0, s.tau = ~0ull;
+  __syncthreads();
+  all.each([&](u64 key, uint32_t i, u64 q) {
+    if (!live(key, i, q)) return;
+    const uint32_t slot = atomicAdd(&s.filled, 1u);
+    if (slot < 256) s.keys[slot] = key, s.weights[slot] = kOne + q;
+  });
+  __syncthreads();
+  const uint32_t n = min(s.filled, 256u);
+  if (tid < n) {
+    const u64 key = s.keys[tid];
+    uint32_t number = skipped;
+    u64 sum = skipped_sum;
+    for (uint32_t j = 0; j < n; ++j)
+      if (s.keys[j] > key) ++number, sum += s.weights[j];
+    // not yet reached before this one: the least such key is the one
+    if (rank ? number < rank : (double)sum * kUnit < need) atomicMin(&s.tau, key);
+  }
+  __syncthreads();
+  const u64 tau = s.tau;
+  __syncthreads();
+  return tau;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
+  const enc_sample_args &a = k.a;
+  __shared__ SampleToken list[kList];
+  __shared__ Select pick;
+  __shared__ double sums[kBins], side[kWide / 64], masses[kWide];
+  __shared__ u64 parts[kSampleSegments];
+  __shared__ u64 part, lowest;
+  __shared__ uint32_t chosen;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = blockIdx.x, row = k.row0 + r;
+  SampleRow &w = k.rows[r];
+  const uint32_t state = w.state;
+  const u64 top = w.top;
+  if (state == kSampleEmpty || state == kSampleFirst) {
+    if (tid == 0) {
+      if (a.d_token) a.d_token[row] = state == kSampleEmpty ? -1 : (int32_t)index_of(top);
+      // one token alone: its weight, relative to its bin's lower edge
+      const double t = place_of(logit_of(top), w.r16);
+      w.z = exp((t - w.edge) * 0.0625);
+    }
+    return;
+  }
+  const T *l = static_cast<const T *>(a.d_logits) + (uint64_t)row * a.logits_row;
+  const uint32_t head = head_of(l);
+  const double r16 = w.r16, edge = w.edge;
+  uint32_t cut = w.cut_bin;
+  u64 tau = 0;
+  double z = w.z;
+  if (state != kSampleWhole) {
+    Tokens<T> all;
+    all.list = list;
+    all.n = state == kSampleListed ? w.n : 0;
+    all.row = state == kSampleListed ? nullptr : l;
+    all.vocab = a.vocab;
+    all.r16 = r16;
+    all.edge = edge;
+    for (uint32_t i = tid; i < all.n; i += kWide) list[i] = k.list[(uint64_t)r * kList + i];
+    if (tid < kBins) sums[tid] = k.sums[(uint64_t)r * kBins + tid];
+    for (uint32_t s = tid; s < k.segments; s += kWide) parts[s] = 0;
+    __syncthreads();
+    const uint32_t bk = w.bk, lo = w.lo, bm = w.bm, kb = w.kb;
+    // weights of a bin's tokens down to a key, in units of 2^-32 of its lower edge
+    const auto sum_of = [&](uint32_t bin, u64 from, bool by_segment) {
+      __syncthreads();
+      if (tid == 0) part = 0;
+      __syncthreads();
+      u64 mine = 0;
+      all.each([&](u64 key, uint32_t i, u64 q) {
+        if (i != bin || key < from) return;
+        mine += kOne + q;
+        if (by_segment) atomicAdd(&parts[(index_of(key) + head) / k.segment], kOne + q);
+      });
+      if (mine) atomicAdd(&part, mine);
+      __syncthreads();
+      return part;
+    };
+    const auto upto = [&](uint32_t bin) { return bin ? sums[bin - 1] : 0.0; };
+    const auto unit_of = [&](uint32_t bin) { return exp((double)bin * -0.0625); };
+    cut = kb;
+    double kept = sums[kb];
+    if (bk != kNoBin) {
+      tau = select(all, bk, w.rank, 0.0, pick);
+      kept = upto(bk) + (double)sum_of(bk, tau, false) * kUnit * unit_of(bk);
+    }
+    if (lo != kNoBin) {
+      const double goal = w.top_p * kept;
+      uint32_t b = lo;
+      while (b < w.hi && sums[b] < goal) ++b;
+      // (never less than the first token, whatever the rounding)
+      const u64 at = select(all, b, 0, fmax((goal - upto(b)) / unit_of(b), 1e-300), pick);
+      if (b < cut || at > tau) tau = at;
+      cut = b;
+    }
+    if (bm != kNoBin && bm <= cut) {
+      if (tid == 0) lowest = ~0ull;   // nothing of the bin, if none is great enough
+      __syncthreads();
+      const double t_min = w.t_min;
+      all.each([&](u64 key, uint32_t i, u64) {
+        if (i == bm && place_of(logit_of(key), r16) >= t_min) atomicMin(&lowest, key);
+      });
+      __syncthreads();
+      if (bm < cut || lowest > tau) tau = lowest;
+      cut = bm;
+    }
+    // (tau 0: a whole bin, which only a filter that ends with it leaves)
+    z = tau ? upto(cut) + (double)sum_of(cut, tau, true) * kUnit * unit_of(cut) : sums[cut];
+    if (tid == 0) {
+      w.cut_bin = cut;
+      w.tau = tau;
+      w.z = z;
+    }
+  }
+  if (!a.d_token) return;
+
+  // the segments' kept weights: bins above the cut, and of its bin what is above tau
+  double mine = 0.0;
+  for (uint32_t s = wave; s < k.segments; s += kWide / 64) {
+    const SampleSegment &seg = k.segs[(uint64_t)r * k.segments + s];
+    const double by = edge - seg.edge;
+    double m = 0.0;
+    if (seg.bins && by < (double)kBins) {
+      const uint32_t d = (uint32_t)by;
+      for (uint32_t i = lane; i < seg.bins; i += 64) {
+        const uint32_t b = d + i;
+        if (b > cut || (b == cut && tau)) continue;
+        const u64 v = k.bins[((uint64_t)r * k.segments + s) * kBins + i];
+        m += ((double)(v >> 49) + (double)(v & kSumMask) * kUnit) * exp((double)b * -0.0625);
+      }
+    }
+    for (uint32_t o = 32; o; o >>= 1) m += __shfl_xor(m, o);
+    if (tau) m += (double)parts[s] * kUnit * exp((double)cut * -0.0625);
+    if (lane == 0) masses[s] = m;
+  }
+  __syncthreads();
+  mine = tid < k.segments ? masses[tid] : 0.0;
+  const double incl = group_scan(mine, side);
+  __syncthreads();
+  if (tid == kWide - 1) side[0] = incl;
+  if (tid == 0) chosen = 0;
+  __syncthreads();
+  const float u = a.d_u[row];
+  const double goal = (u > 0.f ? u < 1.f ? (double)u : 1.0 : 0.0) * side[0];
+  // the first segment whose sum passes it; the last with anything if none does
+  const uint32_t key = incl > goal && mine > 0.0 ? 0x80000000u | (kWide - 1 - tid) : mine > 0.0 ? tid + 1 : 0u;
+  atomicMax(&chosen, key);
+  __syncthreads();
+  const uint32_t seg = chosen & 0x80000000u ? kWide - 1 - (chosen & 0x7FFFFFFFu) : chosen - 1;
+  if (tid == seg) side[1] = incl - mine;
+  __syncthreads();
+  const double before = side[1];
+  // its tokens again, in their order
+  const uint32_t each = k.segment / kWide, first = seg * k.segment + tid * each;
+  double own = 0.0;
+  uint32_t last = 0;   // 1 + the last kept one
+  const auto weight = [&](uint32_t v) {
+    if (v < head || v >= head + a.vocab) return 0.0;
+    const float x = value_at(l, v - head);
+    const double t = place_of(x, r16), below = edge - floor(t);
+    if (!counts(x) || !(below <= (double)cut)) return 0.0;
+    if (tau && (uint32_t)below == cut && key_of(x, v - head) < tau) return 0.0;
+    return (double)(kOne + excess_of(t - floor(t))) * kUnit * exp(below * -0.0625);   // as the bins hold it
+  };
+  for (uint32_t j = 0; j < each; ++j) {
+    const double m = weight(first + j);
+    own += m;
+    if (m > 0.0) last = first + j + 1;
+  }
+  const double run = group_scan(own, side);
+  __syncthreads();
+  if (tid == 0) chosen = 0;
+  __syncthreads();
+  // the first to pass the goal; the last kept one if rounding lets none
+  uint32_t mark = last;
+  if (own > 0.0 && before + run > goal) {
+    double sum = before + run - own;
+    for (uint32_t j = 0; j < each; ++j) {
+      const double m = weight(first + j);
+      sum += m;
+      if (m > 0.0 && (sum > goal || first + j + 1 == last)) {
+        mark = 0x80000000u | (0x7FFFFFFFu - (first + j));
+        break;
+      }
+    }
+  }
+  atomicMax(&chosen, mark);
+  __syncthreads();
+  if (tid == 0) {
+    const uint32_t v = chosen & 0x80000000u ? 0x7FFFFFFFu - (chosen & 0x7FFFFFFFu) : chosen - 1;
+    a.d_token[row] = (int32_t)(v - head);
+  }
+}
+
+// ---- the kept tokens' probabilities
+template <typename T, typename O, uint32_t NT, uint32_t NV>
+__global__ __launch_bounds__(NT) void k_probs(SampleKernelArgs k) {
+  constexpr uint32_t E = kPiece<T>, S = NT * NV * E;
+  const enc_sample_args &a = k.a;
+  const uint32_t tid = threadIdx.x, r = blockIdx.x / k.segments, seg = blockIdx.x - r * k.segments;
+  const SampleRow &w = k.rows[r];
+  const T *l = static_cast<const T *>(a.d_logits) + (uint64_t)(k.row0 + r) * a.logits_row;
+  O *out = static_cast<O *>(a.d_probs) + (uint64_t)(k.row0 + r) * a.probs_row;
+  const uint32_t head = head_of(l), cut = w.cut_bin;
+  const u64 tau = w.tau;
+  const bool empty = w.state == kSampleEmpty;
+  const double r16 = w.r16, edge = w.edge, inv = empty ? 0.0 : 1.0 / w.z;
+#pragma unroll
+  for (uint32_t j = 0; j < NV; ++j) {
+    const uint32_t at = seg * S + (j * NT + tid) * E;
+    if (at >= head + a.vocab) break;
+    float x[E], p[E];
+    values_of<T>(load_piece(l, head, a.vocab, at), x);
+#pragma unroll
+    for (uint32_t e = 0; e < E; ++e) {
+      const double t = place_of(x[e], r16), below = edge - floor(t);
+      bool kept = !empty && counts(x[e]) && below <= (double)cut;
+      if (kept && tau && (uint32_t)below == cut) kept = key_of(x[e], at + e - head) >= tau;
+      p[e] = kept ? (float)(exp((t - edge) * 0.0625) * inv) : 0.f;
+    }
+#pragma unroll
+    for (uint32_t e = 0; e < E; ++e)
+      if (at + e >= head && at + e < head + a.vocab) out[at + e - head] = (O)p[e];
+  }
+}
+
+template <typename T, typename O>
+void launch_probs(const SampleKernelArgs &k, uint32_t rows, hipStream_t s) {
+  constexpr uint32_t E = kPiece<T>;
+  const dim3 grid(rows * k.segments);
+  if (k.segment == 4096)
+    hipLaunchKernelGGL((k_probs<T, O, 256, 16 / E>), grid, dim3(256), 0, s, k);
+  else
+    hipLaunchKernelGGL((k_probs<T, O, 512, 32 / E>), grid, dim3(512), 0, s, k);
+}
+
+template <typename T>
+void launch_rows(const SampleKernelArgs &k, uint32_t rows, hipStream_t s) {
+  constexpr uint32_t E = kPiece<T>;
+  const dim3 grid(rows * k.segments);
+  const bool cuts = k.a.d_top_k || k.a.d_top_p || k.a.d_min_p;
+  if (k.segment == 4096)
+    hipLaunchKernelGGL((k_scan<T, 256, 16 / E>), grid, dim3(256), 0, s, k);
+  else
+    hipLaunchKernelGGL((k_scan<T, 512, 32 / E>), grid, dim3(512), 0, s, k);
+  hipLaunchKernelGGL(k_plan, dim3(rows), dim3(kWide), 0, s, k);
+  if (cuts) {
+    if (k.segment == 4096)
+      hipLaunchKernelGGL((k_collect<T, 256, 16 / E>), grid, dim3(256), 0, s, k);
+    else
+      hipLaunchKernelGGL((k_collect<T, 512, 32 / E>), grid, dim3(512), 0, s, k);
+  }
+  hipLaunchKernelGGL((k_resolve<T>), dim3(rows), dim3(kWide), 0, s, k);
+  if (k.a.d_probs) {
+    if (k.a.probs_dtype == 1)
+      launch_probs<T, __bf16>(k, rows, s);
+    else if (k.a.probs_dtype == 2)
+      launch_probs<T, _Float16>(k, rows, s);
+    else
+      launch_probs<T, float>(k, rows, s);
+  }
+}
+
+}  // namespace
+
+// Segments of 16384 values where that leaves every compute unit one, of 4096
+// below, where a row's latency counts. Rows go 1024 at a time through the
+// workspace.
+SamplePlan plan_sample(uint32_t rows, uint32_t vocab) {
+  SamplePlan p;
+  p.rows = std::min(rows, 1024u);
+  const uint64_t large = (vocab + 7ull + 16383) / 16384;
+  p.segment = p.rows * large >= 256 || (vocab + 7ull + 4095) / 4096 > kSampleSegments ? 16384 : 4096;
+  p.segments = (uint32_t)((vocab + 7ull + p.segment - 1) / p.segment);
+  const uint64_t n = (uint64_t)p.rows * p.segments;
+  p.bins = align_up(8ull * kSampleBins * n, 256);
+  p.segs = align_up(sizeof(SampleSegment) * n, 256);
+  p.sums = align_up(8ull * kSampleBins * p.rows, 256);
+  p.row_bytes = align_up(sizeof(SampleRow) * p.rows, 256);
+  p.list = align_up(sizeof(SampleToken) * (uint64_t)kSampleList * p.rows, 256);
+  return p;
+}
+
+hipError_t launch_sample(SampleKernelArgs k, const SamplePlan &p, hipStream_t s) {
+  for (uint64_t row0 = 0; row0 < k.a.rows; row0 += p.rows) {
+    k.row0 = (uint32_t)row0;
+    const uint32_t rows = std::min(p.rows, k.a.rows - k.row0);
+    switch (k.a.dtype) {
+      case 1: launch_rows<__bf16>(k, rows, s); break;
+      case 2: launch_rows<_Float16>(k, rows, s); break;
+      default: launch_rows<float>(k, rows, s); break;
+    }
+  }
+  return hipGetLastError();
+}
+
+}  // namespace enc

@@ -260,6 +260,50 @@ enc_status enc_verify_tree(const enc_verify_args *a, void *d_ws, uint64_t ws_byt
   return after_launch(launch_verify_tree(k, (hipStream_t)stream), (hipStream_t)stream, "enc_verify_tree");
 }
 
+uint64_t enc_sample_workspace_bytes(uint32_t rows, uint32_t vocab) {
+  set_error(ENC_OK, "%s", "");
+  if (!rows || rows > (1u << 20) || !vocab || vocab > (1u << 22)) return 0;
+  const SamplePlan p = plan_sample(rows, vocab);
+  return p.bins + p.segs + p.sums + p.row_bytes + p.list;
+}
+
+enc_status enc_sample(const enc_sample_args *a, void *d_ws, uint64_t ws_bytes, void *stream) {
+  set_error(ENC_OK, "%s", "");
+  if (!a) return invalid("args is NULL");
+  if (a->reserved != 0) return invalid("reserved is not 0");
+  if (a->dtype - 1u > 2u || (a->d_probs && a->probs_dtype - 1u > 2u)) return unsupported("unknown dtype");
+  if (!a->vocab) return invalid("vocab is 0");
+  if (a->vocab > (1u << 22) || a->rows > (1u << 20)) return unsupported("vocab above 2^22 or rows above 2^20");
+  if (a->rows == 0) return ENC_OK;
+  if (!a->d_logits || (!a->d_token && !a->d_probs)) return invalid("logits is NULL, or no output is asked for");
+  if (a->d_token && !a->d_u) return invalid("a token needs u");
+  if (!a->rows_per_setting) return invalid("rows_per_setting is 0");
+  if (!aligned(a->d_logits, value_bytes(a->dtype)) || (a->d_probs && !aligned(a->d_probs, value_bytes(a->probs_dtype))) ||
+      !aligned(a->d_u, 4) || !aligned(a->d_temperature, 4) || !aligned(a->d_top_p, 4) || !aligned(a->d_min_p, 4) ||
+      !aligned(a->d_top_k, 4) || !aligned(a->d_token, 4))
+    return invalid("a misaligned array");
+  if (a->logits_row >> 40 || a->probs_row >> 40) return unsupported("a stride of 2^40 or more");
+  if (a->d_probs && a->rows > 1 && a->probs_row < a->vocab) return invalid("rows of probs overlap");
+  const SamplePlan p = plan_sample(a->rows, a->vocab);
+  const uint64_t need = p.bins + p.segs + p.sums + p.row_bytes + p.list;
+  if (!d_ws || !aligned(d_ws, 16)) return invalid("workspace is NULL or not 16-byte aligned");
+  if (ws_bytes < need)
+    return set_error(ENC_ERR_CAPACITY, "workspace of %llu bytes, %llu needed", (unsigned long long)ws_bytes,
+                     (unsigned long long)need);
+  SampleKernelArgs k;
+  k.a = *a;
+  k.row0 = 0;
+  k.segment = p.segment;
+  k.segments = p.segments;
+  uint8_t *ws = static_cast<uint8_t *>(d_ws);
+  k.bins = reinterpret_cast<unsigned long long *>(ws);
+  k.segs = reinterpret_cast<SampleSegment *>(ws += p.bins);
+  k.sums = reinterpret_cast<double *>(ws += p.segs);
+  k.rows = reinterpret_cast<SampleRow *>(ws += p.sums);
+  k.list = reinterpret_cast<SampleToken *>(ws += p.row_bytes);
+  return after_launch(launch_sample(k, p, (hipStream_t)stream), (hipStream_t)stream, "enc_sample");
+}
+
 uint64_t enc_cache_workspace_bytes(const enc_cache *c, uint32_t batch, uint32_t nodes) {
   set_error(ENC_OK, "%s", "");
   if (check_cache(c) != ENC_OK || !batch || batch > (1u << 20) || !nodes || nodes > ENC_TREE_MAX_NODES) return 0;

@@ -1,5 +1,5 @@
 // step_common.h -- definitions shared by the kernels of one decoding step
-// (qk_rope, block_norm, tree_attention, verify_tree, cache_pages) and their host side.
+// (qk_rope, block_norm, tree_attention, sample, verify_tree, cache_pages) and their host side.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -107,6 +107,45 @@ struct VerifyPlan {
 };
 VerifyPlan plan_verify_tree(uint32_t batch, uint32_t vocab);
 hipError_t launch_verify_tree(const VerifyKernelArgs &k, hipStream_t s);
+
+// What the passes over a row of logits hand on (see sample.hip).
+constexpr uint32_t kSampleBins = 768, kSampleList = 4096, kSampleSegments = 1024;
+enum : uint32_t { kSampleEmpty, kSampleFirst, kSampleWhole, kSampleListed, kSampleRead };
+struct SampleSegment {
+  unsigned long long top;    // greatest key, 0: none
+  double edge;               // its bin's place
+  uint32_t bins;             // written bins, from there down
+  uint32_t n, first;         // tokens gathered from it, and their place in the list
+  uint32_t reserved;
+};
+struct SampleRow {
+  double edge, r16;          // place of the first bin; 16 / temperature
+  double t_min, top_p, z;    // min-p's least place; kept weights' sum
+  unsigned long long top, tau;  // greatest key; the least that is kept of the cut's bin (0: all)
+  uint32_t state;            // kSample...
+  uint32_t bk, lo, hi, bm;   // bins in which top-k, top-p (from, to) and min-p cut, or ~0
+  uint32_t kb, rank;         // last bin that top-k reaches, and how many tokens of it
+  uint32_t cut_bin, n;       // the cut's bin; tokens to gather
+};
+struct SampleToken {
+  unsigned long long key, at;   // at: bin in the upper 24 bits, weight less 1 in units of 2^-32
+};
+struct SampleKernelArgs {
+  enc_sample_args a;
+  uint32_t row0, segment, segments;
+  unsigned long long *bins;  // [rows, segments, kSampleBins] count in the upper 15 bits, sum below
+  SampleSegment *segs;       // [rows, segments]
+  double *sums;              // [rows, kSampleBins] cumulative weights
+  SampleRow *rows;           // [rows]
+  SampleToken *list;         // [rows, kSampleList]
+};
+struct SamplePlan {
+  uint32_t rows;             // at a time
+  uint32_t segment, segments;
+  uint64_t bins, segs, sums, row_bytes, list;   // bytes of the workspace's parts
+};
+SamplePlan plan_sample(uint32_t rows, uint32_t vocab);
+hipError_t launch_sample(SampleKernelArgs k, const SamplePlan &p, hipStream_t s);
 
 struct CommitArgs {
   enc_cache c;

@@ -110,6 +110,13 @@ class EncVerifyArgs(ctypes.Structure):
         + [(n, ctypes.c_uint32) for n in ("batch", "nodes", "vocab", "dtype")])
 
 
+class EncSampleArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in (
+        "d_logits", "d_u", "d_temperature", "d_top_p", "d_min_p", "d_top_k", "d_token", "d_probs")]
+        + [(n, ctypes.c_uint64) for n in ("logits_row", "probs_row")]
+        + [(n, ctypes.c_uint32) for n in ("rows", "vocab", "rows_per_setting", "dtype", "probs_dtype", "reserved")])
+
+
 class EncCache(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("d_data", "d_table", "d_lens", "d_refs")]
                 + [("plane_stride", ctypes.c_uint64)]
@@ -160,6 +167,8 @@ SIGNATURES = {
     "enc_tree_attention": (_ST, [ctypes.POINTER(EncTreeAttentionArgs), _VP, _U64, _VP]),
     "enc_verify_tree_workspace_bytes": (_U64, [_U32, _U32, _U32]),
     "enc_verify_tree": (_ST, [ctypes.POINTER(EncVerifyArgs), _VP, _U64, _VP]),
+    "enc_sample_workspace_bytes": (_U64, [_U32, _U32]),
+    "enc_sample": (_ST, [ctypes.POINTER(EncSampleArgs), _VP, _U64, _VP]),
     "enc_cache_workspace_bytes": (_U64, [ctypes.POINTER(EncCache), _U32, _U32]),
     "enc_cache_commit": (_ST, [ctypes.POINTER(EncCache), _VP, _U32, _VP, _U64, _U64, _VP, _VP, _U32, _VP,
                                _VP, _U64, _VP]),
@@ -614,6 +623,7 @@ def _load_types():
 _QK_PACK = struct.Struct("=22Q10IfI").pack
 _BLOCK_PACK = struct.Struct("=12Q9I3f").pack
 _ATTN_PACK = struct.Struct("=27Q10IfI").pack
+_SAMPLE_PACK = struct.Struct("=10Q6I").pack
 _VERIFY_PACK = struct.Struct("=13Q4I").pack
 
 
@@ -905,6 +915,60 @@ def enc_verify_tree(parents, tokens, target, draft, u, nodes=None, ws=None, stre
         ts[0], ts[1], ds[0], ds[1], batch, n, vocab, _code(dtype)))
     _check(lib().enc_verify_tree(ctypes.byref(a), *_scratch(ws, device), _handle(stream, device)))
     return path, count, token
+
+
+def enc_sample_workspace_bytes(rows, vocab):
+    return int(lib().enc_sample_workspace_bytes(rows, vocab))
+
+
+def sample_workspace(logits):
+    """A workspace for enc_sample of this shape (no initialisation needed)."""
+    return _empty_u8(max(enc_sample_workspace_bytes(*logits.shape), 16), logits.device)
+
+
+def enc_sample(logits, u=None, temperature=None, top_k=None, top_p=None, min_p=None, return_probs=False,
+               probs_dtype=None, probs=None, ws=None, stream=None):
+    """Filter rows of logits [rows, vocab] (any row stride) and draw a token from
+    each. u: fp32 [rows] random numbers in [0, 1), or None: no token; temperature,
+    top_p, min_p: fp32, top_k: int32, all of one length that divides rows (setting
+    i for rows i * rows / length on), or None. Returns (token int32 [rows] or
+    None, probs [rows, vocab] or None): probs in probs_dtype (float32) with
+    return_probs, or in the tensor `probs`."""
+    device = _device_of(logits)
+    rows, vocab = shape = logits.shape
+    ls = _values(logits, "logits", logits.dtype, shape, device)
+    up = _plain(u, "u", _F32, (rows,), device) if u is not None else 0
+    n = None
+    at = []
+    for name, t, dtype in (("temperature", temperature, _F32), ("top_p", top_p, _F32), ("min_p", min_p, _F32),
+                           ("top_k", top_k, _I32)):
+        if t is None:
+            at.append(0)
+            continue
+        if n is None:
+            n = t.numel()
+        at.append(_plain(t, name, dtype, (n,), device))
+    if n is not None and (rows % n if n else rows):
+        raise ValueError("%d settings for %d rows" % (n, rows))
+
+    def room():
+        return (logits.new_empty(rows, dtype=_I32) if u is not None else None,
+                logits.new_empty(shape, dtype=probs_dtype or _F32) if return_probs and probs is None else probs,
+                sample_workspace(logits) if ws is None else ws)
+
+    if stream is None:
+        token, probs, ws = room()
+    else:
+        with _on(stream):
+            token, probs, ws = room()
+    ps, pp, p_code = 0, 0, 0
+    if probs is not None:
+        ps, pp, p_code = _values(probs, "probs", probs.dtype, shape, device)[0], probs.data_ptr(), _code(probs.dtype)
+    a = EncSampleArgs.from_buffer_copy(_SAMPLE_PACK(
+        logits.data_ptr(), up, *at, token.data_ptr() if token is not None else 0, pp, ls[0], ps, rows, vocab,
+        max(rows // n, 1) if n else 1, _code(logits.dtype), p_code, 0))
+    _check(lib().enc_sample(ctypes.byref(a), *_scratch(ws, device), _handle(stream, device)))
+    return token, probs
 
 
 class Cache:

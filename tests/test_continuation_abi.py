@@ -57,3 +57,44 @@ def test_block_norm_nothing_to_do(L):
     assert L.enc_block_norm(ctypes.byref(norm(tokens=0, d_h=0)), None) == 0
     assert enc.enc_last_error() == ""
     assert L.enc_block_norm(None, None) == -1
+
+
+def test_sample_layout():
+    assert ctypes.sizeof(enc.EncSampleArgs) == 104
+
+
+def sample(**kw):
+    a = enc.EncSampleArgs()
+    for n in ("d_logits", "d_u", "d_temperature", "d_top_p", "d_min_p", "d_top_k", "d_token", "d_probs"):
+        setattr(a, n, P)
+    a.logits_row = a.probs_row = 1000
+    a.rows, a.vocab, a.rows_per_setting, a.dtype, a.probs_dtype = 4, 1000, 1, 3, 1
+    for n, v in kw.items():
+        setattr(a, n, v)
+    return a
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(vocab=0), -1), (dict(vocab=2 ** 22 + 1), -2), (dict(rows=2 ** 20 + 1), -2), (dict(dtype=0), -2), (dict(dtype=4), -2),
+    (dict(probs_dtype=0), -2), (dict(reserved=1), -1), (dict(d_logits=0), -1), (dict(d_token=0, d_probs=0), -1),
+    (dict(d_u=0), -1), (dict(rows_per_setting=0), -1), (dict(d_logits=P + 2), -1), (dict(d_probs=P + 1), -1),
+    (dict(d_u=P + 2), -1), (dict(d_top_k=P + 1), -1), (dict(d_temperature=P + 2), -1), (dict(d_token=P + 2), -1),
+    (dict(logits_row=1 << 40), -2), (dict(probs_row=999), -1),
+])
+def test_sample_refusals(L, kw, status):
+    assert L.enc_sample(ctypes.byref(sample(**kw)), P, 1 << 40, None) == status
+    assert enc.enc_last_error()
+
+
+def test_sample_workspace(L):
+    need = L.enc_sample_workspace_bytes(4, 1000)
+    assert need > 0
+    a = sample()
+    assert L.enc_sample(ctypes.byref(a), P, need - 1, None) == -3
+    assert L.enc_sample(ctypes.byref(a), None, need, None) == -1
+    assert L.enc_sample(ctypes.byref(a), P + 4, need, None) == -1
+    assert L.enc_sample(ctypes.byref(sample(rows=0, d_logits=0)), None, 0, None) == 0
+    assert L.enc_sample(None, None, 0, None) == -1
+    for rows, vocab in ((0, 10), (10, 0), (2 ** 20 + 1, 10), (10, 2 ** 22 + 1)):
+        assert L.enc_sample_workspace_bytes(rows, vocab) == 0
+    assert L.enc_sample_workspace_bytes(2 ** 20, 1000) == L.enc_sample_workspace_bytes(1024, 1000)
