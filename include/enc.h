@@ -521,6 +521,32 @@ uint64_t enc_tree_attention_workspace_bytes(const enc_tree_attention_args *h_arg
 enc_status enc_tree_attention(const enc_tree_attention_args *h_args, void *d_ws, uint64_t ws_bytes,
                               void *stream);
 
+/* Attention of sequences that share their first cached tokens (continuations of
+ * one prompt, questions about one document): enc_tree_attention's results, with
+ * the shared rows of K and V read once for all sequences of a group. Group g is
+ * the batch entries d_starts[g] .. d_starts[g + 1] - 1 and shares d_shared[g]
+ * tokens: the caller says, or enc_cache_shared finds, that these rows are equal
+ * in all of its sequences. They are read where the first of them has them. An
+ * entry of no group, and a group of one, share nothing. Numbers out of range
+ * count as the nearest in it (starts: [0, batch], a start below an earlier one
+ * as that one; d_shared: 0 to the shortest length in the group). Weights are
+ * rounded to the values' type, results once more; softmax sums are fp32. */
+typedef struct enc_prefix_attention_args {
+  enc_tree_attention_args t;       /* as for enc_tree_attention */
+  const int32_t *d_starts;         /* [groups + 1], ascending */
+  const int32_t *d_shared;         /* [groups] */
+  uint32_t groups;                 /* 0: nobody shares anything */
+  uint32_t reserved;               /* 0 */
+} enc_prefix_attention_args;
+
+/* Limits as for enc_tree_attention; groups up to 2^20. The workspace (any
+ * contents) holds the plan of the call, made on the device from lengths and
+ * groups, and the sums of the pieces that rows are cut into, joined in a fixed
+ * order: equal inputs give equal bits. Asynchronous. */
+uint64_t enc_prefix_attention_workspace_bytes(const enc_prefix_attention_args *h_args);
+enc_status enc_prefix_attention(const enc_prefix_attention_args *h_args, void *d_ws, uint64_t ws_bytes,
+                                void *stream);
+
 /* Verification of a tree of drafted tokens against the target's
  * probabilities, from given random numbers. The walk starts at node 0 with
  * r = target[0] and looks at the current node's children in index order:
@@ -644,6 +670,15 @@ enc_status enc_cache_commit(const enc_cache *h_cache, const int32_t *d_seqs, uin
  * or of one sequence with itself, does nothing. Asynchronous. */
 enc_status enc_cache_fork(const enc_cache *h_cache, const int32_t *d_src, const int32_t *d_dst,
                           uint32_t pairs, void *stream);
+
+/* How many leading tokens the sequences of each group hold in the same pages:
+ * group g is d_seqs[d_starts[g]] .. d_seqs[d_starts[g + 1] - 1] (starts as for
+ * enc_prefix_attention), d_shared[g] the tokens of the leading table entries
+ * that are equal in all of them, at most the shortest length; 0 for an empty
+ * group or one with a sequence outside the table. A page that was copied when a
+ * sequence was written behind it is not counted. Asynchronous. */
+enc_status enc_cache_shared(const enc_cache *h_cache, const int32_t *d_seqs, uint32_t batch,
+                            const int32_t *d_starts, uint32_t groups, int32_t *d_shared, void *stream);
 
 /* Cut sequence d_seqs[i] to d_new_lens[i] tokens (no longer than it is; 0
  * frees it) and free the pages past its end that nobody else holds. d_seqs

@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libenc.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["decode.hip", "encode.hip", "encode_onepass.hip", "encode_wide.hip", "gemm.hip", "validate.hip", "probe.hip", "noalloc.hip",
-           "qk_rope.hip", "block_norm.hip", "tree_attention.hip", "sample.hip", "verify_tree.hip", "cache_pages.hip",
+           "qk_rope.hip", "block_norm.hip", "tree_attention.hip", "prefix_attention.hip", "sample.hip", "verify_tree.hip", "cache_pages.hip",
            "enc_api.cpp", "step_api.cpp"]
 ARCH = "gfx950"
 

@@ -50,6 +50,30 @@ enc_status check_attention(const enc_tree_attention_args *a) {
   return ENC_OK;
 }
 
+enc_status check_attention_arrays(const enc_tree_attention_args *a) {
+  if (!std::isfinite(a->scale)) return invalid("scale is not finite");
+  if (!rows_ok(a->d_q, a->dtype, a->q_batch, a->q_node, a->q_head) ||
+      !rows_ok(a->d_out, a->dtype, a->out_batch, a->out_node, a->out_head))
+    return invalid("q or out: NULL, or a base or row that is not 16-byte aligned");
+  if (!rows_ok(a->d_k_new, a->dtype, a->k_new_batch, a->k_new_node, a->k_new_head) ||
+      !rows_ok(a->d_v_new, a->dtype, a->v_new_batch, a->v_new_node, a->v_new_head))
+    return invalid("k_new or v_new: NULL, or a base or row that is not 16-byte aligned");
+  if (!rows_ok(a->d_k_cache, a->dtype, a->cache_page, a->cache_token, a->cache_head) ||
+      !rows_ok(a->d_v_cache, a->dtype, 0, 0))
+    return invalid("cache: NULL, or a base or row that is not 16-byte aligned");
+  if (!a->d_table || !a->d_lens || !aligned(a->d_table, 4) || !aligned(a->d_lens, 4) || !aligned(a->d_seqs, 4) ||
+      !aligned(a->d_nodes, 4) || !aligned(a->d_mask, 8) || !aligned(a->d_lse, 4))
+    return invalid("table or lens NULL, or a misaligned array");
+  if (!a->d_seqs && a->batch > a->max_seqs) return invalid("without seqs, batch must not exceed max_seqs");
+  // row offsets are kept in 16-byte units of 32 bits: each layer's cache below 64 GiB
+  const uint64_t reach = (uint64_t)(a->n_pages - 1) * (a->cache_page / 8) + (uint64_t)(a->page_size - 1) * (a->cache_token / 8);
+  if (a->cache_page >> 35 || a->cache_token >> 35 || reach >> 32) return unsupported("a cache above 64 GiB");
+  if ((a->nodes - 1ull) * (a->k_new_node / 8) >> 31 || (a->nodes - 1ull) * (a->v_new_node / 8) >> 31 ||
+      a->k_new_node >> 35 || a->v_new_node >> 35)
+    return unsupported("k_new or v_new strides above 32 GiB");
+  return ENC_OK;
+}
+
 enc_status check_cache(const enc_cache *c) {
   if (!c) return invalid("cache is NULL");
   if (!c->d_data || !c->d_table || !c->d_lens || !c->d_refs) return invalid("a pointer of the cache is NULL");
@@ -68,6 +92,19 @@ enc_status check_cache(const enc_cache *c) {
   if (used > 0x7FFFFFFFull) return unsupported("n_pages * page_size above 2^31 - 1");
   if (used > (1ull << 40) / c->row_bytes) return unsupported("a plane above 2^40 bytes");
   if (c->n_planes > 1 && c->plane_stride < used * c->row_bytes) return invalid("plane_stride below a plane's bytes");
+  return ENC_OK;
+}
+
+enc_status check_prefix(const enc_prefix_attention_args *a) {
+  if (!a) return invalid("args is NULL");
+  if (a->reserved != 0) return invalid("reserved is not 0");
+  const enc_status st = check_attention(&a->t);
+  if (st != ENC_OK) return st;
+  if (a->groups > (1u << 20)) return unsupported("more than 2^20 groups");
+  if (a->t.batch) {   // a grid holds fewer than 2^32 threads
+    const PrefixAttnPlan p = plan_prefix_attention(a->t, a->groups);
+    if ((uint64_t)p.items * a->t.kv_heads >= (1u << 24)) return unsupported("more than 2^24 pieces");
+  }
   return ENC_OK;
 }
 
@@ -175,26 +212,8 @@ enc_status enc_tree_attention(const enc_tree_attention_args *a, void *d_ws, uint
   const enc_status st = check_attention(a);
   if (st != ENC_OK) return st;
   if (a->batch == 0) return ENC_OK;
-  if (!std::isfinite(a->scale)) return invalid("scale is not finite");
-  if (!rows_ok(a->d_q, a->dtype, a->q_batch, a->q_node, a->q_head) ||
-      !rows_ok(a->d_out, a->dtype, a->out_batch, a->out_node, a->out_head))
-    return invalid("q or out: NULL, or a base or row that is not 16-byte aligned");
-  if (!rows_ok(a->d_k_new, a->dtype, a->k_new_batch, a->k_new_node, a->k_new_head) ||
-      !rows_ok(a->d_v_new, a->dtype, a->v_new_batch, a->v_new_node, a->v_new_head))
-    return invalid("k_new or v_new: NULL, or a base or row that is not 16-byte aligned");
-  if (!rows_ok(a->d_k_cache, a->dtype, a->cache_page, a->cache_token, a->cache_head) ||
-      !rows_ok(a->d_v_cache, a->dtype, 0, 0))
-    return invalid("cache: NULL, or a base or row that is not 16-byte aligned");
-  if (!a->d_table || !a->d_lens || !aligned(a->d_table, 4) || !aligned(a->d_lens, 4) || !aligned(a->d_seqs, 4) ||
-      !aligned(a->d_nodes, 4) || !aligned(a->d_mask, 8) || !aligned(a->d_lse, 4))
-    return invalid("table or lens NULL, or a misaligned array");
-  if (!a->d_seqs && a->batch > a->max_seqs) return invalid("without seqs, batch must not exceed max_seqs");
-  // row offsets are kept in 16-byte units of 32 bits: each layer's cache below 64 GiB
-  const uint64_t reach = (uint64_t)(a->n_pages - 1) * (a->cache_page / 8) + (uint64_t)(a->page_size - 1) * (a->cache_token / 8);
-  if (a->cache_page >> 35 || a->cache_token >> 35 || reach >> 32) return unsupported("a cache above 64 GiB");
-  if ((a->nodes - 1ull) * (a->k_new_node / 8) >> 31 || (a->nodes - 1ull) * (a->v_new_node / 8) >> 31 ||
-      a->k_new_node >> 35 || a->v_new_node >> 35)
-    return unsupported("k_new or v_new strides above 32 GiB");
+  const enc_status ar = check_attention_arrays(a);
+  if (ar != ENC_OK) return ar;
   const TreeAttnPlan p = plan_tree_attention(*a);
   const uint64_t need = p.part_bytes + p.ml_bytes + p.share_bytes;
   if (need) {
@@ -217,6 +236,56 @@ enc_status enc_tree_attention(const enc_tree_attention_args *a, void *d_ws, uint
   k.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(d_ws) + p.part_bytes);
   k.shares = need ? reinterpret_cast<uint2 *>(static_cast<uint8_t *>(d_ws) + p.part_bytes + p.ml_bytes) : nullptr;
   return after_launch(launch_tree_attention(k, p, (hipStream_t)stream), (hipStream_t)stream, "enc_tree_attention");
+}
+
+uint64_t enc_prefix_attention_workspace_bytes(const enc_prefix_attention_args *a) {
+  set_error(ENC_OK, "%s", "");
+  if (check_prefix(a) != ENC_OK || a->t.batch == 0) return 0;
+  return plan_prefix_attention(a->t, a->groups).total();
+}
+
+enc_status enc_prefix_attention(const enc_prefix_attention_args *a, void *d_ws, uint64_t ws_bytes, void *stream) {
+  set_error(ENC_OK, "%s", "");
+  enc_status st = check_prefix(a);
+  if (st != ENC_OK) return st;
+  const enc_tree_attention_args &t = a->t;
+  if (t.batch == 0) return ENC_OK;
+  if ((st = check_attention_arrays(&t)) != ENC_OK) return st;
+  if (a->groups && (!a->d_starts || !a->d_shared || !aligned(a->d_starts, 4) || !aligned(a->d_shared, 4)))
+    return invalid("starts or shared NULL or misaligned");
+  const PrefixAttnPlan p = plan_prefix_attention(t, a->groups);
+  if (!d_ws || !aligned(d_ws, 16)) return invalid("workspace is NULL or not 16-byte aligned");
+  if (ws_bytes < p.total())
+    return set_error(ENC_ERR_CAPACITY, "workspace of %llu bytes, %llu needed", (unsigned long long)ws_bytes,
+                     (unsigned long long)p.total());
+  PrefixAttnArgs k;
+  k.a = t;
+  k.starts = a->d_starts;
+  k.shared = a->d_shared;
+  k.page = FastDiv::of(t.page_size);
+  k.group = FastDiv::of(t.q_heads / t.kv_heads);
+  k.nodes = FastDiv::of(t.nodes);
+  k.groups = a->groups;
+  k.tile = p.tile;
+  k.own_tile = p.own_tile;
+  k.own_tiles = p.own_tiles;
+  k.slots = p.slots;
+  k.least = p.least;
+  k.weight = p.weight;
+  k.mask_words = (t.nodes + 63) / 64 * 2;
+  k.own_rows = (uint64_t)p.most_shared * t.kv_heads * p.tile;
+  uint8_t *ws = static_cast<uint8_t *>(d_ws);
+  k.part = reinterpret_cast<float *>(ws);
+  k.part_ml = reinterpret_cast<float *>(ws += p.part_bytes);
+  k.items = reinterpret_cast<PrefixItem *>(ws += p.ml_bytes);
+  k.first = reinterpret_cast<uint32_t *>(ws += p.item_bytes);
+  k.group_of = reinterpret_cast<uint32_t *>(ws += p.batch_bytes);
+  k.own_parts = reinterpret_cast<uint2 *>(ws += p.batch_bytes);
+  k.ends = reinterpret_cast<uint32_t *>(ws += 2 * p.batch_bytes);
+  k.common = reinterpret_cast<uint32_t *>(ws += p.group_bytes);
+  k.group_parts = reinterpret_cast<uint2 *>(ws += p.group_bytes);
+  k.counts = reinterpret_cast<uint32_t *>(ws += 2 * p.group_bytes);
+  return after_launch(launch_prefix_attention(k, p, (hipStream_t)stream), (hipStream_t)stream, "enc_prefix_attention");
 }
 
 uint64_t enc_verify_tree_workspace_bytes(uint32_t batch, uint32_t nodes, uint32_t vocab) {
@@ -358,6 +427,19 @@ enc_status enc_cache_fork(const enc_cache *c, const int32_t *d_src, const int32_
   if (!d_src || !d_dst || !aligned(d_src, 4) || !aligned(d_dst, 4)) return invalid("src or dst NULL or misaligned");
   return after_launch(launch_cache_fork(*c, d_src, d_dst, pairs, (hipStream_t)stream), (hipStream_t)stream,
                       "enc_cache_fork");
+}
+
+enc_status enc_cache_shared(const enc_cache *c, const int32_t *d_seqs, uint32_t batch, const int32_t *d_starts,
+                            uint32_t groups, int32_t *d_shared, void *stream) {
+  set_error(ENC_OK, "%s", "");
+  const enc_status st = check_cache(c);
+  if (st != ENC_OK) return st;
+  if (!groups) return ENC_OK;
+  if (groups > (1u << 20) || batch > 0x7FFFFFFFu) return unsupported("more than 2^20 groups, or batch above 2^31 - 1");
+  if ((batch && !d_seqs) || !d_starts || !d_shared || !aligned(d_seqs, 4) || !aligned(d_starts, 4) || !aligned(d_shared, 4))
+    return invalid("seqs, starts or shared NULL or misaligned");
+  return after_launch(launch_cache_shared(*c, d_seqs, batch, d_starts, groups, d_shared, (hipStream_t)stream),
+                      (hipStream_t)stream, "enc_cache_shared");
 }
 
 enc_status enc_cache_truncate(const enc_cache *c, const int32_t *d_seqs, const int32_t *d_new_lens, uint32_t count,

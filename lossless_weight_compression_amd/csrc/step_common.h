@@ -1,5 +1,6 @@
 // step_common.h -- definitions shared by the kernels of one decoding step
-// (qk_rope, block_norm, tree_attention, sample, verify_tree, cache_pages) and their host side.
+// (qk_rope, block_norm, tree_attention, prefix_attention,
+// sample, verify_tree, cache_pages) and their host side.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -107,6 +108,40 @@ struct VerifyPlan {
 };
 VerifyPlan plan_verify_tree(uint32_t batch, uint32_t vocab);
 hipError_t launch_verify_tree(const VerifyKernelArgs &k, hipStream_t s);
+
+// A piece's work: a tile of query rows over a range of keys.
+struct PrefixItem {
+  uint32_t b, row0, rows;    // first batch entry, first row of its rows, and how many
+  uint32_t first, ctx, tree; // first cached token, how many, and nodes behind them
+  uint32_t lo, hi;           // strips of 32 keys
+};
+struct PrefixAttnArgs {
+  enc_tree_attention_args a;
+  const int32_t *starts, *shared;
+  FastDiv page, group, nodes;   // page_size; q_heads / kv_heads; nodes
+  uint32_t groups;
+  uint32_t tile, own_tile, own_tiles;   // rows of a tile; tiles of a sequence's rows
+  uint32_t slots, least, weight;        // pieces aimed at; strips in the smallest; work of a shared strip
+  uint32_t mask_words;
+  float unit, slack;         // powers of two to a unit of a maximum; how far a strip may exceed it
+  uint64_t own_rows;         // of the pieces of own tokens, the first
+  float *part, *part_ml;     // [pieces, kv_heads, tile, head_dim], [.., 2] sums; maxima and weights' sums
+  PrefixItem *items;
+  uint32_t *first, *group_of;   // [batch] tokens shared; group, or ~0
+  uint2 *own_parts;          // [batch] first piece and how many
+  uint32_t *ends, *common;   // [groups + 1] batch entries; [groups] tokens shared
+  uint2 *group_parts;        // [groups] first piece and how many
+  uint32_t *counts;          // pieces of shared tokens; of all
+};
+struct PrefixAttnPlan {
+  uint32_t tile, own_tile, own_tiles, slots, least, weight, most_shared, most_own, items;
+  uint64_t part_bytes, ml_bytes, item_bytes, batch_bytes, group_bytes;
+  uint64_t total() const { return part_bytes + ml_bytes + item_bytes + 4 * batch_bytes + 4 * group_bytes + 256; }
+};
+PrefixAttnPlan plan_prefix_attention(const enc_tree_attention_args &a, uint32_t groups);
+hipError_t launch_prefix_attention(PrefixAttnArgs k, const PrefixAttnPlan &p, hipStream_t s);
+hipError_t launch_cache_shared(const enc_cache &c, const int32_t *seqs, uint32_t batch, const int32_t *starts,
+                               uint32_t groups, int32_t *shared, hipStream_t s);
 
 // What the passes over a row of logits hand on (see sample.hip).
 constexpr uint32_t kSampleBins = 768, kSampleList = 4096, kSampleSegments = 1024;

@@ -103,6 +103,11 @@ class EncTreeAttentionArgs(ctypes.Structure):
         + [("scale", ctypes.c_float), ("reserved", ctypes.c_uint32)])
 
 
+class EncPrefixAttentionArgs(ctypes.Structure):
+    _fields_ = [("t", EncTreeAttentionArgs), ("d_starts", ctypes.c_void_p), ("d_shared", ctypes.c_void_p),
+                ("groups", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
 class EncVerifyArgs(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in (
         "d_parents", "d_tokens", "d_target", "d_draft", "d_u", "d_nodes", "d_path", "d_count", "d_token")]
@@ -165,6 +170,8 @@ SIGNATURES = {
     "enc_block_norm": (_ST, [ctypes.POINTER(EncBlockNormArgs), _VP]),
     "enc_tree_attention_workspace_bytes": (_U64, [ctypes.POINTER(EncTreeAttentionArgs)]),
     "enc_tree_attention": (_ST, [ctypes.POINTER(EncTreeAttentionArgs), _VP, _U64, _VP]),
+    "enc_prefix_attention_workspace_bytes": (_U64, [ctypes.POINTER(EncPrefixAttentionArgs)]),
+    "enc_prefix_attention": (_ST, [ctypes.POINTER(EncPrefixAttentionArgs), _VP, _U64, _VP]),
     "enc_verify_tree_workspace_bytes": (_U64, [_U32, _U32, _U32]),
     "enc_verify_tree": (_ST, [ctypes.POINTER(EncVerifyArgs), _VP, _U64, _VP]),
     "enc_sample_workspace_bytes": (_U64, [_U32, _U32]),
@@ -173,6 +180,7 @@ SIGNATURES = {
     "enc_cache_commit": (_ST, [ctypes.POINTER(EncCache), _VP, _U32, _VP, _U64, _U64, _VP, _VP, _U32, _VP,
                                _VP, _U64, _VP]),
     "enc_cache_fork": (_ST, [ctypes.POINTER(EncCache), _VP, _VP, _U32, _VP]),
+    "enc_cache_shared": (_ST, [ctypes.POINTER(EncCache), _VP, _U32, _VP, _U32, _VP, _VP]),
     "enc_cache_truncate": (_ST, [ctypes.POINTER(EncCache), _VP, _VP, _U32, _VP]),
     "enc_status_string": (ctypes.c_char_p, [_ST]),
     "enc_last_error": (ctypes.c_char_p, []),
@@ -624,6 +632,7 @@ _QK_PACK = struct.Struct("=22Q10IfI").pack
 _BLOCK_PACK = struct.Struct("=12Q9I3f").pack
 _ATTN_PACK = struct.Struct("=27Q10IfI").pack
 _SAMPLE_PACK = struct.Struct("=10Q6I").pack
+_PREFIX_PACK = struct.Struct("=27Q10IfI2Q2I").pack
 _VERIFY_PACK = struct.Struct("=13Q4I").pack
 
 
@@ -871,6 +880,70 @@ def enc_tree_attention(q, k_new, v_new, k_cache, v_cache, table, lens, mask=None
     return out, lse
 
 
+def enc_prefix_attention_workspace_bytes(q, k_new, table, k_cache, starts):
+    batch, nodes, q_heads, dim = q.shape
+    a = EncPrefixAttentionArgs.from_buffer_copy(_PREFIX_PACK(
+        *[0] * 27, batch, nodes, q_heads, k_new.shape[2], dim, _code(q.dtype), k_cache.shape[0], k_cache.shape[1],
+        table.shape[1], table.shape[0], 0.0, 0, 0, 0, starts.numel() - 1, 0))
+    return int(lib().enc_prefix_attention_workspace_bytes(ctypes.byref(a)))
+
+
+def prefix_attention_workspace(q, k_new, table, k_cache, starts):
+    """A workspace for enc_prefix_attention of these shapes (no initialisation needed)."""
+    return _empty_u8(enc_prefix_attention_workspace_bytes(q, k_new, table, k_cache, starts), q.device)
+
+
+def enc_prefix_attention(q, k_new, v_new, k_cache, v_cache, table, lens, starts, shared, mask=None, seqs=None,
+                         nodes=None, scale=None, return_lse=False, out=None, ws=None, stream=None):
+    """enc_tree_attention of a batch in which group g, entries starts[g] to
+    starts[g + 1] - 1, shares its first shared[g] cached tokens: their rows are
+    read once for the group. starts: int32 [groups + 1] ascending; shared: int32
+    [groups] (enc_cache_shared finds it). The other arguments, and what is
+    returned, are enc_tree_attention's."""
+    device = _device_of(q)
+    dtype = q.dtype
+    batch, n, q_heads, dim = shape = q.shape
+    pages, page, kv_heads = k_cache.shape[:3]
+    new_shape = (batch, n, kv_heads, dim)
+    qs = _values(q, "q", dtype, shape, device)
+    ks = _values(k_new, "k_new", dtype, new_shape, device)
+    vs = _values(v_new, "v_new", dtype, new_shape, device)
+    cs = _values(k_cache, "k_cache", dtype, (pages, page, kv_heads, dim), device)
+    if _values(v_cache, "v_cache", dtype, k_cache.shape, device) != cs:
+        raise ValueError("k_cache and v_cache must have the same strides")
+    tp = _plain(table, "table", _I32, None, device)
+    max_seqs, max_pages = table.shape
+    lp = _plain(lens, "lens", _I32, (max_seqs,), device)
+    mp = _plain(mask, "mask", _I64, (batch, n, (n + 63) // 64), device) if mask is not None else 0
+    sp = _plain(seqs, "seqs", _I32, (batch,), device) if seqs is not None else 0
+    np_ = _plain(nodes, "nodes", _I32, (batch,), device) if nodes is not None else 0
+    groups = starts.numel() - 1
+    if groups < 0:
+        raise ValueError("starts holds one number more than there are groups")
+    stp = _plain(starts, "starts", _I32, (groups + 1,), device)
+    shp = _plain(shared, "shared", _I32, (groups,), device)
+
+    def room():
+        return (q.new_empty(shape) if out is None else out,
+                q.new_empty((batch, n, q_heads), dtype=_F32) if return_lse else None,
+                prefix_attention_workspace(q, k_new, table, k_cache, starts) if ws is None else ws)
+
+    if stream is None:
+        out, lse, ws = room()
+    else:
+        with _on(stream):
+            out, lse, ws = room()
+    os = _values(out, "out", dtype, shape, device)
+    a = EncPrefixAttentionArgs.from_buffer_copy(_PREFIX_PACK(
+        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
+        lse.data_ptr() if lse is not None else 0, tp, lp, sp, np_, mp,
+        qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], cs[0], cs[1], cs[2], os[0], os[1], os[2],
+        batch, n, q_heads, kv_heads, dim, _code(dtype), pages, page, max_pages, max_seqs,
+        dim ** -0.5 if scale is None else scale, 0, stp, shp, groups, 0))
+    _check(lib().enc_prefix_attention(ctypes.byref(a), *_scratch(ws, device), _handle(stream, device)))
+    return out, lse
+
+
 def enc_verify_tree_workspace_bytes(batch, nodes, vocab):
     return int(lib().enc_verify_tree_workspace_bytes(batch, nodes, vocab))
 
@@ -1053,6 +1126,28 @@ def enc_cache_fork(cache, src, dst, stream=None):
     _check(lib().enc_cache_fork(
         cache.ref, _plain(src, "src", _I32, (src.numel(),), device),
         _plain(dst, "dst", _I32, src.shape, device), src.shape[0], _handle(stream, device)))
+
+
+def enc_cache_shared(cache, seqs, starts, out=None, stream=None):
+    """Leading tokens that the sequences of each group hold in the same pages:
+    group g is seqs[starts[g]:starts[g + 1]]. starts: int32 [groups + 1]. Returns
+    int32 [groups] (out)."""
+    device = _device_of(cache.data)
+    groups = starts.numel() - 1
+    if groups < 0:
+        raise ValueError("starts holds one number more than there are groups")
+    if out is None:
+        if stream is None:
+            out = starts.new_empty(groups)
+        else:
+            with _on(stream):
+                out = starts.new_empty(groups)
+    batch = seqs.numel()
+    _check(lib().enc_cache_shared(
+        cache.ref, _plain(seqs, "seqs", _I32, (batch,), device), batch,
+        _plain(starts, "starts", _I32, (groups + 1,), device), groups, _plain(out, "out", _I32, (groups,), device),
+        _handle(stream, device)))
+    return out
 
 
 def enc_cache_truncate(cache, seqs, lens, stream=None):
