@@ -34,8 +34,7 @@ constexpr uint32_t kWays = 4;          // waves of a workgroup, on different str
 constexpr uint32_t kPlanThreads = 1024;
 
 struct Seq {
-  uint32_t len, live;
-  const int32_t *table;
+  uint32_t len, live, row;   // row: of the table
 };
 
 __device__ __forceinline__ Seq sequence_of(const enc_tree_attention_args &a, uint32_t b) {
@@ -45,7 +44,7 @@ __device__ __forceinline__ Seq sequence_of(const enc_tree_attention_args &a, uin
   int32_t len = s < a.max_seqs ? a.d_lens[s] : 0;
   len = max(len, 0);
   q.len = (uint64_t)len > room ? (uint32_t)room : (uint32_t)len;
-  q.table = a.d_table + (uint64_t)(s < a.max_seqs ? s : 0) * a.max_pages;
+  q.row = s < a.max_seqs ? s : 0;
   int32_t live = a.d_nodes ? a.d_nodes[b] : (int32_t)a.nodes;
   q.live = (uint32_t)max(0, min(live, (int32_t)a.nodes));
   return q;
@@ -77,9 +76,155 @@ template <typename V> __device__ __forceinline__ V group_scan(V v, V *side, V &t
   return before + v;
 }
 
-// Group g is the batch entries from the greatest start up to g to the greatest up
-// to g + 1: for ascending starts the starts themselves, for any others ranges
-// that do not overlap.
+// Strips in a piece: an equal share of all, whole rounds of the waves.
+__device__ __forceinline__ uint32_t size_of(unsigned long long work, uint32_t slots, uint32_t least) {
+  const unsigned long long each = min((work + slots - 1) / slots, 1ull << 30);
+  return (uint32_t)max((each + kWays - 1) / kWays * kWays, (unsigned long long)least);
+}
+
+// The plan where every group and every sequence has a thread: numbers stay in
+// registers and LDS, and the loads that they come from are on their way at once
+// (one group of 64: 4 us, 12 by the general kernel below). Group g is the batch
+// entries from the greatest start up to g to the greatest up to g + 1: for
+// ascending starts the starts themselves, for any others ranges that do not
+// overlap.
+__global__ __launch_bounds__(kPlanThreads) void k_prefix_plan_small(PrefixAttnArgs k) {
+  const enc_tree_attention_args &a = k.a;
+  typedef unsigned long long u64;
+  __shared__ uint32_t ends[kPlanThreads + 1], common[kPlanThreads], group_at[kPlanThreads + 1], own_at[kPlanThreads + 1];
+  __shared__ uint32_t first[kPlanThreads], lens[kPlanThreads], lives[kPlanThreads], seqs[kPlanThreads];
+  __shared__ uint32_t tops[kPlanThreads / 64];
+  __shared__ u64 side[kPlanThreads / 64], side2[kPlanThreads / 64], side3[kPlanThreads / 64];
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, threads = blockDim.x;   // > groups, >= batch
+  const uint32_t per = a.nodes * k.group.d, groups = k.groups, batch = a.batch;
+  uint32_t v = tid <= groups ? (uint32_t)max(0, min(k.starts[tid], (int32_t)batch)) : 0u;
+  const uint32_t asked = tid < groups ? (uint32_t)max(k.shared[tid], 0) : 0u;
+  Seq q;
+  q.len = q.live = q.row = 0;
+  if (tid < batch) q = sequence_of(a, tid);
+
+  for (uint32_t o = 1; o < 64; o <<= 1) {
+    const uint32_t w = __shfl_up(v, o);
+    if (lane >= o) v = max(v, w);
+  }
+  if (lane == 63) tops[wave] = v;
+  __syncthreads();
+  for (uint32_t w = 0; w < wave; ++w) v = max(v, tops[w]);
+  ends[tid] = v;   // past the last group: the last end, or greater ones that nobody reads
+  if (tid < groups) common[tid] = asked;
+  __syncthreads();
+  // the group of this thread's sequence: the last one that begins at or before it
+  uint32_t g = ~0u;
+  if (tid < batch && groups && tid >= ends[0] && tid < ends[groups]) {
+    uint32_t low = 0, high = groups;   // ends[low] <= tid < ends[high]
+    while (high - low > 1) {
+      const uint32_t mid = (low + high) / 2;
+      if (ends[mid] <= tid) low = mid; else high = mid;
+    }
+    g = low;
+    atomicMin(&common[g], q.len);
+  }
+  __syncthreads();
+  uint32_t rows = 0, tiles = 0, units = 0;
+  if (tid < groups) {
+    const uint32_t n = ends[tid + 1] - ends[tid];
+    if (n < 2) common[tid] = 0;   // nobody to share with
+    rows = n * per;
+    tiles = (rows + k.tile - 1) / k.tile;
+    units = (common[tid] + 31) / 32;
+  }
+  __syncthreads();
+  uint32_t own_units = 0;
+  if (tid < batch) {
+    const uint32_t f = g != ~0u ? common[g] : 0u;
+    first[tid] = f;
+    lens[tid] = q.len;
+    lives[tid] = q.live;
+    seqs[tid] = q.row;
+    own_units = (q.len - f + 31) / 32 + (q.live + 31) / 32;
+    k.group_of[tid] = g;
+    k.first[tid] = f;
+  }
+  u64 work = (u64)tiles * units, own_work = (u64)k.own_tiles * own_units;
+  for (uint32_t o = 32; o; o >>= 1) {
+    work += __shfl_xor(work, o);
+    own_work += __shfl_xor(own_work, o);
+  }
+  if (lane == 0) side[wave] = work, side2[wave] = own_work;
+  __syncthreads();
+  work = own_work = 0;
+  for (uint32_t w = 0; w < threads / 64; ++w) work += side[w], own_work += side2[w];
+  const uint32_t size = size_of(work, k.slots, k.least), own_size = size_of(own_work, k.own_slots, k.least);
+
+  // pieces before each group's and each sequence's, both in one scan
+  const uint32_t n = (units + size - 1) / size, own_n = tid < batch ? max((own_units + own_size - 1) / own_size, 1u) : 0u;
+  const u64 mine = (u64)(n * tiles) << 32 | own_n * k.own_tiles;
+  u64 upto = wave_scan(mine);
+  if (lane == 63) side3[wave] = upto;
+  __syncthreads();
+  u64 all = 0;
+  for (uint32_t w = 0; w < threads / 64; ++w) {
+    if (w < wave) upto += side3[w];
+    all += side3[w];
+  }
+  upto -= mine;
+  const uint32_t shared_items = (uint32_t)(all >> 32), own_items = (uint32_t)all;
+  group_at[tid] = (uint32_t)(upto >> 32);
+  own_at[tid] = (uint32_t)upto;
+  if (tid == 0) {
+    group_at[threads] = shared_items;
+    own_at[threads] = own_items;
+    k.counts[0] = shared_items;
+    k.counts[1] = shared_items + own_items;
+  }
+  if (tid <= groups) k.ends[tid] = ends[tid];
+  if (tid < groups) {
+    k.common[tid] = common[tid];
+    k.group_parts[tid] = make_uint2((uint32_t)(upto >> 32), n);
+  }
+  if (tid < batch) k.own_parts[tid] = make_uint2((uint32_t)upto, own_n);
+  __syncthreads();
+  // a thread to a piece: whose it is, by its place
+  for (uint32_t i = tid; i < shared_items + own_items; i += threads) {
+    const bool own = i >= shared_items;
+    const uint32_t j = own ? i - shared_items : i;
+    const uint32_t *at = own ? own_at : group_at;
+    uint32_t low = 0, high = threads;   // at[low] <= j < at[high]
+    while (high - low > 1) {
+      const uint32_t mid = (low + high) / 2;
+      if (at[mid] <= j) low = mid; else high = mid;
+    }
+    PrefixItem it;
+    if (own) {
+      const uint32_t part = (j - at[low]) / k.own_tiles;
+      it.b = low;
+      it.row0 = (j - at[low] - part * k.own_tiles) * k.own_tile;
+      it.rows = per;
+      it.first = first[low];
+      it.ctx = lens[low] - it.first;
+      it.tree = lives[low];
+      it.lo = part * own_size;
+      it.hi = min((it.ctx + 31) / 32 + (it.tree + 31) / 32, it.lo + own_size);
+      it.turn = low + part;
+      it.seq = seqs[low];
+    } else {
+      it.b = ends[low];
+      it.rows = (ends[low + 1] - it.b) * per;
+      const uint32_t t = (it.rows + k.tile - 1) / k.tile, part = (j - at[low]) / t;
+      it.row0 = (j - at[low] - part * t) * k.tile;
+      it.first = 0;
+      it.ctx = common[low];
+      it.tree = 0;
+      it.lo = part * size;
+      it.hi = min((it.ctx + 31) / 32, it.lo + size);
+      it.turn = part;
+      it.seq = seqs[it.b];
+    }
+    k.items[i] = it;
+  }
+}
+
+// The same for any number of groups and sequences.
 __global__ __launch_bounds__(kPlanThreads) void k_prefix_plan(PrefixAttnArgs k) {
   const enc_tree_attention_args &a = k.a;
   typedef unsigned long long u64;
@@ -126,20 +271,18 @@ __global__ __launch_bounds__(kPlanThreads) void k_prefix_plan(PrefixAttnArgs k) 
   }
   __syncthreads();
 
-  // work: strips of all tiles of rows, a strip of many rows counting more
-  u64 work = 0, total;
+  u64 work = 0, own_work = 0, all = 0, own_all = 0;   // strips of all tiles of rows
   for (uint32_t g = tid; g < k.groups; g += kPlanThreads) {
     const uint32_t tiles = ((k.ends[g + 1] - k.ends[g]) * per + k.tile - 1) / k.tile;
-    work += (u64)tiles * ((k.common[g] + 31) / 32) * k.weight;
+    work += (u64)tiles * ((k.common[g] + 31) / 32);
   }
   for (uint32_t b = tid; b < a.batch; b += kPlanThreads) {
     const Seq q = sequence_of(a, b);
-    work += (u64)k.own_tiles * ((q.len - k.first[b] + 31) / 32 + (q.live + 31) / 32);
+    own_work += (u64)k.own_tiles * ((q.len - k.first[b] + 31) / 32 + (q.live + 31) / 32);
   }
-  group_scan(work, side64, total);
-  const u64 each = min((total + k.slots - 1) / k.slots, (u64)1 << 30);
-  const uint32_t own_size = (uint32_t)max((each + kWays - 1) / kWays * kWays, (u64)k.least);
-  const uint32_t size = (uint32_t)max((each + k.weight * kWays - 1) / (k.weight * kWays) * kWays, (u64)k.least);
+  group_scan(work, side64, all);
+  group_scan(own_work, side64, own_all);
+  const uint32_t size = size_of(all, k.slots, k.least), own_size = size_of(own_all, k.own_slots, k.least);
 
   uint32_t slots = 0, sum;
   for (uint32_t g0 = 0; g0 < k.groups; g0 += kPlanThreads) {
@@ -164,6 +307,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_prefix_plan(PrefixAttnArgs k) 
       it.tree = 0;
       it.lo = part * size;
       it.hi = min(units, it.lo + size);
+      it.turn = part;
+      it.seq = tiles ? sequence_of(a, it.b).row : 0;
       k.items[base + i] = it;
     }
     slots += sum;
@@ -181,6 +326,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_prefix_plan(PrefixAttnArgs k) 
       it.first = k.first[b];
       it.ctx = q.len - it.first;
       it.tree = q.live;
+      it.seq = q.row;
       units = (it.ctx + 31) / 32 + (it.tree + 31) / 32;
       n = max((units + own_size - 1) / own_size, 1u);
     }
@@ -191,6 +337,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_prefix_plan(PrefixAttnArgs k) 
       it.row0 = (i - part * k.own_tiles) * k.own_tile;
       it.lo = part * own_size;
       it.hi = min(units, it.lo + own_size);
+      it.turn = b + part;
       k.items[slots + base + i] = it;
     }
     own += sum;
@@ -198,12 +345,29 @@ __global__ __launch_bounds__(kPlanThreads) void k_prefix_plan(PrefixAttnArgs k) 
   if (tid == 0) k.counts[1] = slots + own;
 }
 
+// A piece's numbers: the workgroup's, so scalars.
+__device__ __forceinline__ PrefixItem item_of(const PrefixAttnArgs &k, uint32_t item) {
+  const uint32_t *w = reinterpret_cast<const uint32_t *>(k.items + item);
+  PrefixItem it;
+  it.b = __builtin_amdgcn_readfirstlane(w[0]);
+  it.row0 = __builtin_amdgcn_readfirstlane(w[1]);
+  it.rows = __builtin_amdgcn_readfirstlane(w[2]);
+  it.first = __builtin_amdgcn_readfirstlane(w[3]);
+  it.ctx = __builtin_amdgcn_readfirstlane(w[4]);
+  it.tree = __builtin_amdgcn_readfirstlane(w[5]);
+  it.lo = __builtin_amdgcn_readfirstlane(w[6]);
+  it.hi = __builtin_amdgcn_readfirstlane(w[7]);
+  it.turn = __builtin_amdgcn_readfirstlane(w[8]);
+  it.seq = __builtin_amdgcn_readfirstlane(w[9]);
+  return it;
+}
+
 // ---- a piece
 
 // U: 16-row units of the tile. EXACT: head_dim is DP. OWN: the sequence's own
 // tokens and its tree; else shared ones.
 template <typename T, int DP, int U, bool EXACT, bool OWN>
-__device__ __forceinline__ void piece(const PrefixAttnArgs &k, uint32_t item, uint32_t h, uint64_t at, float *joint) {
+__device__ __forceinline__ void piece(const PrefixAttnArgs &k, const PrefixItem &it, uint32_t h, uint64_t at, float *joint) {
   constexpr int KS = DP / 32;                   // k steps of Q K^T
   constexpr int C = DP >= 128 ? 8 : DP / 16;    // consecutive values a lane transposes
   constexpr int NH = DP / (16 * C);             // groups of 16 C values
@@ -212,24 +376,8 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, uint32_t item, ui
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t l16 = lane & 15, g4 = lane >> 4;
   const uint32_t D = a.head_dim;
-  PrefixItem it;
-  {
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(k.items + item);   // the workgroup's: scalars
-    it.b = __builtin_amdgcn_readfirstlane(w[0]);
-    it.row0 = __builtin_amdgcn_readfirstlane(w[1]);
-    it.rows = __builtin_amdgcn_readfirstlane(w[2]);
-    it.first = __builtin_amdgcn_readfirstlane(w[3]);
-    it.ctx = __builtin_amdgcn_readfirstlane(w[4]);
-    it.tree = __builtin_amdgcn_readfirstlane(w[5]);
-    it.lo = __builtin_amdgcn_readfirstlane(w[6]);
-    it.hi = __builtin_amdgcn_readfirstlane(w[7]);
-  }
   const uint32_t b0 = it.b, first = OWN ? it.first : 0, ctx = it.ctx;
-  const int32_t *table;
-  {
-    const uint32_t s = a.d_seqs ? (uint32_t)a.d_seqs[b0] : b0;
-    table = a.d_table + (uint64_t)(s < a.max_seqs ? s : 0) * a.max_pages;
-  }
+  const int32_t *table = a.d_table + (uint64_t)it.seq * a.max_pages;
   const uint32_t strips_ctx = (ctx + 31) / 32, lo = it.lo, hi = it.hi;
 
   // ---- Q fragments: query row l % 16 of each unit, 8 values per k step. A row
@@ -281,21 +429,27 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, uint32_t item, ui
     if (OWN && strip >= strips_ctx) return 0;
     return table[k.page.quot(first + min(strip * 32 + (lane & 31), ctx - 1))];
   };
-  auto offsets_of = [&](uint32_t strip, int32_t e, uint32_t &ko, uint32_t &vo) {
+  uint32_t ko[2], vo[8];   // of the keys that this lane loads, got from the lanes that know them
+  auto offsets_of = [&](uint32_t strip, int32_t e) {
+    uint32_t k_at, v_at;
     if (!OWN || strip < strips_ctx) {
       const uint32_t key = first + min(strip * 32 + (lane & 31), ctx - 1), page = min((uint32_t)max(e, 0), a.n_pages - 1);
-      ko = vo = page * page_units + (key - k.page.quot(key) * k.page.d) * token_units;
+      k_at = v_at = page * page_units + (key - k.page.quot(key) * k.page.d) * token_units;
     } else {
       const uint32_t key = min((strip - strips_ctx) * 32 + (lane & 31), it.tree - 1);
-      ko = key * (uint32_t)(a.k_new_node / 8);
-      vo = key * (uint32_t)(a.v_new_node / 8);
+      k_at = key * (uint32_t)(a.k_new_node / 8);
+      v_at = key * (uint32_t)(a.v_new_node / 8);
     }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) ko[t] = (uint32_t)__shfl((int)k_at, 16 * t + l16);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) vo[j] = (uint32_t)__shfl((int)v_at, 16 * (j >> 2) + 4 * g4 + (j & 3));
   };
-  auto load_k = [&](uint32_t strip, uint32_t off) {
+  auto load_k = [&](uint32_t strip) {
     const uint4 *base = !OWN || strip < strips_ctx ? kc : reinterpret_cast<const uint4 *>(kn);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const uint4 *p = base + (uint32_t)__shfl((int)off, 16 * t + l16);
+      const uint4 *p = base + ko[t];
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const uint32_t c = 4 * s + g4;
@@ -308,11 +462,11 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, uint32_t item, ui
       }
     }
   };
-  auto load_v = [&](uint32_t strip, uint32_t off) {
+  auto load_v = [&](uint32_t strip) {
     const uint4 *base = !OWN || strip < strips_ctx ? vc : reinterpret_cast<const uint4 *>(vn);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint4 *p = base + (uint32_t)__shfl((int)off, 16 * (j >> 2) + 4 * g4 + (j & 3));
+      const uint4 *p = base + vo[j];
 #pragma unroll
       for (int n = 0; n < NH; ++n) {
         uint32_t d = (n * 16 + l16) * C;
@@ -360,7 +514,9 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, uint32_t item, ui
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[u][4 * t + e] = s[e];
       }
+    __builtin_amdgcn_sched_barrier(0);   // the next strip's K into the same registers
     after_k();
+    __builtin_amdgcn_sched_barrier(0);
 
     const bool tree = OWN && SPECIAL && strip >= strips_ctx;
     const uint32_t from = (tree ? strip - strips_ctx : strip) * 32;
@@ -435,40 +591,46 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, uint32_t item, ui
 #pragma unroll
         for (int u = 0; u < U; ++u) o[u][n][f] = Half<T>::mfma(vf, pf[u], o[u][n][f]);
       }
+    __builtin_amdgcn_sched_barrier(0);
     after_v();
+    __builtin_amdgcn_sched_barrier(0);
   };
 
-  const uint32_t whole = min(hi, ctx / 32);     // strips of 32 cached keys
+  // Whole strips of cached keys but the wave's last: every one loads the next
+  // without asking whether there is one (a branch around loads makes the waits
+  // behind it wait for all of them). The last whole strip, the one that is not
+  // full and the tree's follow, one load at a time.
+  const uint32_t whole = min(hi, ctx / 32);
   uint32_t strip = lo + wave;
-  uint32_t ko, vo;
-  if (strip < whole) {
-    offsets_of(strip, entry_of(strip), ko, vo);
-    load_k(strip, ko);
-    load_v(strip, vo);
-    int32_t entry = strip + kWays < whole ? entry_of(strip + kWays) : 0;
-    while (true) {
+  if (strip < hi) {
+    offsets_of(strip, entry_of(strip));
+    // in the loop's order, or its waits allow for both
+    load_k(strip);
+    __builtin_amdgcn_sched_barrier(0);
+    int32_t entry = entry_of(min(strip + kWays, hi - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    load_v(strip);
+    __builtin_amdgcn_sched_barrier(0);
+    while (strip + kWays < whole) {
       const uint32_t next = strip + kWays;
-      const bool more = next < whole;
-      if (more) offsets_of(next, entry, ko, vo);
+      offsets_of(next, entry);
       compute(
           std::false_type{}, strip,
           [&] {
-            if (!more) return;
-            load_k(next, ko);
-            entry = next + kWays < whole ? entry_of(next + kWays) : 0;
+            load_k(next);
+            entry = entry_of(min(next + kWays, hi - 1));
           },
-          [&] {
-            if (more) load_v(next, vo);
-          });
+          [&] { load_v(next); });
       strip = next;
-      if (!more) break;
     }
-  }
-  for (; strip < hi; strip += kWays) {
-    offsets_of(strip, entry_of(strip), ko, vo);
-    load_k(strip, ko);
-    load_v(strip, vo);
-    compute(std::true_type{}, strip, [] {}, [] {});
+    while (true) {
+      compute(std::true_type{}, strip, [] {}, [] {});
+      strip += kWays;
+      if (strip >= hi) break;
+      offsets_of(strip, entry_of(strip));
+      load_k(strip);
+      load_v(strip);
+    }
   }
   // Infinities and NaN went in as zeros, since 0 times them would reach rows
   // that do not see them: add them to the rows that do.
@@ -557,18 +719,442 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, uint32_t item, ui
   }
 }
 
-// UP, US: units of a tile of shared and of own tokens' rows.
+// The pieces from item0 on. UP, US: units of a tile of shared (0: another kernel
+// takes those) and of own tokens' rows.
 template <typename T, int DP, int UP, int US, bool EXACT>
-__global__ __launch_bounds__(256, (DP == 256 || UP * DP > 256 ? 1 : 2)) void k_pieces(PrefixAttnArgs k) {
+__global__ __launch_bounds__(256, (DP == 256 ? 1 : UP + US == 1 ? 3 : 2)) void k_pieces(PrefixAttnArgs k) {
   constexpr int U = UP > US ? UP : US;
   __shared__ float joint[2 * (U * DP / 4 + 2 * U) * 64];
-  const uint32_t heads = k.a.kv_heads, item = blockIdx.x / heads, h = blockIdx.x - item * heads;
-  const uint32_t shared = __builtin_amdgcn_readfirstlane(k.counts[0]);
+  const uint32_t shared = __builtin_amdgcn_readfirstlane(k.counts[0]), heads = k.a.kv_heads;
+  const uint32_t at = blockIdx.x / heads, item = UP ? at : at + shared;
+  const PrefixItem it = item_of(k, item);   // on its way with the count
   if (item >= __builtin_amdgcn_readfirstlane(k.counts[1])) return;
-  if (item < shared)
-    piece<T, DP, UP, EXACT, false>(k, item, h, ((uint64_t)item * heads + h) * (16 * UP), joint);
-  else
-    piece<T, DP, US, EXACT, true>(k, item, h, k.own_rows + ((uint64_t)(item - shared) * heads + h) * (16 * US), joint);
+  // Neighbouring workgroups differ in their head; with 8 heads the tiles of a
+  // range meet on one die and in its L2.
+  const uint32_t h = (blockIdx.x - at * heads + it.turn) % heads;
+  if constexpr (UP)
+    if (item < shared) {
+      piece<T, DP, UP, EXACT, false>(k, it, h, ((uint64_t)item * heads + h) * (16 * UP), joint);
+      return;
+    }
+  piece<T, DP, US, EXACT, true>(k, it, h, k.own_rows + ((uint64_t)(item - shared) * heads + h) * (16 * US), joint);
+}
+
+// ---- pieces of shared tokens with many rows: K and V through LDS
+//
+// Eight waves: four tiles of U units of rows, two at different keys. A stage of
+// 64 keys is brought in by all of them and read by each, 32 keys of it, so that
+// a range's sums are joined over two waves and its rows written once: with eight
+// tiles of rows on the same keys there would be twice the partial sums, which
+// cost as much HBM traffic as the keys themselves at 256 rows and 8192 tokens.
+// Direct loads into fragments, as in `piece`, take a cache line for every 16
+// bytes of K: 64 rows and more wait for that. Heads up to 128 values: three
+// stages lie in LDS (the one computed, the next, whose first K fragments are read
+// early, and the one a slower wave may still be in), a fourth is on its way into
+// registers. Above: two, for want of registers and LDS. Banks: a wave reads one
+// 16-byte chunk of 16 rows of K at a time, so chunk c of row r lies at
+// c ^ k_turn(r); of V it reads 32 bytes of 8 rows, so rows lie 32 bytes further
+// apart than they are long. V^T fragments come from ds_read_b64_tr.
+template <int NCH> __device__ __forceinline__ constexpr uint32_t k_turn(uint32_t r) {
+  return NCH == 8 ? r >> 1 & 7 : r & 15;   // 16 rows (two to 256 bytes, for 8 chunks) on 16 places
+}
+
+constexpr uint32_t kStage = 64;      // keys of a stage
+constexpr float kFar = 65536.f;      // see below
+
+template <typename T, int DP, int U>
+__global__ __launch_bounds__(512, 2) void k_shared(PrefixAttnArgs k) {
+  constexpr int KS = DP / 32, NF = DP / 16, NCH = DP / 8;
+  constexpr bool PIPE = DP <= 128;                 // registers for a strip's K and V fragments at once
+  constexpr uint32_t NB = PIPE ? 3 : 2;            // stages in LDS
+  constexpr int NT = 512, NR = kStage * NCH / NT;  // chunks of K (and of V) a thread brings in
+  constexpr int PITCH = NCH + 2;                   // 16-byte chunks from row to row of V
+  constexpr uint32_t kRows = 64 * U;               // of the tile
+  const enc_tree_attention_args &a = k.a;
+  __shared__ __align__(16) uint4 room[NB * kStage * (NCH + PITCH)];
+  uint4 *const ks = room, *const vs = room + NB * kStage * NCH;
+
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t l16 = lane & 15, g4 = lane >> 4, half = wave >> 2;   // the strip of a stage that is this wave's
+  const uint32_t D = a.head_dim, heads = a.kv_heads, item = blockIdx.x / heads;
+  const PrefixItem it = item_of(k, item);   // on its way with the count
+  if (item >= __builtin_amdgcn_readfirstlane(k.counts[0])) return;
+  const uint32_t h = (blockIdx.x - item * heads + it.turn) % heads, ctx = it.ctx;
+  const uint32_t lo = it.lo / 2, hi = (it.hi + 1) / 2;   // stages
+  const int32_t *table = a.d_table + (uint64_t)it.seq * a.max_pages;
+
+  const uint32_t first_row = it.row0 + (wave & 3) * (16 * U);
+  const bool busy = first_row < it.rows;   // this wave has rows
+  uint4 qf[U][KS];
+  const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;   // -scale (-q).k
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t r = first_row + 16 * u + l16, rr = min(r, it.rows - 1);
+    const uint32_t turn = k.group.quot(rr), member = k.nodes.quot(turn), node = turn - member * a.nodes;
+    const uint32_t head = h * k.group.d + (rr - turn * k.group.d);
+    const T *p = static_cast<const T *>(a.d_q) + (it.b + member) * a.q_batch + node * a.q_node + head * a.q_head;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const uint32_t d = 32 * s + 8 * g4;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < it.rows && d < D) v = *reinterpret_cast<const uint4 *>(p + d);
+      qf[u][s] = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+    }
+  }
+  // A key's weight is 2^(p c2 - mc), p = q.k: one fma, exact until it is rounded,
+  // so that mc, the row's maximum mr times c2 (less the lift), may be rounded as
+  // it likes. From kFar on the rounding of mc alone is no longer small beside 1:
+  // there it is 2^((p - mr) c2), whose difference is exact where it is small.
+  const float c2 = k.unit, slack = k.slack;
+  f32x4 o[U][NF];
+  float mr[U], mc[U], l[U];   // mr: -infinity until the row has seen a key
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    mr[u] = -__builtin_inff();
+    mc[u] = kLowest;
+    l[u] = 0.f;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) o[u][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  bool far = false;   // some row of the wave has got there
+  auto beyond = [&](int u) { return !(fabsf(mc[u]) < kFar); };   // this one (or it has seen nothing)
+
+  // ---- bringing a stage in: thread's chunk i is chunk ch of row r0 + i kRowStep
+  const uint32_t ch = tid % NCH, r0 = tid / NCH;
+  constexpr uint32_t kRowStep = NT / NCH;
+  const bool chunk_live = ch * 8 < D;
+  // One or two stages are on their way into registers while another waits in LDS. Loads
+  // are never behind a branch (one would make the waits behind it wait for all):
+  // stages past the last stand for the last, keys past the end for the last one,
+  // and what is no key's becomes 0 when it is placed.
+  const uint4 *kc = static_cast<const uint4 *>(a.d_k_cache) + h * (a.cache_head / 8) + (chunk_live ? ch : 0);
+  const uint4 *vc = static_cast<const uint4 *>(a.d_v_cache) + h * (a.cache_head / 8) + (chunk_live ? ch : 0);
+  const uint32_t page_units = (uint32_t)(a.cache_page / 8), token_units = (uint32_t)(a.cache_token / 8);
+  constexpr uint32_t kAhead = 2;      // stages on their way: registers
+  uint4 kr[kAhead][NR], vr[kAhead][NR];
+  const uint32_t whole_end = min(hi, ctx / kStage);   // stages from here on are not full
+  const bool part = D != DP;
+  auto entry_of = [&](uint32_t st) { return table[k.page.quot(min(min(st, hi - 1) * kStage + lane, ctx - 1))]; };
+  auto fetch = [&](auto slot_, uint32_t st, int32_t entry) __attribute__((always_inline)) {   // entry: for key lane
+    constexpr int S = decltype(slot_)::value;
+    const uint32_t key = min(min(st, hi - 1) * kStage + lane, ctx - 1), page = min((uint32_t)max(entry, 0), a.n_pages - 1);
+    const uint32_t at = page * page_units + (key - k.page.quot(key) * k.page.d) * token_units;
+    uint32_t off[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) off[i] = (uint32_t)__shfl((int)at, r0 + i * kRowStep);
+#pragma unroll
+    for (int i = 0; i < NR; ++i) kr[S][i] = kc[off[i]];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) vr[S][i] = vc[off[i]];
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto place = [&](auto slot_, uint32_t st, uint32_t buf) __attribute__((always_inline)) {
+    constexpr int S = decltype(slot_)::value;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const uint32_t r = r0 + i * kRowStep;
+      uint4 kv = kr[S][i], vv = vr[S][i];
+      if (part || st >= whole_end) {   // a branch, not selects on every stage's way
+        asm volatile("");
+        if (!chunk_live || st * kStage + r >= ctx) kv = vv = make_uint4(0, 0, 0, 0);
+      }
+      ks[(buf * kStage + r) * NCH + (ch ^ k_turn<NCH>(r))] = kv;
+      vs[(buf * kStage + r) * PITCH + ch] = vv;
+    }
+  };
+
+  // New maxima where a strip exceeds the old ones, and what is summed so far
+  // brought to them; other rows stay as they are, to the bit.
+  auto grow = [&](const float (&top)[U]) __attribute__((always_inline)) {
+    bool out = false;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float up = top[u] - mr[u] > slack ? top[u] : mr[u], at = fmaf(up, c2, -Half<T>::kLift2);
+      const bool was = beyond(u), is = !(fabsf(at) < kFar);
+      const float by = was ? is ? (mr[u] - up) * c2 : fmaf(mr[u], c2, -at) - Half<T>::kLift2
+                           : is ? fmaf(-up, c2, mc[u]) + Half<T>::kLift2 : mc[u] - at;
+      const float shrink = mr[u] > -__builtin_inff() ? __builtin_amdgcn_exp2f(by) : 0.f;
+      mr[u] = up;
+      mc[u] = fmaxf(at, kLowest);
+      out = out || (is && up > -__builtin_inff());
+      l[u] *= shrink;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) o[u][f] *= shrink;
+    }
+    far = __any(out);
+  };
+
+  float p[U][8], top[U];
+  uint4 kf[2][KS];
+  auto read_k = [&](uint32_t buf) {
+    const uint4 *row = ks + (buf * kStage + half * 32 + l16) * NCH;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < KS; ++e) kf[t][e] = row[16 * t * NCH + ((4 * e + g4) ^ k_turn<NCH>(l16))];
+  };
+  auto maxima = [&] {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float t = p[u][0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) t = fmaxf(t, p[u][j]);
+      top[u] = rows_max(t);
+    }
+  };
+  auto scores = [&](float (&x)[U][8]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      f32x4 s[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < KS; ++e)
+#pragma unroll
+        for (int u = 0; u < U; ++u) s[u] = Half<T>::mfma(kf[t][e], qf[u][e], s[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[u][4 * t + e] = s[u][e];
+    }
+  };
+  auto values_at = [&](uint32_t buf) {
+    return reinterpret_cast<const char *>(vs + (buf * kStage + half * 32 + 4 * g4 + (l16 >> 2)) * PITCH) + (l16 & 3) * 8;
+  };
+  // The weights of a strip whose maxima are known, packed; l grows by them. With
+  // `masked` only the keys of `bits` weigh anything. `between`: what runs beside
+  // the exponentials.
+  auto weigh = [&](auto masked_, uint32_t bits, uint4 (&pf)[U], auto between) __attribute__((always_inline)) {
+    bool grown = false;
+#pragma unroll
+    for (int u = 0; u < U; ++u) grown = grown || top[u] - mr[u] > slack;
+    if (__any(grown)) grow(top);
+    float off[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) off[u] = mc[u];
+    if (far) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float less = beyond(u) ? fmaxf(mr[u], kLowest) : 0.f;
+        if (beyond(u)) off[u] = -Half<T>::kLift2;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[u][j] -= less;
+      }
+    }
+    between();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        p[u][j] = __builtin_amdgcn_exp2f(fmaf(p[u][j], c2, -off[u]));
+        if constexpr (decltype(masked_)::value)   // -infinity times a scale of 0 is no number
+          if (!(bits >> (16 * (j >> 2) + 4 * g4 + (j & 3)) & 1u)) p[u][j] = 0.f;
+      }
+      l[u] += ((p[u][0] + p[u][1]) + (p[u][2] + p[u][3])) + ((p[u][4] + p[u][5]) + (p[u][6] + p[u][7]));
+      pf[u] = make_uint4(pack2<T>(p[u][0], p[u][1]), pack2<T>(p[u][2], p[u][3]), pack2<T>(p[u][4], p[u][5]),
+                         pack2<T>(p[u][6], p[u][7]));
+    }
+  };
+
+  // ---- a strip by itself: the last ones, and heads above 128 values
+  auto compute = [&](uint32_t st, uint32_t buf) __attribute__((always_inline)) {
+    const uint32_t from = st * kStage + half * 32;
+    const uint32_t bits = ctx >= from + 32 ? 0xFFFFFFFFu : ctx <= from ? 0u : (1u << (ctx - from)) - 1u;
+    if constexpr (PIPE) {
+      read_k(buf);
+      scores(p);
+    } else {   // half of K at a time: registers
+      const uint4 *row = ks + (buf * kStage + half * 32 + l16) * NCH;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f32x4 s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < KS; ++e) {
+          const uint4 f = row[16 * t * NCH + ((4 * e + g4) ^ k_turn<NCH>(l16))];
+#pragma unroll
+          for (int u = 0; u < U; ++u) s[u] = Half<T>::mfma(f, qf[u][e], s[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[u][4 * t + e] = s[u][e];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!(bits >> (16 * (j >> 2) + 4 * g4 + (j & 3)) & 1u)) p[u][j] = -__builtin_inff();
+    maxima();
+    uint4 pf[U];
+    weigh(std::true_type{}, bits, pf, [] {});
+    const char *vb = values_at(buf);
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const uint2 v0 = read_transposed(vb + 32 * f), v1 = read_transposed(vb + 16 * PITCH * 16 + 32 * f);
+      const uint4 vf = make_uint4(v0.x, v0.y, v1.x, v1.y);
+#pragma unroll
+      for (int u = 0; u < U; ++u) o[u][f] = Half<T>::mfma(vf, pf[u], o[u][f]);
+    }
+  };
+
+  // ---- whole strips, two in flight: while the exponentials of one are taken,
+  // the products of the next with K run, and while its products with V run, the
+  // next's maxima are taken
+  auto step = [&](uint32_t buf, uint32_t k_buf) __attribute__((always_inline)) {
+    if constexpr (PIPE) {
+      read_k(k_buf);
+      float x[U][8];
+      uint4 pf[U];
+      weigh(std::false_type{}, 0u, pf, [&] {
+        __builtin_amdgcn_sched_barrier(0);
+        scores(x);
+      });
+#pragma unroll
+      for (int i = 0; i < 2 * KS * U; ++i) {   // a product, then a few of the others, in turn
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[u][j] = x[u][j];
+      const char *vb = values_at(buf);
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const uint2 v0 = read_transposed(vb + 32 * f), v1 = read_transposed(vb + 16 * PITCH * 16 + 32 * f);
+        const uint4 vf = make_uint4(v0.x, v0.y, v1.x, v1.y);
+#pragma unroll
+        for (int u = 0; u < U; ++u) o[u][f] = Half<T>::mfma(vf, pf[u], o[u][f]);
+      }
+      maxima();
+#pragma unroll
+      for (int i = 0; i < NF * U; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  // A stage's turn. With PIPE the next one is placed ahead of it (its first K is
+  // read before the other's end), else the stage itself.
+  uint32_t st = lo, buf = 0;
+  int32_t entry;   // of the stage that is fetched next
+  auto turn_of = [&](auto slot_) __attribute__((always_inline)) {
+    constexpr int S = decltype(slot_)::value;
+    const uint32_t next = buf + 1 == NB ? 0 : buf + 1;
+    if constexpr (PIPE) {
+      place(std::integral_constant<int, S>{}, st + 1, next);
+      fetch(std::integral_constant<int, S>{}, st + 1 + kAhead, entry);
+      entry = entry_of(st + 2 + kAhead);
+      __syncthreads();
+      if (busy) step(buf, st + 1 < whole_end ? next : buf);   // else: products that nobody asks for
+    } else {
+      place(std::integral_constant<int, S>{}, st, buf);
+      fetch(std::integral_constant<int, S>{}, st + kAhead, entry);
+      entry = entry_of(st + 1 + kAhead);
+      __syncthreads();
+      if (busy) compute(st, buf);
+    }
+    buf = next;
+    ++st;
+  };
+  constexpr int kOther = kAhead - 1;
+  const int32_t e0 = entry_of(lo), e1 = entry_of(lo + 1), e2 = entry_of(lo + 2);
+  __builtin_amdgcn_sched_barrier(0);
+  fetch(std::integral_constant<int, 0>{}, lo, e0);
+  if constexpr (kAhead == 2) fetch(std::integral_constant<int, 1>{}, lo + 1, e1);
+  if constexpr (PIPE) {
+    place(std::integral_constant<int, 0>{}, lo, 0);
+    fetch(std::integral_constant<int, 0>{}, lo + kAhead, kAhead == 2 ? e2 : e1);
+    entry = entry_of(lo + 1 + kAhead);
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();
+    if (st < whole_end) {
+      if (busy) {
+        read_k(0);
+        scores(p);
+        maxima();
+      }
+      while (true) {
+        turn_of(std::integral_constant<int, kOther>{});
+        if (st >= whole_end) break;
+        if constexpr (kAhead == 2) {
+          turn_of(std::integral_constant<int, 0>{});
+          if (st >= whole_end) break;
+        }
+      }
+    }
+    if (st < hi) {   // one that is not full
+      __syncthreads();
+      if (busy) compute(st, buf);
+    }
+  } else {
+    entry = kAhead == 2 ? e2 : e1;
+    while (true) {
+      turn_of(std::integral_constant<int, 0>{});
+      if (st >= hi) break;
+      if constexpr (kAhead == 2) {
+        turn_of(std::integral_constant<int, 1>{});
+        if (st >= hi) break;
+      }
+    }
+  }
+
+  // ---- join the two waves of a tile, write
+  constexpr uint32_t kLane = U * (4 * NF + 2);   // numbers of a lane
+  static_assert(kLane * 64 * 4 * 4 <= sizeof(room), "the sums of four waves fit the stages' room");
+  float *const mine = reinterpret_cast<float *>(room) + (wave & 3) * kLane * 64 + lane;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    // sums of weights 2^((p - mr) c2 + lift), whichever way they were taken
+    const float fix = beyond(u) ? 1.f : __builtin_amdgcn_exp2f(fmaf(-mr[u], c2, mc[u]) + Half<T>::kLift2);
+    l[u] = rows_sum(l[u]) * fix;
+    mr[u] = fmaxf(mr[u], kLowest);
+#pragma unroll
+    for (int f = 0; f < NF; ++f) o[u][f] *= fix;
+  }
+  __syncthreads();
+  if (half == 1) {
+    uint32_t i = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      mine[64 * i++] = mr[u];
+      mine[64 * i++] = l[u];
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mine[64 * i++] = o[u][f][e];
+    }
+  }
+  __syncthreads();
+  if (half == 1 || !busy) return;
+  uint32_t i = 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float m2 = mine[64 * i++], l2 = mine[64 * i++];
+    const float up = fmaxf(mr[u], m2);
+    const float w1 = __builtin_amdgcn_exp2f((mr[u] - up) * c2), w2 = __builtin_amdgcn_exp2f((m2 - up) * c2);
+    l[u] = l[u] * w1 + l2 * w2;
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[u][f][e] = o[u][f][e] * w1 + mine[64 * i++] * w2;
+    if (first_row + 16 * u + l16 >= it.rows) continue;
+    const uint64_t row = ((uint64_t)item * heads + h) * kRows + (wave & 3) * (16 * U) + 16 * u + l16;
+    if (g4 == 0) *reinterpret_cast<float2 *>(k.part_ml + 2 * row) = make_float2(up, l[u]);
+    float *dst = k.part + row * D;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const uint32_t d = 16 * f + 4 * g4;
+      if (d < D) *reinterpret_cast<f32x4 *>(dst + d) = o[u][f];
+    }
+  }
 }
 
 // ---- the join: a wave to a query row, its pieces in their order, 64 / LD of
@@ -635,8 +1221,8 @@ __global__ __launch_bounds__(256) void k_prefix_join(PrefixAttnArgs k) {
 }
 
 template <typename T, int DP, int UP, int US>
-void launch_pieces(const PrefixAttnArgs &k, const PrefixAttnPlan &p, hipStream_t s) {
-  const dim3 grid(p.items * k.a.kv_heads), block(256);
+void launch_pieces(const PrefixAttnArgs &k, uint32_t items, hipStream_t s) {
+  const dim3 grid(items * k.a.kv_heads), block(256);
   if (k.a.head_dim == DP)
     hipLaunchKernelGGL((k_pieces<T, DP, UP, US, true>), grid, block, 0, s, k);
   else
@@ -645,19 +1231,29 @@ void launch_pieces(const PrefixAttnArgs &k, const PrefixAttnPlan &p, hipStream_t
 
 template <typename T, int DP>
 void launch_dim(const PrefixAttnArgs &k, const PrefixAttnPlan &p, hipStream_t s) {
-  constexpr int UP = DP <= 128 ? 4 : 2;
-  if (p.tile == 16)
-    launch_pieces<T, DP, 1, 1>(k, p, s);
-  else if (p.own_tile == 16)
-    launch_pieces<T, DP, UP, 1>(k, p, s);
-  else
-    launch_pieces<T, DP, UP, UP>(k, p, s);
+  constexpr int US = DP <= 128 ? 2 : 1;   // units of many own rows
+  if (p.tile == 16) {
+    launch_pieces<T, DP, 1, 1>(k, p.items, s);
+    return;
+  }
+  const dim3 grid(p.most_shared * k.a.kv_heads), block(512);
+  if (p.tile == 64)
+    hipLaunchKernelGGL((k_shared<T, DP, 1>), grid, block, 0, s, k);
+  else if constexpr (DP <= 128)
+    hipLaunchKernelGGL((k_shared<T, DP, 2>), grid, block, 0, s, k);
+  if (p.own_tile == 16)
+    launch_pieces<T, DP, 0, 1>(k, p.most_own, s);
+  else if constexpr (US > 1)
+    launch_pieces<T, DP, 0, US>(k, p.most_own, s);
 }
 
 template <typename T>
 void launch_type(const PrefixAttnArgs &k, const PrefixAttnPlan &p, hipStream_t s) {
   const uint32_t D = k.a.head_dim, rows = k.a.batch * k.a.nodes * k.a.q_heads;
-  hipLaunchKernelGGL(k_prefix_plan, dim3(1), dim3(kPlanThreads), 0, s, k);
+  if (k.a.batch <= kPlanThreads && k.groups < kPlanThreads)
+    hipLaunchKernelGGL(k_prefix_plan_small, dim3(1), dim3((std::max({k.a.batch, k.groups + 1, 256u}) + 63) / 64 * 64), 0, s, k);
+  else
+    hipLaunchKernelGGL(k_prefix_plan, dim3(1), dim3(kPlanThreads), 0, s, k);
   if (D <= 64)
     launch_dim<T, 64>(k, p, s);
   else if (D <= 128)
@@ -673,8 +1269,7 @@ void launch_type(const PrefixAttnArgs &k, const PrefixAttnPlan &p, hipStream_t s
     hipLaunchKernelGGL((k_prefix_join<T, 64>), grid, block, 0, s, k);
 }
 
-// ---- how many leading tokens the sequences of a group have in common: table
-// entries are compared column by column, up to the first that differs
+// ---- how many leading tokens the sequences of a group have in common
 __global__ __launch_bounds__(kPlanThreads) void k_cache_shared(enc_cache c, const int32_t *seqs, uint32_t batch,
                                                                const int32_t *starts, int32_t *shared) {
   __shared__ uint32_t bottom, least, differs;
@@ -702,44 +1297,68 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_shared(enc_cache c, cons
   __syncthreads();
   len = least;
   const uint32_t pages = (len + c.page_size - 1) / c.page_size;
-  // (len is not 0 below: every sequence is one of the table)
+  // A wave to four sequences, 256 entries of each at a time, all on their way at
+  // once, up to the first that differs from the group's first sequence's. (len is
+  // not 0 below: every sequence is one of the table.)
   const int32_t *row0 = c.d_table + (uint64_t)(uint32_t)seqs[from] * c.max_pages;
-  for (uint32_t p0 = 0; p0 < pages; p0 += kPlanThreads) {
-    const uint32_t p = p0 + tid;
-    if (p < pages) {
-      const int32_t e = row0[p];
-      bool alike = e >= 0;
-#pragma unroll 8
-      for (uint32_t b = from + 1; b < to; ++b) alike &= c.d_table[(uint64_t)(uint32_t)seqs[b] * c.max_pages + p] == e;
-      if (!alike) atomicMin(&differs, p);
+  const uint32_t lane = tid & 63;
+  for (uint32_t b = from + (tid >> 6) * 4; b < to; b += kPlanThreads / 64 * 4) {
+    const int32_t *row[4];
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) row[i] = c.d_table + (uint64_t)(uint32_t)seqs[min(b + i, to - 1)] * c.max_pages;
+    const uint32_t end = min(pages, differs);   // (others may lower it meanwhile)
+    for (uint32_t p0 = 0; p0 < end; p0 += 256) {
+      bool odd[4] = {false, false, false, false};
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e) {
+        const uint32_t p = min(p0 + 64 * e + lane, pages - 1);
+        const int32_t want = row0[p];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const int32_t own = row[i][p];
+          odd[e] |= own < 0 || own != want;
+        }
+      }
+      uint32_t at = ~0u;
+#pragma unroll
+      for (int e = 3; e >= 0; --e) {
+        const uint64_t hit = __ballot(odd[e]);
+        if (hit) at = p0 + 64 * e + __builtin_ctzll(hit);
+      }
+      if (at != ~0u) {
+        if (lane == 0) atomicMin(&differs, min(at, pages));
+        break;
+      }
     }
-    __syncthreads();
-    if (differs != ~0u) break;
-    __syncthreads();
   }
+  __syncthreads();
   if (tid == 0) shared[g] = (int32_t)min((uint64_t)min(differs, pages) * c.page_size, (uint64_t)len);
 }
 
 }  // namespace
 
-// Tiles of 64 rows (32 for heads above 128 values) where a group has more than
-// 16 on average, of 16 below; the same for a sequence's own rows.
+// Tiles of 128 rows where groups have more than 64 on average (heads up to 128
+// values), of 64 where they have more than 16, of 16 below; a sequence's own rows
+// by 32 where there are more than 16 (heads above 128: 16).
 PrefixAttnPlan plan_prefix_attention(const enc_tree_attention_args &a, uint32_t groups) {
   PrefixAttnPlan p;
-  const uint32_t per = a.nodes * (a.q_heads / a.kv_heads), large = a.head_dim <= 128 ? 64 : 32;
-  const uint64_t rows = (uint64_t)a.batch * per;
-  p.tile = per > 16 || rows > 16ull * std::max(groups, 1u) ? large : 16;
-  p.own_tile = per > 16 ? large : 16;
+  const uint32_t per = a.nodes * (a.q_heads / a.kv_heads);
+  const bool large = a.head_dim > 128;
+  const uint64_t rows = (uint64_t)a.batch * per, mean = rows / std::max(groups, 1u);
+  p.tile = mean > 64 && !large ? 128 : mean > 16 ? 64 : 16;
+  p.own_tile = per > 16 && !large ? 32 : 16;
+  if (p.tile == 16) p.own_tile = 16;   // one kernel for both
   p.own_tiles = (per + p.own_tile - 1) / p.own_tile;
-  p.weight = 1;
-  p.slots = std::max(512 / a.kv_heads, 1u);
+  // resident workgroups: one of eight waves to a compute unit, or two or three of four
+  p.slots = std::max((p.tile == 16 ? 512 : 256) / a.kv_heads, 1u);
+  p.own_slots = std::max(768 / a.kv_heads, 1u);
   p.least = kWays;
   // pieces of `slots` equal shares of the work, and one more, a short one, for
   // every tile
   const uint64_t tiles = std::min<uint64_t>(rows / p.tile + groups, rows);
   p.most_shared = (uint32_t)(p.slots + tiles);
-  p.most_own = (uint32_t)(p.slots + (uint64_t)a.batch * p.own_tiles);
-  p.items = p.most_shared + (uint32_t)((uint64_t)a.batch * p.own_tiles);
+  p.most_own = (uint32_t)(p.own_slots + (uint64_t)a.batch * p.own_tiles);
+  p.items = p.most_shared + p.most_own;
   const uint64_t n = (uint64_t)p.most_shared * a.kv_heads * p.tile + (uint64_t)p.most_own * a.kv_heads * p.own_tile;
   p.part_bytes = align_up(4 * n * a.head_dim, 256);
   p.ml_bytes = align_up(8 * n, 256);

@@ -271,7 +271,7 @@ enc_status enc_prefix_attention(const enc_prefix_attention_args *a, void *d_ws, 
   k.own_tiles = p.own_tiles;
   k.slots = p.slots;
   k.least = p.least;
-  k.weight = p.weight;
+  k.own_slots = p.own_slots;
   k.mask_words = (t.nodes + 63) / 64 * 2;
   k.own_rows = (uint64_t)p.most_shared * t.kv_heads * p.tile;
   uint8_t *ws = static_cast<uint8_t *>(d_ws);

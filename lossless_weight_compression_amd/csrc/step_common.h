@@ -114,6 +114,8 @@ struct PrefixItem {
   uint32_t b, row0, rows;    // first batch entry, first row of its rows, and how many
   uint32_t first, ctx, tree; // first cached token, how many, and nodes behind them
   uint32_t lo, hi;           // strips of 32 keys
+  uint32_t turn;             // heads are taken from this one on
+  uint32_t seq;              // row of the table
 };
 struct PrefixAttnArgs {
   enc_tree_attention_args a;
@@ -121,7 +123,7 @@ struct PrefixAttnArgs {
   FastDiv page, group, nodes;   // page_size; q_heads / kv_heads; nodes
   uint32_t groups;
   uint32_t tile, own_tile, own_tiles;   // rows of a tile; tiles of a sequence's rows
-  uint32_t slots, least, weight;        // pieces aimed at; strips in the smallest; work of a shared strip
+  uint32_t slots, own_slots, least;     // pieces aimed at; strips in the smallest
   uint32_t mask_words;
   float unit, slack;         // powers of two to a unit of a maximum; how far a strip may exceed it
   uint64_t own_rows;         // of the pieces of own tokens, the first
@@ -134,7 +136,7 @@ struct PrefixAttnArgs {
   uint32_t *counts;          // pieces of shared tokens; of all
 };
 struct PrefixAttnPlan {
-  uint32_t tile, own_tile, own_tiles, slots, least, weight, most_shared, most_own, items;
+  uint32_t tile, own_tile, own_tiles, slots, own_slots, least, most_shared, most_own, items;
   uint64_t part_bytes, ml_bytes, item_bytes, batch_bytes, group_bytes;
   uint64_t total() const { return part_bytes + ml_bytes + item_bytes + 4 * batch_bytes + 4 * group_bytes + 256; }
 };
