@@ -73,6 +73,67 @@ __device__ __forceinline__ u64 excess_of(double f) {
   return (u64)__double_as_longlong(fma(s * z, 4294967296.0, 4503599627370496.0)) & ((1ull << 52) - 1);
 }
 
+// e^(-i / 16), a bin's lower edge relative to the first bin's: whole powers of e
+// times sixteenths (rounded to fp64 each).
+__device__ const double kWholes[48] = {
+    1.0, 0.36787944117144233, 0.1353352832366127, 0.049787068367863944,
+    0.01831563888873418, 0.006737946999085467, 0.0024787521766663585, 0.0009118819655545162,
+    0.00033546262790251185, 0.00012340980408667956, 4.5399929762484854e-05, 1.670170079024566e-05,
+    6.14421235332821e-06, 2.2603294069810542e-06, 8.315287191035679e-07, 3.059023205018258e-07,
+    1.1253517471925912e-07, 4.139937718785167e-08, 1.522997974471263e-08, 5.602796437537268e-09,
+    2.061153622438558e-09, 7.582560427911907e-10, 2.7894680928689246e-10, 1.026187963170189e-10,
+    3.775134544279098e-11, 1.3887943864964021e-11, 5.109089028063325e-12, 1.8795288165390832e-12,
+    6.914400106940203e-13, 2.543665647376923e-13, 9.357622968840175e-14, 3.442477108469977e-14,
+    1.2664165549094176e-14, 4.658886145103398e-15, 1.713908431542013e-15, 6.305116760146989e-16,
+    2.3195228302435696e-16, 8.533047625744066e-17, 3.1391327920480296e-17, 1.1548224173015786e-17,
+    4.248354255291589e-18, 1.5628821893349888e-18, 5.74952226429356e-19, 2.1151310375910805e-19,
+    7.781132241133797e-20, 2.8625185805493937e-20, 1.0530617357553812e-20, 3.873997628687187e-21};
+__device__ const double kParts[16] = {
+    1.0, 0.9394130628134758, 0.8824969025845955, 0.8290291181804004,
+    0.7788007830714049, 0.7316156289466418, 0.6872892787909722, 0.645648526427892,
+    0.6065306597126334, 0.569782824730923, 0.5352614285189903, 0.5028315779709409,
+    0.4723665527410147, 0.44374731008107987, 0.4168620196785084, 0.391605626676799};
+static_assert(kBins == 48 * 16, "the tables cover the bins");
+__device__ __forceinline__ void fill_edges(double *edges) {   // in LDS
+  for (uint32_t i = threadIdx.x; i < kBins; i += blockDim.x) edges[i] = kWholes[i >> 4] * kParts[i & 15];
+}
+
+// A token's bin below `edge` (kBins or more: none) and excess. Where the first
+// bin's place is below 2^20 in size, the place rounded to 2^-30 is read off the
+// sum's bits: bin and rest are a shift and a mask. Logits far below (NaN and
+// -infinity among them) are raised to one that is in no bin.
+struct Places {
+  double r16, edge;
+  float lowest;        // raises what lies below 2^-20 of r16
+  uint32_t first;      // the first bin's place plus 3 2^21, as a whole number
+  bool near_;
+  __device__ __forceinline__ Places(double r, double e) : r16(r), edge(e) {
+    near_ = fabs(e) < 1048576.0 && r > 1e-30;
+    lowest = near_ ? (float)fmax(-2000000.0 / r, -3e38) : 0.f;
+    first = (uint32_t)(int32_t)(near_ ? e : 0.0) + 6291456u;
+  }
+  template <bool NEAR> __device__ __forceinline__ uint32_t bin_of(float l, uint32_t &excess) const {
+    if constexpr (NEAR) {
+      const double at = fma((double)fmaxf(l, lowest), r16, 6291456.0);
+      const u64 bits = (u64)__double_as_longlong(at);
+      // 2^22 <= at < 2^23: 30 bits of fraction, then the whole number, whose
+      // leading one the mask leaves
+      const uint32_t whole = ((uint32_t)(bits >> 30) & 0x3FFFFFu) | 0x400000u;
+      const double f = (double)((uint32_t)bits & 0x3FFFFFFFu) * (1.0 / 1073741824.0);
+      excess = (uint32_t)excess_of(f);
+      return first - whole;
+    } else {
+      const double t = place_of(l, r16), at = floor(t), below = edge - at;
+      if (!counts(l) || !(below < (double)kBins)) return kBins;
+      excess = (uint32_t)excess_of(t - at);
+      return (uint32_t)below;
+    }
+  }
+  __device__ __forceinline__ uint32_t bin_of(float l, uint32_t &excess) const {
+    return near_ ? bin_of<true>(l, excess) : bin_of<false>(l, excess);
+  }
+};
+
 struct Setting {
   double r16;        // 16 / temperature
   double top_p, min_p;
@@ -206,16 +267,24 @@ __global__ __launch_bounds__(NT) void k_scan(SampleKernelArgs k) {
   }
   if (top == 0 || set.first) return;   // nothing in it, or nothing but the first is asked for
   const double edge = floor(place_of(logit_of(top), set.r16));
+  const Places places(set.r16, edge);
+  const auto fill = [&](auto near_) __attribute__((always_inline)) {
 #pragma unroll
-  for (uint32_t j = 0; j < NV; ++j) {
-    float x[E];
-    values_of<T>(piece[j], x);
+    for (uint32_t j = 0; j < NV; ++j) {
+      float x[E];
+      values_of<T>(piece[j], x);
 #pragma unroll
-    for (uint32_t e = 0; e < E; ++e) {
-      const double t = place_of(x[e], set.r16), at = floor(t), below = edge - at;
-      if (counts(x[e]) && below < (double)kBins) atomicAdd(&bins[(uint32_t)below], (1ull << 49) + excess_of(t - at));
+      for (uint32_t e = 0; e < E; ++e) {
+        uint32_t excess;
+        const uint32_t bin = places.bin_of<decltype(near_)::value>(x[e], excess);
+        if (bin < kBins) atomicAdd(&bins[bin], (1ull << 49) + excess);
+      }
     }
-  }
+  };
+  if (places.near_)
+    fill(std::true_type{});
+  else
+    fill(std::false_type{});
   __syncthreads();
   u64 *dst = k.bins + ((uint64_t)r * k.segments + seg) * kBins;
   uint32_t used = 0;
@@ -240,13 +309,22 @@ __global__ __launch_bounds__(kWide) void k_plan(SampleKernelArgs k) {
   __shared__ double sums[kBins], side[kWide / 64];
   __shared__ uint32_t numbers[kBins], side_n[kWide / 64];
   __shared__ uint32_t k_bin, p_low, p_high;
+  __shared__ uint32_t starts[kSampleSegments], used[kSampleSegments], gathered[kSampleSegments];
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = blockIdx.x, row = k.row0 + r;
   SampleSegment *segs = k.segs + (uint64_t)r * k.segments;
   const Setting set = setting_of(a, row);
   SampleRow &out = k.rows[r];
+  const uint32_t segments = k.segments;
 
+  // (a segment to a thread: there are at most as many)
   u64 top = 0;
-  for (uint32_t s = tid; s < k.segments; s += kWide) top = max(top, segs[s].top);
+  double my_edge = 0.0;
+  uint32_t my_used = 0;
+  if (tid < segments) {
+    top = segs[tid].top;
+    my_edge = segs[tid].edge;
+    my_used = segs[tid].bins;
+  }
   top = wave_max(top);
   if (lane == 0) tops[wave] = top;
   if (tid == 0) k_bin = p_low = p_high = kBins - 1;
@@ -260,25 +338,34 @@ __global__ __launch_bounds__(kWide) void k_plan(SampleKernelArgs k) {
     out.n = 0;
     out.cut_bin = 0;
     out.tau = top;
-    out.z = 0.0;
+    // one token alone: its weight, relative to its bin's lower edge
+    out.z = top == 0 ? 0.0 : 1.0 + (double)excess_of(t_max - edge) * kUnit;
     out.state = top == 0 ? kSampleEmpty : kSampleFirst;
   }
   if (top == 0 || set.first) return;
+  if (tid < segments) {
+    const double by = edge - my_edge;   // (an empty segment's edge is nothing)
+    const bool any = my_used && by < (double)kBins;
+    starts[tid] = any ? (uint32_t)by : 0u;
+    used[tid] = any ? my_used : 0u;
+  }
+  __syncthreads();
 
   u64 sum = 0;
   uint32_t number = 0;
-  if (tid < kBins)
-    for (uint32_t s = 0; s < k.segments; ++s) {
-      const double by = edge - segs[s].edge;
-      if (!(segs[s].bins && by < (double)kBins)) continue;
-      const uint32_t at = tid - (uint32_t)by;   // wraps where the segment has no such bin
-      if (at < segs[s].bins) {
-        const u64 v = k.bins[((uint64_t)r * k.segments + s) * kBins + at];
-        number += (uint32_t)(v >> 49);
-        sum += v & kSumMask;
-      }
+  if (tid < kBins) {
+    const u64 *bins = k.bins + (uint64_t)r * segments * kBins;
+#pragma unroll 8
+    for (uint32_t s = 0; s < segments; ++s) {
+      const uint32_t at = tid - starts[s];   // wraps where the segment has no such bin
+      const bool has = at < used[s];
+      const u64 v = bins[(uint64_t)s * kBins + (has ? at : 0)];
+      number += has ? (uint32_t)(v >> 49) : 0;
+      sum += has ? v & kSumMask : 0;
     }
-  const double mass = tid < kBins ? ((double)number + (double)sum * kUnit) * exp((double)tid * -0.0625) : 0.0;
+  }
+  const double mass =
+      tid < kBins ? ((double)number + (double)sum * kUnit) * (kWholes[tid >> 4] * kParts[tid & 15]) : 0.0;
   const double upto = group_scan(mass, side);
   const uint32_t n_upto = group_scan(number, side_n);
   if (tid < kBins) {
@@ -323,26 +410,26 @@ __global__ __launch_bounds__(kWide) void k_plan(SampleKernelArgs k) {
     __syncthreads();
     total = side_n[0];
     if (total <= kList) {
-      uint32_t base = 0;
-      for (uint32_t s0 = 0; s0 < k.segments; s0 += kWide) {
-        // a wave counts a segment's wanted bins; then a scan over the segments
-        __syncthreads();
-        for (uint32_t s = s0 + wave; s < min(k.segments, s0 + kWide); s += kWide / 64) {
-          const double by = edge - segs[s].edge;
-          uint32_t c = 0;
-          if (segs[s].bins && by < (double)kBins)
-            for (uint32_t i = lane; i < segs[s].bins; i += 64)
-              if (i + (uint32_t)by < kBins && wanted(i + (uint32_t)by))
-                c += (uint32_t)(k.bins[((uint64_t)r * k.segments + s) * kBins + i] >> 49);
-          c = wave_incl_scan(c);
-          if (lane == 63) segs[s].n = c;
+      // a wave counts a segment's wanted bins; then a scan over the segments
+      for (uint32_t s = wave; s < segments; s += kWide / 64) {
+        const u64 *bins = k.bins + ((uint64_t)r * segments + s) * kBins;
+        uint32_t c = 0;
+#pragma unroll
+        for (uint32_t i0 = 0; i0 < kBins; i0 += 64) {
+          const uint32_t i = i0 + lane;
+          const bool has = i < used[s] && i + starts[s] < kBins && wanted(i + starts[s]);
+          const u64 v = bins[has ? i : 0];
+          c += has ? (uint32_t)(v >> 49) : 0;
         }
-        __syncthreads();
-        const uint32_t s = s0 + tid;
-        const uint32_t c = s < k.segments ? segs[s].n : 0;
-        const uint32_t incl = group_scan(c, side_n);
-        if (s < k.segments) segs[s].first = base + incl - c;
-        for (uint32_t w = 0; w < kWide / 64; ++w) base += side_n[w];
+        c = wave_incl_scan(c);
+        if (lane == 63) gathered[s] = c;
+      }
+      __syncthreads();
+      const uint32_t c = tid < segments ? gathered[tid] : 0;
+      const uint32_t incl = group_scan(c, side_n);
+      if (tid < segments) {
+        segs[tid].n = c;
+        segs[tid].first = incl - c;
       }
     }
   }
@@ -382,24 +469,29 @@ __global__ __launch_bounds__(NT) void k_collect(SampleKernelArgs k) {
   if (tid == 0) filled = 0;
   __syncthreads();
   const uint32_t bk = w.bk, lo = w.lo, hi = w.hi, bm = w.bm;
-  const double r16 = w.r16, edge = w.edge;
+  const Places places(w.r16, w.edge);
   const uint32_t n = me.n;
   SampleToken *dst = k.list + (uint64_t)r * kList + me.first;
+  const auto gather = [&](auto near_) __attribute__((always_inline)) {
 #pragma unroll
-  for (uint32_t j = 0; j < NV; ++j) {
-    float x[E];
-    values_of<T>(piece[j], x);
+    for (uint32_t j = 0; j < NV; ++j) {
+      float x[E];
+      values_of<T>(piece[j], x);
 #pragma unroll
-    for (uint32_t e = 0; e < E; ++e) {
-      const double t = place_of(x[e], r16), at = floor(t), below = edge - at;
-      if (!counts(x[e]) || !(below < (double)kBins)) continue;
-      const uint32_t i = (uint32_t)below;
-      if (i == bk || i == bm || (lo != kNoBin && i >= lo && i <= hi)) {
-        const uint32_t slot = atomicAdd(&filled, 1u);   // any order: what is selected does not depend on it
-        if (slot < n) dst[slot] = SampleToken{key_of(x[e], seg * S + (j * NT + tid) * E + e - head), (u64)i << 40 | excess_of(t - at)};
+      for (uint32_t e = 0; e < E; ++e) {
+        uint32_t excess;
+        const uint32_t i = places.bin_of<decltype(near_)::value>(x[e], excess);
+        if (i < kBins && (i == bk || i == bm || (i >= lo && i <= hi))) {   // (without lo nothing is as large)
+          const uint32_t slot = atomicAdd(&filled, 1u);   // any order: what is selected does not depend on it
+          if (slot < n) dst[slot] = SampleToken{key_of(x[e], seg * S + (j * NT + tid) * E + e - head), (u64)i << 40 | excess};
+        }
       }
     }
-  }
+  };
+  if (places.near_)
+    gather(std::true_type{});
+  else
+    gather(std::false_type{});
 }
 
 // ---- per row: the cuts among the gathered tokens, then the draw
@@ -425,10 +517,13 @@ template <typename T> struct Tokens {
       for (uint32_t i = threadIdx.x; i < n; i += kWide)
         f(list[i].key, (uint32_t)(list[i].at >> 40), list[i].at & ((1ull << 40) - 1));
     } else {
+      const Places places(r16, edge);
+#pragma unroll 4
       for (uint32_t i = threadIdx.x; i < vocab; i += kWide) {
         const float x = value_at(row, i);
-        const double t = place_of(x, r16), at = floor(t), below = edge - at;
-        if (counts(x) && below < (double)kBins) f(key_of(x, i), (uint32_t)below, excess_of(t - at));
+        uint32_t excess;
+        const uint32_t bin = places.bin_of(x, excess);
+        if (bin < kBins) f(key_of(x, i), bin, (u64)excess);
       }
     }
   }
@@ -547,12 +642,13 @@ __device__ u64 select(const Tokens<T> &all, uint32_t bin, uint32_t rank, double 
   return tau;
 }
 
-template <typename T>
+// ROUNDS: 64 tokens at a time, of a sixteenth of a segment.
+template <typename T, uint32_t ROUNDS>
 __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
   const enc_sample_args &a = k.a;
   __shared__ SampleToken list[kList];
   __shared__ Select pick;
-  __shared__ double sums[kBins], side[kWide / 64], masses[kWide];
+  __shared__ double sums[kBins], edges[kBins], side[kWide / 64], masses[kWide];
   __shared__ u64 parts[kSampleSegments];
   __shared__ u64 part, lowest;
   __shared__ uint32_t chosen;
@@ -563,9 +659,6 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
   if (state == kSampleEmpty || state == kSampleFirst) {
     if (tid == 0) {
       if (a.d_token) a.d_token[row] = state == kSampleEmpty ? -1 : (int32_t)index_of(top);
-      // one token alone: its weight, relative to its bin's lower edge
-      const double t = place_of(logit_of(top), w.r16);
-      w.z = exp((t - w.edge) * 0.0625);
     }
     return;
   }
@@ -575,6 +668,7 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
   uint32_t cut = w.cut_bin;
   u64 tau = 0;
   double z = w.z;
+  fill_edges(edges);
   if (state != kSampleWhole) {
     Tokens<T> all;
     all.list = list;
@@ -604,7 +698,7 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
       return part;
     };
     const auto upto = [&](uint32_t bin) { return bin ? sums[bin - 1] : 0.0; };
-    const auto unit_of = [&](uint32_t bin) { return exp((double)bin * -0.0625); };
+    const auto unit_of = [&](uint32_t bin) { return edges[bin]; };
     cut = kb;
     double kept = sums[kb];
     if (bk != kNoBin) {
@@ -642,22 +736,26 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
   if (!a.d_token) return;
 
   // the segments' kept weights: bins above the cut, and of its bin what is above tau
+  __syncthreads();
   double mine = 0.0;
   for (uint32_t s = wave; s < k.segments; s += kWide / 64) {
     const SampleSegment &seg = k.segs[(uint64_t)r * k.segments + s];
+    const u64 *bins = k.bins + ((uint64_t)r * k.segments + s) * kBins;
+    const uint32_t n = seg.bins;
     const double by = edge - seg.edge;
     double m = 0.0;
-    if (seg.bins && by < (double)kBins) {
+    if (n && by < (double)kBins) {
       const uint32_t d = (uint32_t)by;
-      for (uint32_t i = lane; i < seg.bins; i += 64) {
-        const uint32_t b = d + i;
-        if (b > cut || (b == cut && tau)) continue;
-        const u64 v = k.bins[((uint64_t)r * k.segments + s) * kBins + i];
-        m += ((double)(v >> 49) + (double)(v & kSumMask) * kUnit) * exp((double)b * -0.0625);
+#pragma unroll
+      for (uint32_t i0 = 0; i0 < kBins; i0 += 64) {
+        const uint32_t i = i0 + lane, b = d + i;
+        const bool has = i < n && (b < cut || (b == cut && !tau));
+        const u64 v = bins[has ? i : 0];
+        m += has ? ((double)(v >> 49) + (double)(v & kSumMask) * kUnit) * edges[b] : 0.0;
       }
     }
     for (uint32_t o = 32; o; o >>= 1) m += __shfl_xor(m, o);
-    if (tau) m += (double)parts[s] * kUnit * exp((double)cut * -0.0625);
+    if (tau) m += (double)parts[s] * kUnit * edges[cut];
     if (lane == 0) masses[s] = m;
   }
   __syncthreads();
@@ -677,45 +775,72 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
   if (tid == seg) side[1] = incl - mine;
   __syncthreads();
   const double before = side[1];
-  // its tokens again, in their order
-  const uint32_t each = k.segment / kWide, first = seg * k.segment + tid * each;
+  // Its tokens again: a wave takes a run of them, 64 at a time, and sums their
+  // weights; the one that passes the goal lays its weights out in LDS, each lane
+  // a run of its own, for the order within.
+  const uint32_t first = seg * k.segment + wave * (64 * ROUNDS);
+  const Places places(r16, edge);
+  float x[ROUNDS];
+#pragma unroll
+  for (uint32_t j = 0; j < ROUNDS; ++j)   // all on their way at once
+    x[j] = value_at(l, min(max(first + 64 * j + lane, head), head + a.vocab - 1) - head);
+  double weight[ROUNDS];
   double own = 0.0;
-  uint32_t last = 0;   // 1 + the last kept one
-  const auto weight = [&](uint32_t v) {
-    if (v < head || v >= head + a.vocab) return 0.0;
-    const float x = value_at(l, v - head);
-    const double t = place_of(x, r16), below = edge - floor(t);
-    if (!counts(x) || !(below <= (double)cut)) return 0.0;
-    if (tau && (uint32_t)below == cut && key_of(x, v - head) < tau) return 0.0;
-    return (double)(kOne + excess_of(t - floor(t))) * kUnit * exp(below * -0.0625);   // as the bins hold it
-  };
-  for (uint32_t j = 0; j < each; ++j) {
-    const double m = weight(first + j);
-    own += m;
-    if (m > 0.0) last = first + j + 1;
+#pragma unroll
+  for (uint32_t j = 0; j < ROUNDS; ++j) {
+    const uint32_t v = first + 64 * j + lane;
+    uint32_t excess;
+    const uint32_t bin = places.bin_of(x[j], excess);
+    const bool kept = v >= head && v < head + a.vocab && (bin < cut || (bin == cut && key_of(x[j], v - head) >= tau));
+    weight[j] = kept ? (double)(kOne + excess) * kUnit * edges[bin] : 0.0;   // as the bins hold it
+    own += weight[j];
   }
-  const double run = group_scan(own, side);
+  for (uint32_t o = 32; o; o >>= 1) own += __shfl_xor(own, o);
+  if (lane == 0) masses[wave] = own;   // (what it held has been read)
   __syncthreads();
-  if (tid == 0) chosen = 0;
-  __syncthreads();
-  // the first to pass the goal; the last kept one if rounding lets none
-  uint32_t mark = last;
-  if (own > 0.0 && before + run > goal) {
-    double sum = before + run - own;
-    for (uint32_t j = 0; j < each; ++j) {
-      const double m = weight(first + j);
-      sum += m;
-      if (m > 0.0 && (sum > goal || first + j + 1 == last)) {
-        mark = 0x80000000u | (0x7FFFFFFFu - (first + j));
-        break;
+  // the first wave whose sum passes; the last with anything if none does
+  double sum = before;
+  uint32_t chosen_wave = 0;
+  bool passed = false;
+  for (uint32_t w2 = 0; w2 < kWide / 64 && !passed; ++w2) {
+    const double m = masses[w2];
+    if (m > 0.0) {
+      chosen_wave = w2;
+      passed = sum + m > goal;
+    }
+    if (!passed) sum += m;
+  }
+  if (wave != chosen_wave) return;
+  if (!passed) sum = -1.0;   // its last one, whatever the sums say
+  double *const laid = reinterpret_cast<double *>(list);   // nobody else's by now
+#pragma unroll
+  for (uint32_t j = 0; j < ROUNDS; ++j) laid[64 * j + lane] = weight[j];
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  own = 0.0;
+  uint32_t last = 0;   // 1 + this lane's last kept one
+  for (uint32_t j = 0; j < ROUNDS; ++j) {
+    const double m = laid[lane * ROUNDS + j];
+    own += m;
+    if (m > 0.0) last = j + 1;
+  }
+  const double upto_lane = sum + wave_scan(own);
+  const uint64_t hits = __ballot(passed && own > 0.0 && upto_lane > goal), any = __ballot(own > 0.0);
+  const int at = hits ? __builtin_ctzll(hits) : 63 - __builtin_clzll(any);
+  if ((int)lane == at) {
+    uint32_t i = last - 1;
+    if (hits) {
+      double upto = upto_lane - own;
+      for (uint32_t j = 0; j < ROUNDS; ++j) {
+        const double m = laid[lane * ROUNDS + j];
+        upto += m;
+        if (m > 0.0 && (upto > goal || j + 1 == last)) {
+          i = j;
+          break;
+        }
       }
     }
-  }
-  atomicMax(&chosen, mark);
-  __syncthreads();
-  if (tid == 0) {
-    const uint32_t v = chosen & 0x80000000u ? 0x7FFFFFFFu - (chosen & 0x7FFFFFFFu) : chosen - 1;
-    a.d_token[row] = (int32_t)(v - head);
+    a.d_token[row] = (int32_t)(first + lane * ROUNDS + i - head);
   }
 }
 
@@ -725,30 +850,55 @@ __global__ __launch_bounds__(NT) void k_probs(SampleKernelArgs k) {
   constexpr uint32_t E = kPiece<T>, S = NT * NV * E;
   const enc_sample_args &a = k.a;
   const uint32_t tid = threadIdx.x, r = blockIdx.x / k.segments, seg = blockIdx.x - r * k.segments;
+  __shared__ double edges[kBins];
   const SampleRow &w = k.rows[r];
   const T *l = static_cast<const T *>(a.d_logits) + (uint64_t)(k.row0 + r) * a.logits_row;
   O *out = static_cast<O *>(a.d_probs) + (uint64_t)(k.row0 + r) * a.probs_row;
   const uint32_t head = head_of(l), cut = w.cut_bin;
+  uint4 piece[NV];
+#pragma unroll
+  for (uint32_t j = 0; j < NV; ++j) piece[j] = load_piece(l, head, a.vocab, seg * S + (j * NT + tid) * E);
   const u64 tau = w.tau;
   const bool empty = w.state == kSampleEmpty;
-  const double r16 = w.r16, edge = w.edge, inv = empty ? 0.0 : 1.0 / w.z;
+  const double inv = empty ? 0.0 : 1.0 / w.z;
+  fill_edges(edges);
+  __syncthreads();
+  const Places places(w.r16, w.edge);
+  // whole pieces of the output where its rows lie as the logits' do
+  const bool whole = head_of(out) % E == head && sizeof(O) * E <= 16;
+  const auto write = [&](auto near_) __attribute__((always_inline)) {
 #pragma unroll
-  for (uint32_t j = 0; j < NV; ++j) {
-    const uint32_t at = seg * S + (j * NT + tid) * E;
-    if (at >= head + a.vocab) break;
-    float x[E], p[E];
-    values_of<T>(load_piece(l, head, a.vocab, at), x);
+    for (uint32_t j = 0; j < NV; ++j) {
+      const uint32_t at = seg * S + (j * NT + tid) * E;
+      float x[E];
+      O p[E];
+      values_of<T>(piece[j], x);
 #pragma unroll
-    for (uint32_t e = 0; e < E; ++e) {
-      const double t = place_of(x[e], r16), below = edge - floor(t);
-      bool kept = !empty && counts(x[e]) && below <= (double)cut;
-      if (kept && tau && (uint32_t)below == cut) kept = key_of(x[e], at + e - head) >= tau;
-      p[e] = kept ? (float)(exp((t - edge) * 0.0625) * inv) : 0.f;
+      for (uint32_t e = 0; e < E; ++e) {
+        uint32_t excess;
+        const uint32_t bin = places.bin_of<decltype(near_)::value>(x[e], excess);
+        float v = 0.f;
+        if (!empty && (bin < cut || (bin == cut && key_of(x[e], at + e - head) >= tau)))
+          v = (float)((1.0 + (double)excess * kUnit) * edges[bin] * inv);
+        p[e] = (O)v;
+      }
+      typedef O Run __attribute__((ext_vector_type(E)));
+      if (whole && at >= head && at + E <= head + a.vocab) {
+        Run run;
+#pragma unroll
+        for (uint32_t e = 0; e < E; ++e) run[e] = p[e];
+        *reinterpret_cast<Run *>(out + ((int64_t)at - head)) = run;
+      } else {
+#pragma unroll
+        for (uint32_t e = 0; e < E; ++e)
+          if (at + e >= head && at + e < head + a.vocab) out[at + e - head] = p[e];
+      }
     }
-#pragma unroll
-    for (uint32_t e = 0; e < E; ++e)
-      if (at + e >= head && at + e < head + a.vocab) out[at + e - head] = (O)p[e];
-  }
+  };
+  if (places.near_)
+    write(std::true_type{});
+  else
+    write(std::false_type{});
 }
 
 template <typename T, typename O>
@@ -777,7 +927,10 @@ void launch_rows(const SampleKernelArgs &k, uint32_t rows, hipStream_t s) {
     else
       hipLaunchKernelGGL((k_collect<T, 512, 32 / E>), grid, dim3(512), 0, s, k);
   }
-  hipLaunchKernelGGL((k_resolve<T>), dim3(rows), dim3(kWide), 0, s, k);
+  if (k.segment == 4096)
+    hipLaunchKernelGGL((k_resolve<T, 4>), dim3(rows), dim3(kWide), 0, s, k);
+  else
+    hipLaunchKernelGGL((k_resolve<T, 16>), dim3(rows), dim3(kWide), 0, s, k);
   if (k.a.d_probs) {
     if (k.a.probs_dtype == 1)
       launch_probs<T, __bf16>(k, rows, s);
