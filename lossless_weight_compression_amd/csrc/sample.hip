@@ -230,7 +230,9 @@ template <typename T, uint32_t NT, uint32_t NV>
 __global__ __launch_bounds__(NT) void k_scan(SampleKernelArgs k) {
   constexpr uint32_t E = kPiece<T>, S = NT * NV * E;
   const enc_sample_args &a = k.a;
-  __shared__ u64 bins[kBins];
+  // Lanes count into four copies: two that meet in a word wait for each other.
+  constexpr uint32_t kCopies = 4;
+  __shared__ u64 bins[kCopies][kBins];
   __shared__ u64 tops[NT / 64];
   __shared__ uint32_t last;
   const uint32_t tid = threadIdx.x, r = blockIdx.x / k.segments, seg = blockIdx.x - r * k.segments;
@@ -241,7 +243,7 @@ __global__ __launch_bounds__(NT) void k_scan(SampleKernelArgs k) {
 #pragma unroll
   for (uint32_t j = 0; j < NV; ++j) piece[j] = load_piece(l, head, a.vocab, seg * S + (j * NT + tid) * E);
   const Setting set = setting_of(a, row);
-  for (uint32_t i = tid; i < kBins; i += NT) bins[i] = 0;
+  for (uint32_t i = tid; i < kCopies * kBins; i += NT) bins[0][i] = 0;
   if (tid == 0) last = 0;
 
   u64 top = 0;
@@ -277,7 +279,7 @@ __global__ __launch_bounds__(NT) void k_scan(SampleKernelArgs k) {
       for (uint32_t e = 0; e < E; ++e) {
         uint32_t excess;
         const uint32_t bin = places.bin_of<decltype(near_)::value>(x[e], excess);
-        if (bin < kBins) atomicAdd(&bins[bin], (1ull << 49) + excess);
+        if (bin < kBins) atomicAdd(&bins[tid % kCopies][bin], (1ull << 49) + excess);
       }
     }
   };
@@ -288,14 +290,21 @@ __global__ __launch_bounds__(NT) void k_scan(SampleKernelArgs k) {
   __syncthreads();
   u64 *dst = k.bins + ((uint64_t)r * k.segments + seg) * kBins;
   uint32_t used = 0;
-  for (uint32_t i = tid; i < kBins; i += NT) {
-    const u64 v = bins[i];
-    if (v) used = i + 1;
+  u64 mine[(kBins + NT - 1) / NT];
+#pragma unroll
+  for (uint32_t j = 0; j < (kBins + NT - 1) / NT; ++j) {
+    const uint32_t i = tid + j * NT;
+    mine[j] = 0;
+    if (i < kBins)
+      for (uint32_t c = 0; c < kCopies; ++c) mine[j] += bins[c][i];
+    if (mine[j]) used = i + 1;
   }
   atomicMax(&last, used);
   __syncthreads();
   used = last;
-  for (uint32_t i = tid; i < used; i += NT) dst[i] = bins[i];
+#pragma unroll
+  for (uint32_t j = 0; j < (kBins + NT - 1) / NT; ++j)
+    if (tid + j * NT < used) dst[tid + j * NT] = mine[j];
   if (tid == 0) {
     out->edge = edge;
     out->bins = used;
@@ -443,6 +452,8 @@ __global__ __launch_bounds__(kWide) void k_plan(SampleKernelArgs k) {
     out.top_p = set.top_p;
     out.t_min = t_min;
     out.n = total;
+    out.bk_n = k_part ? numbers[kb] - (kb ? numbers[kb - 1] : 0) : 0;
+    out.lo_n = lo != kNoBin && lo == hi ? numbers[lo] - (lo ? numbers[lo - 1] : 0) : 0;
     out.cut_bin = hi;   // where no list is needed: a whole bin ends what is kept
     out.tau = 0;
     out.z = sums[hi];
@@ -496,13 +507,13 @@ __global__ __launch_bounds__(NT) void k_collect(SampleKernelArgs k) {
 
 // ---- per row: the cuts among the gathered tokens, then the draw
 
+constexpr uint32_t kFew = 64;   // few enough for one wave, a token to a lane
 struct Select {
-  u64 keys[256];        // few enough to compare each with each
-  u64 weights[256];
+  u64 keys[kFew], weights[kFew];
   u64 sum[256];         // of a digit's values
   uint32_t number[256];
-  u64 any, every, tau, skipped_sum;
-  uint32_t filled, digit, skipped;
+  u64 any, every, tau, upto, skipped_sum;
+  uint32_t filled, digit, skipped, left;
 };
 
 // Tokens of a row: those gathered, or the row itself. f(key, bin, excess).
@@ -531,11 +542,12 @@ template <typename T> struct Tokens {
 
 // The key of the token of a bin, in the order, at which the count reaches `rank`
 // (from 1), or, with rank 0, the weights' sum reaches `need` (in bin units); the
-// bin's last token if neither does. First a digit of the excess, which spreads a
-// bin's tokens, then digits of the key from its highest bit that differs, until
-// 256 tokens are left, which are compared each with each.
+// bin's last token if neither does. `left`: how many the bin has. First a digit
+// of the excess, which spreads a bin's tokens, then, where many are equal, digits
+// of the key from its highest bit that differs, until a wave has a lane for each.
+// `upto`: the bin's weights from its first token to that one, in units of 2^-32.
 template <typename T>
-__device__ u64 select(const Tokens<T> &all, uint32_t bin, uint32_t rank, double need, Select &s) {
+__device__ u64 select(const Tokens<T> &all, uint32_t bin, uint32_t left, uint32_t rank, double need, Select &s, u64 &upto) {
   const uint32_t tid = threadIdx.x, lane = tid & 63;
   u64 low = 0, high = ~0ull;   // keys still in question
   uint32_t qd = kNoBin;        // their excess' first digit
@@ -544,32 +556,30 @@ __device__ u64 select(const Tokens<T> &all, uint32_t bin, uint32_t rank, double 
   const auto live = [&](u64 key, uint32_t i, u64 q) {
     return i == bin && key >= low && key <= high && (qd == kNoBin || (uint32_t)(q >> 21) == qd);
   };
-  for (uint32_t round = 0;; ++round) {
-    // how many, and in which bits they differ
-    __syncthreads();
-    if (tid == 0) s.filled = 0, s.any = 0, s.every = ~0ull;
-    __syncthreads();
-    u64 any = 0, every = ~0ull;
-    uint32_t mine = 0;
-    all.each([&](u64 key, uint32_t i, u64 q) {
-      if (!live(key, i, q)) return;
-      any |= key;
-      every &= key;
-      ++mine;
-    });
-    if (mine) {
-      atomicAdd(&s.filled, mine);
-      atomicOr(&s.any, any);
-      atomicAnd(&s.every, every);
-    }
-    __syncthreads();
-    if (s.filled <= 256) break;
-    const u64 common = s.every, differ = s.any & ~common;
-    const uint32_t top_bit = 63 - __clzll((long long)differ);   // keys are distinct: some bit differs
-    const uint32_t shift = top_bit >= 7 ? top_bit - 7 : 0;
+  for (uint32_t round = 0; left > kFew; ++round) {
     const bool by_excess = round == 0;
-    if (tid < 256) s.sum[tid] = 0, s.number[tid] = 0;
+    uint32_t shift = 0;
+    u64 common = 0;
     __syncthreads();
+    if (tid < 256) s.sum[tid] = 0, s.number[tid] = 0;
+    if (tid == 0) s.any = 0, s.every = ~0ull;
+    __syncthreads();
+    if (!by_excess) {   // where they differ
+      u64 any = 0, every = ~0ull;
+      all.each([&](u64 key, uint32_t i, u64 q) {
+        if (!live(key, i, q)) return;
+        any |= key;
+        every &= key;
+      });
+      if (any) {
+        atomicOr(&s.any, any);
+        atomicAnd(&s.every, every);
+      }
+      __syncthreads();
+      common = s.every;
+      const uint32_t top_bit = 63 - __clzll((long long)(s.any & ~common));   // keys are distinct: some bit differs
+      shift = top_bit >= 7 ? top_bit - 7 : 0;
+    }
     all.each([&](u64 key, uint32_t i, u64 q) {
       if (!live(key, i, q)) return;
       const uint32_t d = by_excess ? (uint32_t)(q >> 21) : (uint32_t)(key >> shift) & 255u;
@@ -595,7 +605,7 @@ __device__ u64 select(const Tokens<T> &all, uint32_t bin, uint32_t rank, double 
       const u64 hits = __ballot(hit != kNoBin), lasts = __ballot(last != kNoBin);
       // the first lane that reaches it; if none does (rounding), the last token
       const int from = hits ? __builtin_ctzll(hits) : 63 - __builtin_clzll(lasts);
-      uint32_t d = __builtin_amdgcn_readlane(hits ? hit : last, from);
+      const uint32_t d = __builtin_amdgcn_readlane(hits ? hit : last, from);
       if (!hits) {   // everything before the last digit is passed
         n_at = skipped, m_at = skipped_sum;
         for (uint32_t e = 255; e > d; --e) n_at += s.number[e], m_at += s.sum[e];
@@ -604,11 +614,12 @@ __device__ u64 select(const Tokens<T> &all, uint32_t bin, uint32_t rank, double 
         m_at = (u64)(uint32_t)__builtin_amdgcn_readlane((uint32_t)m_at, from) |
                (u64)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(m_at >> 32), from) << 32;
       }
-      if (lane == 0) s.digit = d, s.skipped = n_at, s.skipped_sum = m_at;
+      if (lane == 0) s.digit = d, s.skipped = n_at, s.skipped_sum = m_at, s.left = s.number[d];
     }
     __syncthreads();
     skipped = s.skipped;
     skipped_sum = s.skipped_sum;
+    left = s.left;
     if (by_excess) {
       qd = s.digit;
     } else {
@@ -618,28 +629,36 @@ __device__ u64 select(const Tokens<T> &all, uint32_t bin, uint32_t rank, double 
     }
   }
   __syncthreads();
-  if (tid == 0) s.filled = 0, s.tau = ~0ull;
+  if (tid == 0) s.filled = 0;
   __syncthreads();
   all.each([&](u64 key, uint32_t i, u64 q) {
     if (!live(key, i, q)) return;
     const uint32_t slot = atomicAdd(&s.filled, 1u);
-    if (slot < 256) s.keys[slot] = key, s.weights[slot] = kOne + q;
+    if (slot < kFew) s.keys[slot] = key, s.weights[slot] = kOne + q;
   });
   __syncthreads();
-  const uint32_t n = min(s.filled, 256u);
-  if (tid < n) {
-    const u64 key = s.keys[tid];
+  if (tid < 64) {
+    const uint32_t n = min(s.filled, kFew);
+    const u64 key = lane < n ? s.keys[lane] : 0, weight = lane < n ? s.weights[lane] : 0;
     uint32_t number = skipped;
     u64 sum = skipped_sum;
-    for (uint32_t j = 0; j < n; ++j)
-      if (s.keys[j] > key) ++number, sum += s.weights[j];
+    for (uint32_t j = 0; j < n; ++j) {
+      const u64 other = s.keys[j], w = s.weights[j];
+      if (other > key) ++number, sum += w;
+    }
     // not yet reached before this one: the least such key is the one
-    if (rank ? number < rank : (double)sum * kUnit < need) atomicMin(&s.tau, key);
+    const bool kept = lane < n && (rank ? number < rank : (double)sum * kUnit < need);
+    u64 least = kept ? key : ~0ull;
+    for (uint32_t o = 32; o; o >>= 1) {
+      const u64 w = __shfl_xor(least, o);
+      least = w < least ? w : least;
+    }
+    if (kept && key == least) s.tau = key, s.upto = sum + weight;
+    if (lane == 0 && least == ~0ull) s.tau = ~0ull, s.upto = skipped_sum;
   }
   __syncthreads();
-  const u64 tau = s.tau;
-  __syncthreads();
-  return tau;
+  upto = s.upto;
+  return s.tau;
 }
 
 // ROUNDS: 64 tokens at a time, of a sixteenth of a segment.
@@ -651,7 +670,7 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
   __shared__ double sums[kBins], edges[kBins], side[kWide / 64], masses[kWide];
   __shared__ u64 parts[kSampleSegments];
   __shared__ u64 part, lowest;
-  __shared__ uint32_t chosen;
+  __shared__ uint32_t chosen, counted;
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = blockIdx.x, row = k.row0 + r;
   SampleRow &w = k.rows[r];
   const uint32_t state = w.state;
@@ -682,55 +701,64 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
     for (uint32_t s = tid; s < k.segments; s += kWide) parts[s] = 0;
     __syncthreads();
     const uint32_t bk = w.bk, lo = w.lo, bm = w.bm, kb = w.kb;
-    // weights of a bin's tokens down to a key, in units of 2^-32 of its lower edge
-    const auto sum_of = [&](uint32_t bin, u64 from, bool by_segment) {
+    // tokens of a bin that top-p may cut: known where there is one such bin
+    const auto count_in = [&](uint32_t bin) {
+      if (bin == w.hi && lo == w.hi) return w.lo_n;
       __syncthreads();
-      if (tid == 0) part = 0;
+      if (tid == 0) counted = 0;
       __syncthreads();
-      u64 mine = 0;
-      all.each([&](u64 key, uint32_t i, u64 q) {
-        if (i != bin || key < from) return;
-        mine += kOne + q;
-        if (by_segment) atomicAdd(&parts[(index_of(key) + head) / k.segment], kOne + q);
-      });
-      if (mine) atomicAdd(&part, mine);
+      uint32_t n = 0;
+      all.each([&](u64, uint32_t i, u64) { n += i == bin; });
+      if (n) atomicAdd(&counted, n);
       __syncthreads();
-      return part;
+      return counted;
     };
     const auto upto = [&](uint32_t bin) { return bin ? sums[bin - 1] : 0.0; };
     const auto unit_of = [&](uint32_t bin) { return edges[bin]; };
     cut = kb;
     double kept = sums[kb];
+    u64 in_cut = 0;   // kept weights of the cut's bin, where tau says which
     if (bk != kNoBin) {
-      tau = select(all, bk, w.rank, 0.0, pick);
-      kept = upto(bk) + (double)sum_of(bk, tau, false) * kUnit * unit_of(bk);
+      tau = select(all, bk, w.bk_n, w.rank, 0.0, pick, in_cut);
+      kept = upto(bk) + (double)in_cut * kUnit * unit_of(bk);
     }
     if (lo != kNoBin) {
       const double goal = w.top_p * kept;
       uint32_t b = lo;
       while (b < w.hi && sums[b] < goal) ++b;
       // (never less than the first token, whatever the rounding)
-      const u64 at = select(all, b, 0, fmax((goal - upto(b)) / unit_of(b), 1e-300), pick);
-      if (b < cut || at > tau) tau = at;
+      u64 in_b;
+      const u64 at = select(all, b, count_in(b), 0, fmax((goal - upto(b)) / unit_of(b), 1e-300), pick, in_b);
+      if (b < cut || at > tau) tau = at, in_cut = in_b;
       cut = b;
     }
     if (bm != kNoBin && bm <= cut) {
-      if (tid == 0) lowest = ~0ull;   // nothing of the bin, if none is great enough
+      if (tid == 0) lowest = ~0ull, part = 0;   // nothing of the bin, if none is great enough
       __syncthreads();
       const double t_min = w.t_min;
-      all.each([&](u64 key, uint32_t i, u64) {
-        if (i == bm && place_of(logit_of(key), r16) >= t_min) atomicMin(&lowest, key);
+      u64 sum = 0;
+      all.each([&](u64 key, uint32_t i, u64 q) {
+        if (i != bm || place_of(logit_of(key), r16) < t_min) return;
+        atomicMin(&lowest, key);
+        sum += kOne + q;
       });
+      if (sum) atomicAdd(&part, sum);
       __syncthreads();
-      if (bm < cut || lowest > tau) tau = lowest;
+      if (bm < cut || lowest > tau) tau = lowest, in_cut = part;
       cut = bm;
     }
     // (tau 0: a whole bin, which only a filter that ends with it leaves)
-    z = tau ? upto(cut) + (double)sum_of(cut, tau, true) * kUnit * unit_of(cut) : sums[cut];
+    z = tau ? upto(cut) + (double)in_cut * kUnit * unit_of(cut) : sums[cut];
     if (tid == 0) {
       w.cut_bin = cut;
       w.tau = tau;
       w.z = z;
+    }
+    if (state == kSampleRead && tau && a.d_token) {   // each segment's part of the cut's bin
+      __syncthreads();
+      all.each([&](u64 key, uint32_t i, u64 q) {
+        if (i == cut && key >= tau) atomicAdd(&parts[(index_of(key) + head) / k.segment], kOne + q);
+      });
     }
   }
   if (!a.d_token) return;
@@ -755,7 +783,18 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
       }
     }
     for (uint32_t o = 32; o; o >>= 1) m += __shfl_xor(m, o);
-    if (tau) m += (double)parts[s] * kUnit * edges[cut];
+    if (tau) {
+      u64 in_cut = state == kSampleRead ? parts[s] : 0;
+      if (state == kSampleListed) {
+        for (uint32_t i = lane; i < w.n; i += 64) {
+          const SampleToken t = list[i];
+          const bool mine_too = (uint32_t)(t.at >> 40) == cut && t.key >= tau && (index_of(t.key) + head) / k.segment == s;
+          in_cut += mine_too ? kOne + (t.at & ((1ull << 40) - 1)) : 0;
+        }
+        for (uint32_t o = 32; o; o >>= 1) in_cut += __shfl_xor(in_cut, o);
+      }
+      m += (double)in_cut * kUnit * edges[cut];
+    }
     if (lane == 0) masses[s] = m;
   }
   __syncthreads();

@@ -162,6 +162,7 @@ struct SampleRow {
   uint32_t state;            // kSample...
   uint32_t bk, lo, hi, bm;   // bins in which top-k, top-p (from, to) and min-p cut, or ~0
   uint32_t kb, rank;         // last bin that top-k reaches, and how many tokens of it
+  uint32_t bk_n, lo_n;       // tokens of bin bk; of bin lo, if that is hi
   uint32_t cut_bin, n;       // the cut's bin; tokens to gather
 };
 struct SampleToken {
