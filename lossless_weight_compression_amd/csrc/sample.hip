@@ -60,17 +60,19 @@ __device__ __forceinline__ double place_of(float l, double r16) {
   constexpr double kRound = 6291456.0;   // 3 2^21: one unit in its last place is 2^-30
   return l == __builtin_inff() ? 1e300 : fma((double)l, r16, kRound) - kRound;
 }
-// e^(f / 16) - 1 for 0 <= f < 1 in units of 2^-32 (the next term is below 2^-40).
-__device__ __forceinline__ u64 excess_of(double f) {
-  const double z = f * 0.0625;
-  double s = 1.0 / 720.0;
-  s = fma(s, z, 1.0 / 120.0);
-  s = fma(s, z, 1.0 / 24.0);
-  s = fma(s, z, 1.0 / 6.0);
-  s = fma(s, z, 0.5);
-  s = fma(s, z, 1.0);
-  // the low bits of 2^52 + n are n
-  return (u64)__double_as_longlong(fma(s * z, 4294967296.0, 4503599627370496.0)) & ((1ull << 52) - 1);
+// e^(f / 16) - 1 for f = n 2^-30 < 1 in units of 2^-32, rounded (the next term of
+// the series is below 2^-40).
+__device__ __forceinline__ uint32_t excess_of(uint32_t n) {
+  constexpr double z = 1.0 / 17179869184.0, one = 4294967296.0;   // 2^-34: f / 16 is n z
+  const double x = (double)n;
+  double s = one * z * z * z * z * z * z / 720.0;
+  s = fma(s, x, one * z * z * z * z * z / 120.0);
+  s = fma(s, x, one * z * z * z * z / 24.0);
+  s = fma(s, x, one * z * z * z / 6.0);
+  s = fma(s, x, one * z * z / 2.0);
+  s = fma(s, x, one * z);
+  // the low bits of 2^52 + m are m
+  return (uint32_t)__double_as_longlong(fma(s, x, 4503599627370496.0));
 }
 
 // e^(-i / 16), a bin's lower edge relative to the first bin's: whole powers of e
@@ -99,33 +101,29 @@ __device__ __forceinline__ void fill_edges(double *edges) {   // in LDS
 }
 
 // A token's bin below `edge` (kBins or more: none) and excess. Where the first
-// bin's place is below 2^20 in size, the place rounded to 2^-30 is read off the
-// sum's bits: bin and rest are a shift and a mask. Logits far below (NaN and
-// -infinity among them) are raised to one that is in no bin.
+// bin's place is below 2^20 in size, both are read off the bits of the rounded
+// sum 3 2^21 + place: 30 bits of fraction, then the whole number under an exponent
+// that is the same for all. Logits far below (NaN and -infinity among them) are
+// raised to one that is in no bin.
 struct Places {
   double r16, edge;
-  float lowest;        // raises what lies below 2^-20 of r16
-  uint32_t first;      // the first bin's place plus 3 2^21, as a whole number
+  float lowest;
+  uint32_t first;      // the first bin's bits from the 30th on
   bool near_;
   __device__ __forceinline__ Places(double r, double e) : r16(r), edge(e) {
     near_ = fabs(e) < 1048576.0 && r > 1e-30;
-    lowest = near_ ? (float)fmax(-2000000.0 / r, -3e38) : 0.f;
-    first = (uint32_t)(int32_t)(near_ ? e : 0.0) + 6291456u;
+    lowest = near_ ? (float)(-2000000.0 / r) : 0.f;   // place above -2^21
+    first = (uint32_t)((u64)__double_as_longlong(6291456.0 + (near_ ? e : 0.0)) >> 30);
   }
   template <bool NEAR> __device__ __forceinline__ uint32_t bin_of(float l, uint32_t &excess) const {
     if constexpr (NEAR) {
-      const double at = fma((double)fmaxf(l, lowest), r16, 6291456.0);
-      const u64 bits = (u64)__double_as_longlong(at);
-      // 2^22 <= at < 2^23: 30 bits of fraction, then the whole number, whose
-      // leading one the mask leaves
-      const uint32_t whole = ((uint32_t)(bits >> 30) & 0x3FFFFFu) | 0x400000u;
-      const double f = (double)((uint32_t)bits & 0x3FFFFFFFu) * (1.0 / 1073741824.0);
-      excess = (uint32_t)excess_of(f);
-      return first - whole;
+      const u64 bits = (u64)__double_as_longlong(fma((double)fmaxf(l, lowest), r16, 6291456.0));
+      excess = excess_of((uint32_t)bits & 0x3FFFFFFFu);
+      return first - (uint32_t)(bits >> 30);
     } else {
       const double t = place_of(l, r16), at = floor(t), below = edge - at;
       if (!counts(l) || !(below < (double)kBins)) return kBins;
-      excess = (uint32_t)excess_of(t - at);
+      excess = excess_of((uint32_t)((t - at) * 1073741824.0));   // whole: t is a multiple of 2^-30, or of 1
       return (uint32_t)below;
     }
   }
@@ -230,11 +228,9 @@ template <typename T, uint32_t NT, uint32_t NV>
 __global__ __launch_bounds__(NT) void k_scan(SampleKernelArgs k) {
   constexpr uint32_t E = kPiece<T>, S = NT * NV * E;
   const enc_sample_args &a = k.a;
-  // Lanes count into four copies: two that meet in a word wait for each other.
-  constexpr uint32_t kCopies = 4;
-  __shared__ u64 bins[kCopies][kBins];
-  __shared__ u64 tops[NT / 64];
-  __shared__ uint32_t last;
+  __shared__ u64 bins[kBins];
+  __shared__ float tops[NT / 64];
+  __shared__ uint32_t last, lowest;
   const uint32_t tid = threadIdx.x, r = blockIdx.x / k.segments, seg = blockIdx.x - r * k.segments;
   const uint32_t row = k.row0 + r;
   const T *l = static_cast<const T *>(a.d_logits) + (uint64_t)row * a.logits_row;
@@ -243,25 +239,36 @@ __global__ __launch_bounds__(NT) void k_scan(SampleKernelArgs k) {
 #pragma unroll
   for (uint32_t j = 0; j < NV; ++j) piece[j] = load_piece(l, head, a.vocab, seg * S + (j * NT + tid) * E);
   const Setting set = setting_of(a, row);
-  for (uint32_t i = tid; i < kCopies * kBins; i += NT) bins[0][i] = 0;
-  if (tid == 0) last = 0;
+  for (uint32_t i = tid; i < kBins; i += NT) bins[i] = 0;
+  if (tid == 0) last = 0, lowest = ~0u;
 
-  u64 top = 0;
+  float best = -__builtin_inff();   // (NaN is passed over)
 #pragma unroll
   for (uint32_t j = 0; j < NV; ++j) {
     float x[E];
     values_of<T>(piece[j], x);
 #pragma unroll
-    for (uint32_t e = 0; e < E; ++e)
-      if (counts(x[e])) {
-        const u64 key = key_of(x[e], seg * S + (j * NT + tid) * E + e - head);
-        top = key > top ? key : top;
-      }
+    for (uint32_t e = 0; e < E; ++e) best = fmaxf(best, x[e]);
   }
-  top = wave_max(top);
-  if ((tid & 63) == 0) tops[tid >> 6] = top;
+  for (uint32_t o = 32; o; o >>= 1) best = fmaxf(best, __shfl_xor(best, o));
+  if ((tid & 63) == 0) tops[tid >> 6] = best;
   __syncthreads();
-  for (uint32_t w = 0; w < NT / 64; ++w) top = tops[w] > top ? tops[w] : top;
+  for (uint32_t w = 0; w < NT / 64; ++w) best = fmaxf(best, tops[w]);
+  // the first token that has it: only asked for where no other is kept
+  if (set.first && counts(best)) {
+    uint32_t at = ~0u;
+#pragma unroll
+    for (uint32_t j = 0; j < NV; ++j) {
+      float x[E];
+      values_of<T>(piece[j], x);
+#pragma unroll
+      for (uint32_t e = 0; e < E; ++e)
+        if (x[e] == best) at = min(at, seg * S + (j * NT + tid) * E + e - head);
+    }
+    if (at != ~0u) atomicMin(&lowest, at);
+    __syncthreads();
+  }
+  const u64 top = counts(best) ? key_of(best, set.first ? lowest : 0u) : 0ull;
   SampleSegment *out = k.segs + (uint64_t)r * k.segments + seg;
   if (tid == 0) {
     out->top = top;
@@ -279,7 +286,7 @@ __global__ __launch_bounds__(NT) void k_scan(SampleKernelArgs k) {
       for (uint32_t e = 0; e < E; ++e) {
         uint32_t excess;
         const uint32_t bin = places.bin_of<decltype(near_)::value>(x[e], excess);
-        if (bin < kBins) atomicAdd(&bins[tid % kCopies][bin], (1ull << 49) + excess);
+        if (bin < kBins) atomicAdd(&bins[bin], (1ull << 49) + excess);
       }
     }
   };
@@ -294,9 +301,7 @@ __global__ __launch_bounds__(NT) void k_scan(SampleKernelArgs k) {
 #pragma unroll
   for (uint32_t j = 0; j < (kBins + NT - 1) / NT; ++j) {
     const uint32_t i = tid + j * NT;
-    mine[j] = 0;
-    if (i < kBins)
-      for (uint32_t c = 0; c < kCopies; ++c) mine[j] += bins[c][i];
+    mine[j] = i < kBins ? bins[i] : 0;
     if (mine[j]) used = i + 1;
   }
   atomicMax(&last, used);
@@ -348,7 +353,7 @@ __global__ __launch_bounds__(kWide) void k_plan(SampleKernelArgs k) {
     out.cut_bin = 0;
     out.tau = top;
     // one token alone: its weight, relative to its bin's lower edge
-    out.z = top == 0 ? 0.0 : 1.0 + (double)excess_of(t_max - edge) * kUnit;
+    out.z = top == 0 ? 0.0 : 1.0 + (double)excess_of((uint32_t)((t_max - edge) * 1073741824.0)) * kUnit;
     out.state = top == 0 ? kSampleEmpty : kSampleFirst;
   }
   if (top == 0 || set.first) return;
@@ -684,6 +689,9 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
   const T *l = static_cast<const T *>(a.d_logits) + (uint64_t)row * a.logits_row;
   const uint32_t head = head_of(l);
   const double r16 = w.r16, edge = w.edge;
+  const uint32_t listed = w.n;
+  constexpr uint32_t kShift = ROUNDS == 4 ? 12 : 14;   // of a segment of 1024 ROUNDS
+  static_assert(1u << kShift == 1024 * ROUNDS, "a segment is 1024 times the rounds");
   uint32_t cut = w.cut_bin;
   u64 tau = 0;
   double z = w.z;
@@ -691,7 +699,7 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
   if (state != kSampleWhole) {
     Tokens<T> all;
     all.list = list;
-    all.n = state == kSampleListed ? w.n : 0;
+    all.n = state == kSampleListed ? listed : 0;
     all.row = state == kSampleListed ? nullptr : l;
     all.vocab = a.vocab;
     all.r16 = r16;
@@ -757,7 +765,7 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
     if (state == kSampleRead && tau && a.d_token) {   // each segment's part of the cut's bin
       __syncthreads();
       all.each([&](u64 key, uint32_t i, u64 q) {
-        if (i == cut && key >= tau) atomicAdd(&parts[(index_of(key) + head) / k.segment], kOne + q);
+        if (i == cut && key >= tau) atomicAdd(&parts[(index_of(key) + head) >> kShift], kOne + q);
       });
     }
   }
@@ -786,9 +794,10 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
     if (tau) {
       u64 in_cut = state == kSampleRead ? parts[s] : 0;
       if (state == kSampleListed) {
-        for (uint32_t i = lane; i < w.n; i += 64) {
+#pragma unroll 4
+        for (uint32_t i = lane; i < listed; i += 64) {
           const SampleToken t = list[i];
-          const bool mine_too = (uint32_t)(t.at >> 40) == cut && t.key >= tau && (index_of(t.key) + head) / k.segment == s;
+          const bool mine_too = (uint32_t)(t.at >> 40) == cut && t.key >= tau && (index_of(t.key) + head) >> kShift == s;
           in_cut += mine_too ? kOne + (t.at & ((1ull << 40) - 1)) : 0;
         }
         for (uint32_t o = 32; o; o >>= 1) in_cut += __shfl_xor(in_cut, o);
@@ -825,15 +834,21 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
     x[j] = value_at(l, min(max(first + 64 * j + lane, head), head + a.vocab - 1) - head);
   double weight[ROUNDS];
   double own = 0.0;
+  const auto weigh = [&](auto near_) __attribute__((always_inline)) {
 #pragma unroll
-  for (uint32_t j = 0; j < ROUNDS; ++j) {
-    const uint32_t v = first + 64 * j + lane;
-    uint32_t excess;
-    const uint32_t bin = places.bin_of(x[j], excess);
-    const bool kept = v >= head && v < head + a.vocab && (bin < cut || (bin == cut && key_of(x[j], v - head) >= tau));
-    weight[j] = kept ? (double)(kOne + excess) * kUnit * edges[bin] : 0.0;   // as the bins hold it
-    own += weight[j];
-  }
+    for (uint32_t j = 0; j < ROUNDS; ++j) {
+      const uint32_t v = first + 64 * j + lane;
+      uint32_t excess;
+      const uint32_t bin = places.bin_of<decltype(near_)::value>(x[j], excess);
+      const bool kept = v >= head && v < head + a.vocab && (bin < cut || (bin == cut && key_of(x[j], v - head) >= tau));
+      weight[j] = kept ? (double)(kOne + excess) * kUnit * edges[bin] : 0.0;   // as the bins hold it
+      own += weight[j];
+    }
+  };
+  if (places.near_)
+    weigh(std::true_type{});
+  else
+    weigh(std::false_type{});
   for (uint32_t o = 32; o; o >>= 1) own += __shfl_xor(own, o);
   if (lane == 0) masses[wave] = own;   // (what it held has been read)
   __syncthreads();
@@ -841,13 +856,17 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
   double sum = before;
   uint32_t chosen_wave = 0;
   bool passed = false;
-  for (uint32_t w2 = 0; w2 < kWide / 64 && !passed; ++w2) {
-    const double m = masses[w2];
-    if (m > 0.0) {
+  double each[kWide / 64];
+#pragma unroll
+  for (uint32_t w2 = 0; w2 < kWide / 64; ++w2) each[w2] = masses[w2];
+#pragma unroll
+  for (uint32_t w2 = 0; w2 < kWide / 64; ++w2) {
+    if (passed) continue;
+    if (each[w2] > 0.0) {
       chosen_wave = w2;
-      passed = sum + m > goal;
+      passed = sum + each[w2] > goal;
     }
-    if (!passed) sum += m;
+    if (!passed) sum += each[w2];
   }
   if (wave != chosen_wave) return;
   if (!passed) sum = -1.0;   // its last one, whatever the sums say
