@@ -1279,7 +1279,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_shared(enc_cache c, cons
   const auto clamped = [&](uint32_t i) { return (uint32_t)max(0, min(starts[i], (int32_t)batch)); };
   uint32_t from = 0;
   for (uint32_t i = tid; i <= g; i += kPlanThreads) from = max(from, clamped(i));
-  atomicMax(&bottom, from);
+  for (uint32_t o = 32; o; o >>= 1) from = max(from, (uint32_t)__shfl_xor((int)from, o));
+  if ((tid & 63) == 0) atomicMax(&bottom, from);   // (64 lanes with values of their own would go one by one)
   __syncthreads();
   from = bottom;
   const uint32_t to = max(from, clamped(g + 1));
@@ -1293,7 +1294,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_shared(enc_cache c, cons
     const uint32_t s = (uint32_t)seqs[b];
     len = min(len, s < c.max_seqs ? min((uint32_t)max(c.d_lens[s], 0), room) : 0u);
   }
-  atomicMin(&least, len);
+  for (uint32_t o = 32; o; o >>= 1) len = min(len, (uint32_t)__shfl_xor((int)len, o));
+  if ((tid & 63) == 0) atomicMin(&least, len);
   __syncthreads();
   len = least;
   const uint32_t pages = (len + c.page_size - 1) / c.page_size;

@@ -202,6 +202,11 @@ __device__ __forceinline__ u64 wave_max(u64 v) {
   return v;
 }
 
+template <typename V> __device__ __forceinline__ V wave_total(V v) {
+  for (uint32_t o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
 template <typename V> __device__ __forceinline__ V wave_scan(V v) {   // inclusive
   const uint32_t lane = threadIdx.x & 63;
   for (uint32_t o = 1; o < 64; o <<= 1) {
@@ -304,7 +309,8 @@ __global__ __launch_bounds__(NT) void k_scan(SampleKernelArgs k) {
     mine[j] = i < kBins ? bins[i] : 0;
     if (mine[j]) used = i + 1;
   }
-  atomicMax(&last, used);
+  for (uint32_t o = 32; o; o >>= 1) used = max(used, (uint32_t)__shfl_xor((int)used, o));
+  if ((tid & 63) == 0) atomicMax(&last, used);   // (64 lanes with values of their own would go one by one)
   __syncthreads();
   used = last;
 #pragma unroll
@@ -576,7 +582,11 @@ __device__ u64 select(const Tokens<T> &all, uint32_t bin, uint32_t left, uint32_
         any |= key;
         every &= key;
       });
-      if (any) {
+      for (uint32_t o = 32; o; o >>= 1) {
+        any |= __shfl_xor(any, o);
+        every &= __shfl_xor(every, o);
+      }
+      if (lane == 0 && any) {
         atomicOr(&s.any, any);
         atomicAnd(&s.every, every);
       }
@@ -717,7 +727,8 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
       __syncthreads();
       uint32_t n = 0;
       all.each([&](u64, uint32_t i, u64) { n += i == bin; });
-      if (n) atomicAdd(&counted, n);
+      n = wave_total(n);
+      if (lane == 0 && n) atomicAdd(&counted, n);
       __syncthreads();
       return counted;
     };
@@ -744,13 +755,18 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
       if (tid == 0) lowest = ~0ull, part = 0;   // nothing of the bin, if none is great enough
       __syncthreads();
       const double t_min = w.t_min;
-      u64 sum = 0;
+      u64 sum = 0, least = ~0ull;
       all.each([&](u64 key, uint32_t i, u64 q) {
         if (i != bm || place_of(logit_of(key), r16) < t_min) return;
-        atomicMin(&lowest, key);
+        least = min(least, key);
         sum += kOne + q;
       });
-      if (sum) atomicAdd(&part, sum);
+      sum = wave_total(sum);
+      least = ~wave_max(~least);
+      if (lane == 0 && sum) {
+        atomicAdd(&part, sum);
+        atomicMin(&lowest, least);
+      }
       __syncthreads();
       if (bm < cut || lowest > tau) tau = lowest, in_cut = part;
       cut = bm;
@@ -773,41 +789,43 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
 
   // the segments' kept weights: bins above the cut, and of its bin what is above tau
   __syncthreads();
-  double mine = 0.0;
-  for (uint32_t s = wave; s < k.segments; s += kWide / 64) {
+  // (several waves to a segment where there are few)
+  const uint32_t ways = k.segments > 8 ? 1 : k.segments > 4 ? 2 : k.segments > 2 ? 4 : 8;
+  for (uint32_t unit = wave; unit < k.segments * ways; unit += kWide / 64) {
+    const uint32_t s = unit / ways, way = unit - s * ways;
     const SampleSegment &seg = k.segs[(uint64_t)r * k.segments + s];
     const u64 *bins = k.bins + ((uint64_t)r * k.segments + s) * kBins;
     const uint32_t n = seg.bins;
     const double by = edge - seg.edge;
     double m = 0.0;
     if (n && by < (double)kBins) {
-      const uint32_t d = (uint32_t)by;
-#pragma unroll
-      for (uint32_t i0 = 0; i0 < kBins; i0 += 64) {
-        const uint32_t i = i0 + lane, b = d + i;
-        const bool has = i < n && (b < cut || (b == cut && !tau));
-        const u64 v = bins[has ? i : 0];
-        m += has ? ((double)(v >> 49) + (double)(v & kSumMask) * kUnit) * edges[b] : 0.0;
+      const uint32_t d = (uint32_t)by, end = min(n, cut + 1 > d ? cut + 1 - d : 0u);
+#pragma unroll 4
+      for (uint32_t i = 64 * way + lane; i < end; i += 64 * ways) {
+        const u64 v = bins[i];
+        m += d + i < cut || !tau ? ((double)(v >> 49) + (double)(v & kSumMask) * kUnit) * edges[d + i] : 0.0;
       }
     }
-    for (uint32_t o = 32; o; o >>= 1) m += __shfl_xor(m, o);
+    m = wave_total(m);
     if (tau) {
-      u64 in_cut = state == kSampleRead ? parts[s] : 0;
+      u64 in_cut = state == kSampleRead && way == 0 ? parts[s] : 0;
       if (state == kSampleListed) {
 #pragma unroll 4
-        for (uint32_t i = lane; i < listed; i += 64) {
+        for (uint32_t i = 64 * way + lane; i < listed; i += 64 * ways) {
           const SampleToken t = list[i];
           const bool mine_too = (uint32_t)(t.at >> 40) == cut && t.key >= tau && (index_of(t.key) + head) >> kShift == s;
           in_cut += mine_too ? kOne + (t.at & ((1ull << 40) - 1)) : 0;
         }
-        for (uint32_t o = 32; o; o >>= 1) in_cut += __shfl_xor(in_cut, o);
+        in_cut = wave_total(in_cut);
       }
       m += (double)in_cut * kUnit * edges[cut];
     }
-    if (lane == 0) masses[s] = m;
+    if (lane == 0) masses[unit] = m;
   }
   __syncthreads();
-  mine = tid < k.segments ? masses[tid] : 0.0;
+  double mine = 0.0;
+  if (tid < k.segments)
+    for (uint32_t i = 0; i < ways; ++i) mine += masses[tid * ways + i];
   const double incl = group_scan(mine, side);
   __syncthreads();
   if (tid == kWide - 1) side[0] = incl;
@@ -816,8 +834,10 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
   const float u = a.d_u[row];
   const double goal = (u > 0.f ? u < 1.f ? (double)u : 1.0 : 0.0) * side[0];
   // the first segment whose sum passes it; the last with anything if none does
-  const uint32_t key = incl > goal && mine > 0.0 ? 0x80000000u | (kWide - 1 - tid) : mine > 0.0 ? tid + 1 : 0u;
-  atomicMax(&chosen, key);
+  const uint64_t passes = __ballot(incl > goal && mine > 0.0), has = __ballot(mine > 0.0);
+  if (lane == 0 && has)
+    atomicMax(&chosen, passes ? 0x80000000u | (kWide - 1 - (64 * wave + __builtin_ctzll(passes)))
+                              : 64 * wave + 64 - __builtin_clzll(has));
   __syncthreads();
   const uint32_t seg = chosen & 0x80000000u ? kWide - 1 - (chosen & 0x7FFFFFFFu) : chosen - 1;
   if (tid == seg) side[1] = incl - mine;
