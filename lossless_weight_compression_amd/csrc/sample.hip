@@ -224,7 +224,11 @@ template <typename V> __device__ __forceinline__ V group_scan(V v, V *side) {
   if ((threadIdx.x & 63) == 63) side[wave] = v;
   __syncthreads();
   V before = 0;
-  for (uint32_t w = 0; w < wave; ++w) before += side[w];
+#pragma unroll
+  for (uint32_t w = 0; w < kWide / 64; ++w) {   // all read at once
+    const V other = side[w];
+    if (w < wave) before += other;
+  }
   return before + v;
 }
 
