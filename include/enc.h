@@ -542,7 +542,8 @@ typedef struct enc_prefix_attention_args {
 /* Limits as for enc_tree_attention; groups up to 2^20. The workspace (any
  * contents) holds the plan of the call, made on the device from lengths and
  * groups, and the sums of the pieces that rows are cut into, joined in a fixed
- * order: equal inputs give equal bits. Asynchronous. */
+ * order: equal inputs give equal bits. Calls sharing one must not overlap.
+ * Asynchronous. */
 uint64_t enc_prefix_attention_workspace_bytes(const enc_prefix_attention_args *h_args);
 enc_status enc_prefix_attention(const enc_prefix_attention_args *h_args, void *d_ws, uint64_t ws_bytes,
                                 void *stream);
@@ -623,8 +624,8 @@ typedef struct enc_sample_args {
 
 /* vocab up to 2^22, rows up to 2^20; rows need no alignment beyond their
  * type's. d_probs must not overlap d_logits. The workspace may hold anything;
- * its size does not depend on the settings and stops growing at 1024 rows.
- * Asynchronous. */
+ * its size does not depend on the settings and stops growing at 1024 rows, or
+ * some 300 MB; calls sharing one must not overlap. Asynchronous. */
 uint64_t enc_sample_workspace_bytes(uint32_t rows, uint32_t vocab);
 enc_status enc_sample(const enc_sample_args *h_args, void *d_ws, uint64_t ws_bytes, void *stream);
 

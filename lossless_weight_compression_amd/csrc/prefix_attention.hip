@@ -97,7 +97,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_prefix_plan_small(PrefixAttnAr
   __shared__ u64 side[kPlanThreads / 64], side2[kPlanThreads / 64], side3[kPlanThreads / 64];
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, threads = blockDim.x;   // > groups, >= batch
   const uint32_t per = a.nodes * k.group.d, groups = k.groups, batch = a.batch;
-  uint32_t v = tid <= groups ? (uint32_t)max(0, min(k.starts[tid], (int32_t)batch)) : 0u;
+  // (without groups there need be no starts)
+  uint32_t v = groups && tid <= groups ? (uint32_t)max(0, min(k.starts[tid], (int32_t)batch)) : 0u;
   const uint32_t asked = tid < groups ? (uint32_t)max(k.shared[tid], 0) : 0u;
   Seq q;
   q.len = q.live = q.row = 0;
@@ -240,7 +241,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_prefix_plan(PrefixAttnArgs k) 
   uint32_t floor_ = 0;   // greatest start so far
   for (uint32_t g0 = 0; g0 <= k.groups; g0 += kPlanThreads) {
     const uint32_t g = g0 + tid;
-    uint32_t v = g <= k.groups ? (uint32_t)max(0, min(k.starts[g], (int32_t)a.batch)) : 0u;
+    uint32_t v = k.groups && g <= k.groups ? (uint32_t)max(0, min(k.starts[g], (int32_t)a.batch)) : 0u;
     for (uint32_t o = 1; o < 64; o <<= 1) {
       const uint32_t w = __shfl_up(v, o);
       if (lane >= o) v = max(v, w);

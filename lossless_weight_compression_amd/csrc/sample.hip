@@ -1027,11 +1027,12 @@ void launch_rows(const SampleKernelArgs &k, uint32_t rows, hipStream_t s) {
 
 // Segments of 16384 values where that leaves every compute unit one, of 4096
 // below, where a row's latency counts. Rows go 1024 at a time through the
-// workspace.
+// workspace, fewer where they are so long that it would pass some 300 MB.
 SamplePlan plan_sample(uint32_t rows, uint32_t vocab) {
   SamplePlan p;
   p.rows = std::min(rows, 1024u);
   const uint64_t large = (vocab + 7ull + 16383) / 16384;
+  p.rows = (uint32_t)std::min<uint64_t>(p.rows, 32768 / large);
   p.segment = p.rows * large >= 256 || (vocab + 7ull + 4095) / 4096 > kSampleSegments ? 16384 : 4096;
   p.segments = (uint32_t)((vocab + 7ull + p.segment - 1) / p.segment);
   const uint64_t n = (uint64_t)p.rows * p.segments;

@@ -103,7 +103,7 @@ enc_status check_prefix(const enc_prefix_attention_args *a) {
   if (a->groups > (1u << 20)) return unsupported("more than 2^20 groups");
   if (a->t.batch) {   // a grid holds fewer than 2^32 threads
     const PrefixAttnPlan p = plan_prefix_attention(a->t, a->groups);
-    if ((uint64_t)p.items * a->t.kv_heads >= (1u << 24)) return unsupported("more than 2^24 pieces");
+    if ((uint64_t)p.items * a->t.kv_heads >= (1u << 23)) return unsupported("more than 2^23 pieces");
   }
   return ENC_OK;
 }

@@ -167,15 +167,15 @@ SIGNATURES = {
     "enc_gemm_dense_nt": (_ST, [_VP, _U32, _U32, _VP, _U32, _VP, _VP, _U64, _VP]),
     "enc_stream_probe": (_ST, [_VP, _U64, _VP, _U64, _U32, _U32, _VP]),
     "enc_qk_norm_rope": (_ST, [ctypes.POINTER(EncQkArgs), _VP]),
-    "enc_block_norm": (_ST, [ctypes.POINTER(EncBlockNormArgs), _VP]),
+    "enc_block_norm": (_ST, [_VP, _VP]),
     "enc_tree_attention_workspace_bytes": (_U64, [ctypes.POINTER(EncTreeAttentionArgs)]),
     "enc_tree_attention": (_ST, [ctypes.POINTER(EncTreeAttentionArgs), _VP, _U64, _VP]),
     "enc_prefix_attention_workspace_bytes": (_U64, [ctypes.POINTER(EncPrefixAttentionArgs)]),
-    "enc_prefix_attention": (_ST, [ctypes.POINTER(EncPrefixAttentionArgs), _VP, _U64, _VP]),
+    "enc_prefix_attention": (_ST, [_VP, _VP, _U64, _VP]),
     "enc_verify_tree_workspace_bytes": (_U64, [_U32, _U32, _U32]),
     "enc_verify_tree": (_ST, [ctypes.POINTER(EncVerifyArgs), _VP, _U64, _VP]),
     "enc_sample_workspace_bytes": (_U64, [_U32, _U32]),
-    "enc_sample": (_ST, [ctypes.POINTER(EncSampleArgs), _VP, _U64, _VP]),
+    "enc_sample": (_ST, [_VP, _VP, _U64, _VP]),
     "enc_cache_workspace_bytes": (_U64, [ctypes.POINTER(EncCache), _U32, _U32]),
     "enc_cache_commit": (_ST, [ctypes.POINTER(EncCache), _VP, _U32, _VP, _U64, _U64, _VP, _VP, _U32, _VP,
                                _VP, _U64, _VP]),
@@ -627,7 +627,8 @@ def _load_types():
     _codes.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
 
 
-# the argument structs in one go (field by field costs about 0.1 us each)
+# the argument structs in one go (field by field costs about 0.1 us each); the
+# calls that take them as bytes save the copy into a struct
 _QK_PACK = struct.Struct("=22Q10IfI").pack
 _BLOCK_PACK = struct.Struct("=12Q9I3f").pack
 _ATTN_PACK = struct.Struct("=27Q10IfI").pack
@@ -812,10 +813,10 @@ def enc_block_norm(h, y=None, gate=None, w_post=None, w_pre=None, post_norm=Fals
     if not writes_h and x is None:
         return ho, None
     flags = (ENC_BLOCK_POST_NORM if post_norm else 0) | (ENC_BLOCK_UNIT_OFFSET if unit_offset else 0)
-    a = EncBlockNormArgs.from_buffer_copy(_BLOCK_PACK(
+    a = _BLOCK_PACK(
         yp, h.data_ptr(), gp, qp, pp, hop, op, ys, hs[0], gs, hos, os, tokens, width, every, y_code, h_code, g_code,
-        w_code, out_code, flags, eps, h_scale, y_scale))
-    _check(lib().enc_block_norm(ctypes.byref(a), _handle(stream, device)))
+        w_code, out_code, flags, eps, h_scale, y_scale)
+    _check(lib().enc_block_norm(a, _handle(stream, device)))
     return ho, x
 
 
@@ -934,13 +935,13 @@ def enc_prefix_attention(q, k_new, v_new, k_cache, v_cache, table, lens, starts,
         with _on(stream):
             out, lse, ws = room()
     os = _values(out, "out", dtype, shape, device)
-    a = EncPrefixAttentionArgs.from_buffer_copy(_PREFIX_PACK(
+    a = _PREFIX_PACK(
         q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
         lse.data_ptr() if lse is not None else 0, tp, lp, sp, np_, mp,
         qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], cs[0], cs[1], cs[2], os[0], os[1], os[2],
         batch, n, q_heads, kv_heads, dim, _code(dtype), pages, page, max_pages, max_seqs,
-        dim ** -0.5 if scale is None else scale, 0, stp, shp, groups, 0))
-    _check(lib().enc_prefix_attention(ctypes.byref(a), *_scratch(ws, device), _handle(stream, device)))
+        dim ** -0.5 if scale is None else scale, 0, stp, shp, groups, 0)
+    _check(lib().enc_prefix_attention(a, *_scratch(ws, device), _handle(stream, device)))
     return out, lse
 
 
@@ -1037,10 +1038,10 @@ def enc_sample(logits, u=None, temperature=None, top_k=None, top_p=None, min_p=N
     ps, pp, p_code = 0, 0, 0
     if probs is not None:
         ps, pp, p_code = _values(probs, "probs", probs.dtype, shape, device)[0], probs.data_ptr(), _code(probs.dtype)
-    a = EncSampleArgs.from_buffer_copy(_SAMPLE_PACK(
+    a = _SAMPLE_PACK(
         logits.data_ptr(), up, *at, token.data_ptr() if token is not None else 0, pp, ls[0], ps, rows, vocab,
-        max(rows // n, 1) if n else 1, _code(logits.dtype), p_code, 0))
-    _check(lib().enc_sample(ctypes.byref(a), *_scratch(ws, device), _handle(stream, device)))
+        max(rows // n, 1) if n else 1, _code(logits.dtype), p_code, 0)
+    _check(lib().enc_sample(a, *_scratch(ws, device), _handle(stream, device)))
     return token, probs
 
 

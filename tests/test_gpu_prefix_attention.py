@@ -8,6 +8,7 @@ off by less than 256 2^-24 sum |q k| scale, which for the inputs here (|q|,
 |k| about 1 a value) is below 2^-11 absolute and so relative in p. Together
 |err| <= u |o| + (u + 2^-10) sum p |v|, and the log-sum-exp is off by less than
 2^-11 + 2^-20 |lse|."""
+import ctypes
 import sys
 
 import numpy as np
@@ -150,11 +151,12 @@ def test_chain_without_a_mask(E, T):
     Case([(100, [3, 50]), (33, [0, 1])], T, 4, 2, 128, 16, seed=1).check(E, mask=False)
 
 
-@pytest.mark.parametrize("D,dt", [(64, BF), (128, FP), (256, BF)])
-def test_any_shared_length(E, D, dt):
+@pytest.mark.parametrize("D,dt,T", [(64, BF, 2), (128, FP, 2), (256, BF, 2), (64, FP, 10), (128, BF, 10), (256, FP, 10),
+                                    (64, BF, 30), (128, BF, 30), (96, FP, 30)])
+def test_any_shared_length(E, D, dt, T):
     """Fewer tokens than the rows agree in, none, more than the shortest has, negative: results stay the same."""
-    say("shared lengths", D)
-    c = Case([(100, [0, 3, 40]), (65, [1, 2])], 2, 4, 2, D, 16, dt, seed=2)
+    say("shared lengths", D, T)
+    c = Case([(100, [0, 3, 40]), (65, [1, 2])], T, 4, 2, D, 16, dt, seed=2)
     for shared in ([100, 65], [99, 1], [0, 0], [32, 64], [31, 33], [-7, 65], [1, -2 ** 31]):
         c.check(E, shared=shared)
     c = Case([(100, [0, 3, 40])], 1, 4, 2, D, 16, dt, seed=3)
@@ -193,7 +195,7 @@ def test_table_far_wider_than_the_histories(E):
     Case([(700, [30, 0, 500])], 3, 8, 2, 128, 16, seed=7, width=4000).check(E)
 
 
-@pytest.mark.parametrize("T", [2, 20])
+@pytest.mark.parametrize("T", [2, 8, 20])
 def test_strangers_leave_rows_alone(E, T):
     """NaN and infinities in pages' unused rows, in pages of nobody, and in nodes that a row does not see."""
     say("strangers", T)
@@ -220,10 +222,11 @@ def test_strangers_leave_rows_alone(E, T):
     assert out[1, T - 1].isnan().all() and (out[0, T - 1] == float("inf")).all()
 
 
-def test_a_row_depends_on_nothing_but_its_own(E):
+@pytest.mark.parametrize("T", [1, 8, 30])
+def test_a_row_depends_on_nothing_but_its_own(E, T):
     """Large and infinite queries of one sequence change nothing in the others, to the bit."""
-    say("rows")
-    c = Case([(300, [0, 3, 40, 7, 9])], 1, 8, 2, 128, 16, seed=9)
+    say("rows", T)
+    c = Case([(300, [0, 3, 40, 7, 9])], T, 8, 2, 128, 16, seed=9)
     want, wl = c.run(E)
     c.q[2] *= 1000.0
     c.q[3, 0, 1] = float("inf")
@@ -232,11 +235,12 @@ def test_a_row_depends_on_nothing_but_its_own(E):
         assert torch.equal(got[b], want[b]) and torch.equal(gl[b], wl[b])
 
 
+@pytest.mark.parametrize("T", [3, 10, 30])                                # up to 16 rows of a group, 64, more
 @pytest.mark.parametrize("scale", [0.0, -0.1, 30.0, 1e-30, 1e30, -1e38, 3e38])
-def test_scales(E, scale):
+def test_scales(E, scale, T):
     """Any finite scale. With large ones one key takes all: then inputs are whole numbers, so that scores are exact."""
-    say("scale", scale)
-    c = Case([(90, [0, 20]), (40, [3, 3, 3])], 3, 4, 2, 64, 16, seed=10)
+    say("scale", scale, T)
+    c = Case([(90, [0, 20]), (40, [3, 3, 3])], T, 4, 2, 64, 16, seed=10)
     if abs(scale) > 1:
         for t in (c.q, c.kn, c.kc):
             t.copy_(t.mul(2).round())
@@ -351,6 +355,42 @@ def test_against_tree_attention(E):
     want, wl, size = c.want()
     compare(same, same_lse, want, wl, size)
     assert (lse - same_lse).abs().max() < 2.0 ** -10
+
+
+def test_far_scores(E):
+    """Scores that differ by little where they are large: whole numbers up to 2^16 and beyond, in every kernel."""
+    say("far scores")
+    for T in (1, 8, 30):
+        c = Case([(200, [0, 9, 40])], T, 4, 2, 64, 16, seed=19)
+        for t in (c.q, c.kn, c.kc):
+            t.copy_(t.mul(2).round())
+        c.q[..., 0], c.kn[..., 0], c.kc[..., 0] = 256.0, 256.0, 256.0      # 65536 in every score
+        c.q[..., 1] *= 64
+        c.scale = 0.125
+        c.check(E)
+
+
+def test_no_groups_no_pointers(E):
+    """groups = 0: starts and shared may be NULL."""
+    say("no groups")
+    c = Case([(60, [0, 3])], 2, 4, 2, 64, 16, seed=20)
+    want, _ = c.run(E, starts=[0], shared=[])
+    out = torch.empty_like(c.q)
+    table, lens, mask = dev(c.table), dev(c.lens), dev(ref.mask_words(c.seen), np.int64)
+    ws = E.prefix_attention_workspace(c.q, c.kn, table, c.kc, dev([0]))
+    a = E.EncPrefixAttentionArgs()
+    t = a.t
+    t.d_q, t.d_k_new, t.d_v_new, t.d_k_cache, t.d_v_cache, t.d_out = (x.data_ptr() for x in (c.q, c.kn, c.vn, c.kc, c.vc, out))
+    t.d_table, t.d_lens, t.d_mask = table.data_ptr(), lens.data_ptr(), mask.data_ptr()
+    for n, x in (("q", c.q), ("k_new", c.kn), ("v_new", c.vn), ("out", out)):
+        for m, st in zip(("batch", "node", "head"), x.stride()):
+            setattr(t, n + "_" + m, st)
+    t.cache_page, t.cache_token, t.cache_head = c.kc.stride()[:3]
+    t.batch, t.nodes, t.q_heads, t.kv_heads, t.head_dim, t.dtype = c.B, c.T, c.H, c.G, c.D, 1
+    t.n_pages, t.page_size, t.max_pages, t.max_seqs, t.scale = c.kc.shape[0], 16, c.table.shape[1], c.B, c.scale
+    assert E.lib().enc_prefix_attention(ctypes.byref(a), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
 
 
 def test_binding_refusals(E):
