@@ -793,23 +793,24 @@ def enc_block_norm(h, y=None, gate=None, w_post=None, w_pre=None, post_norm=Fals
             raise TypeError("the weights must have one type")
     if not pre_norm and (out is not None or w_pre is not None):
         raise ValueError("out or w_pre without pre_norm")
-    writes_h = y is not None or h_scale != 1.0 or h_out is not None
+    ho, x = h_out, out
+    writes_h = y is not None or h_scale != 1.0 or ho is not None
+    if writes_h and ho is None or pre_norm and x is None:
+        def room():
+            return (h.new_empty(shape) if writes_h and ho is None else ho,
+                    h.new_empty(shape, dtype=out_dtype or _BF16) if pre_norm and x is None else x)
 
-    def room():
-        return (h.new_empty(shape) if writes_h and h_out is None else h_out,
-                h.new_empty(shape, dtype=out_dtype or _BF16) if pre_norm and out is None else out)
-
-    if stream is None:
-        ho, x = room()
-    else:
-        with _on(stream):
+        if stream is None:
             ho, x = room()
-    if writes_h:
-        hos, hop = _values(ho, "h_out", h.dtype, shape, device)[0], ho.data_ptr()
+        else:
+            with _on(stream):
+                ho, x = room()
+    if writes_h:   # (what was made here needs no checks)
+        hos, hop = width if h_out is None else _values(ho, "h_out", h.dtype, shape, device)[0], ho.data_ptr()
     else:
         ho = h
     if x is not None:
-        os, op, out_code = _values(x, "out", x.dtype, shape, device)[0], x.data_ptr(), _code(x.dtype)
+        os, op, out_code = width if out is None else _values(x, "out", x.dtype, shape, device)[0], x.data_ptr(), _code(x.dtype)
     if not writes_h and x is None:
         return ho, None
     flags = (ENC_BLOCK_POST_NORM if post_norm else 0) | (ENC_BLOCK_UNIT_OFFSET if unit_offset else 0)
@@ -924,6 +925,8 @@ def enc_prefix_attention(q, k_new, v_new, k_cache, v_cache, table, lens, starts,
     stp = _plain(starts, "starts", _I32, (groups + 1,), device)
     shp = _plain(shared, "shared", _I32, (groups,), device)
 
+    given = out is not None
+
     def room():
         return (q.new_empty(shape) if out is None else out,
                 q.new_empty((batch, n, q_heads), dtype=_F32) if return_lse else None,
@@ -934,7 +937,7 @@ def enc_prefix_attention(q, k_new, v_new, k_cache, v_cache, table, lens, starts,
     else:
         with _on(stream):
             out, lse, ws = room()
-    os = _values(out, "out", dtype, shape, device)
+    os = _values(out, "out", dtype, shape, device) if given else (n * q_heads * dim, q_heads * dim, dim)
     a = _PREFIX_PACK(
         q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
         lse.data_ptr() if lse is not None else 0, tp, lp, sp, np_, mp,
@@ -1025,6 +1028,8 @@ def enc_sample(logits, u=None, temperature=None, top_k=None, top_p=None, min_p=N
     if n is not None and (rows % n if n else rows):
         raise ValueError("%d settings for %d rows" % (n, rows))
 
+    given = probs is not None
+
     def room():
         return (logits.new_empty(rows, dtype=_I32) if u is not None else None,
                 logits.new_empty(shape, dtype=probs_dtype or _F32) if return_probs and probs is None else probs,
@@ -1037,7 +1042,8 @@ def enc_sample(logits, u=None, temperature=None, top_k=None, top_p=None, min_p=N
             token, probs, ws = room()
     ps, pp, p_code = 0, 0, 0
     if probs is not None:
-        ps, pp, p_code = _values(probs, "probs", probs.dtype, shape, device)[0], probs.data_ptr(), _code(probs.dtype)
+        ps = _values(probs, "probs", probs.dtype, shape, device)[0] if given else vocab
+        pp, p_code = probs.data_ptr(), _code(probs.dtype)
     a = _SAMPLE_PACK(
         logits.data_ptr(), up, *at, token.data_ptr() if token is not None else 0, pp, ls[0], ps, rows, vocab,
         max(rows // n, 1) if n else 1, _code(logits.dtype), p_code, 0)
