@@ -542,7 +542,8 @@ typedef struct enc_prefix_attention_args {
 /* Limits as for enc_tree_attention; groups up to 2^20. The workspace (any
  * contents) holds the plan of the call, made on the device from lengths and
  * groups, and the sums of the pieces that rows are cut into, joined in a fixed
- * order: equal inputs give equal bits. Calls sharing one must not overlap.
+ * order: equal inputs give equal bits. Its size depends on batch, nodes, heads,
+ * head_dim, groups and max_pages * page_size. Calls sharing one must not overlap.
  * Asynchronous. */
 uint64_t enc_prefix_attention_workspace_bytes(const enc_prefix_attention_args *h_args);
 enc_status enc_prefix_attention(const enc_prefix_attention_args *h_args, void *d_ws, uint64_t ws_bytes,

@@ -8,17 +8,34 @@
 // the sequence's. Each piece leaves its rows' maxima, sums and unnormalised
 // outputs in fp32, and a last kernel joins a row's pieces in their order.
 //
-// Both kinds run in one kernel, k_pieces: a workgroup takes a tile of rows, a KV
-// head and a range of keys. Its four waves hold the same rows and take strips of
-// 32 keys in turn, straight from memory into registers: no barrier in the loop,
-// and a range's sums are joined through LDS before they are written, so that a
-// range costs one set of partial sums, not four. S^T = K Q^T and O^T += V^T P^T
-// as in tree_attention.hip: S^T leaves lane l with keys 4 (l / 16) + i of query
-// row l % 16, which, rounded, are the P^T fragment of the second product; V is
-// transposed in registers.
+// S^T = K Q^T and O^T += V^T P^T as in tree_attention.hip: S^T leaves lane l with
+// keys 4 (l / 16) + i of query row l % 16, which, rounded, are the P^T fragment of
+// the second product. Which pieces there are the device finds from the lengths:
+// k_prefix_plan* cut shared and own work into equal shares.
 //
-// Shared tokens are bound by the matrix unit and the exponentials, own ones by
-// HBM. A wave with 64 rows (U = 4) reads a strip once for 64 rows.
+// k_shared, groups of many rows: eight waves to a workgroup, 64 or 128 rows, a KV
+// head and a range of keys. Keys and values go through LDS in stages of 64, used
+// by four tiles of rows each; two waves to a tile take half of a stage's keys
+// each. Two stages are on their way in registers, three lie in LDS: with one on
+// its way 131072 tokens took 145 us instead of 102. Long ranges of many rows run at 743
+// TFLOP/s (256 rows, from 8192 to 32768 tokens; 3200 cycles a stage of 64 keys):
+// the vector unit is the busiest (51% of the cycles; the matrix unit 23), with the
+// exponentials and conversions; a piece's start and end, some 10 us, is the rest
+// of a short call. Few rows are bound by HBM: 64 rows, 131072 tokens of 8 heads, 102
+// us = 5.3 TB/s.
+//
+// k_pieces, each sequence's own tokens and tree, and groups of few rows: four
+// waves hold the same rows and take strips of 32 keys in turn, straight from
+// memory into registers, with no barrier in the loop; V is transposed in
+// registers; the waves' sums are joined through LDS before they are written, so
+// that a range costs one set of partial sums, not four. It is bound by HBM, and in
+// short calls by the way from the table to the keys. (For the shared tokens of
+// many rows it took 33 us with 32 rows to a wave and 45 with 64, k_shared 24.)
+//
+// Measured, BF16, heads of 128, 32 query and 8 KV heads, whole call on the device:
+// 4 sequences over 1021 shared tokens 15.9 us (plan 5.9, pieces 7.4, join 4.1); 64
+// over 8192 with 512 own tokens at most 62.4 (5.9, shared 24.0, own 21.6, join 6.6;
+// 5.4 for enc_cache_shared); 16 over 131072 132 (5.9, 102, 15, 7.8).
 #include "attention_math.h"
 #include "group_math.h"
 #include "step_common.h"
@@ -84,7 +101,7 @@ __device__ __forceinline__ uint32_t size_of(unsigned long long work, uint32_t sl
 
 // The plan where every group and every sequence has a thread: numbers stay in
 // registers and LDS, and the loads that they come from are on their way at once
-// (one group of 64: 4 us, 12 by the general kernel below). Group g is the batch
+// (one group of 64 sequences: 5.9 us, 12 by the general kernel below). Group g is the batch
 // entries from the greatest start up to g to the greatest up to g + 1: for
 // ascending starts the starts themselves, for any others ranges that do not
 // overlap.
@@ -1348,11 +1365,29 @@ PrefixAttnPlan plan_prefix_attention(const enc_tree_attention_args &a, uint32_t 
   const uint32_t per = a.nodes * (a.q_heads / a.kv_heads);
   const bool large = a.head_dim > 128;
   const uint64_t rows = (uint64_t)a.batch * per, mean = rows / std::max(groups, 1u);
-  p.tile = mean > 64 && !large ? 128 : mean > 16 ? 64 : 16;
-  p.own_tile = per > 16 && !large ? 32 : 16;
+  // Rows of a tile of the shared tokens. A tile that has rows to spare, or two
+  // tiles that each read the keys, cost more by the token; a call of less than
+  // some ten microseconds more of them starts later with the larger one (its
+  // first stage, the exchange between its waves, what it writes). Times in us,
+  // 8 KV heads of 128, for 1021 / 8192 / 131072 shared tokens:
+  //   32 rows: tiles of 16 16.1 / 27.2 / 139, one of 64 22.3 / 31.8 / 119;
+  //   64 rows: four tiles of 16 25 / 35 / 124, one of 64 23.7 / 34.7 / 123;
+  //   128 rows: two tiles of 64 25.1 / 36.5 / 165, one of 128 28.4 / 40.0 / 141;
+  //   256 rows, 8192 tokens, the shared tokens alone: 27 and 24; 1024 rows: 80 and 59.
+  // What a sequence's table can hold stands for its length, which the host does
+  // not know.
+  const uint64_t room = (uint64_t)a.max_pages * a.page_size;
+  p.tile = mean > (room > 16384 ? 64 : 128) && !large ? 128 : mean > (room > 32768 ? 16 : 32) ? 64 : 16;
+  // Of own tokens. 32 rows of a sequence: two tiles of 16 take 48.9 us, one of 32
+  // 52.8 (16 sequences of 8 nodes, 1000 own tokens, heads of 128), but 44.3 and
+  // 42.6 with heads of 64 (40 sequences, 300 tokens). 64 rows: 62.6 and 60.6.
+  p.own_tile = per > (a.head_dim > 64 ? 32 : 16) && !large ? 32 : 16;
   if (p.tile == 16) p.own_tile = 16;   // one kernel for both
   p.own_tiles = (per + p.own_tile - 1) / p.own_tile;
-  // resident workgroups: one of eight waves to a compute unit, or two or three of four
+  // Resident workgroups: one of eight waves to a compute unit, or two or three of
+  // four. 64 sequences over 8192 shared tokens take 62.4 us; with twice as many
+  // shares of the shared tokens 73.5, with three quarters 64.9; with half or twice
+  // as many shares of the own ones 62.4 and 60.9.
   p.slots = std::max((p.tile == 16 ? 512 : 256) / a.kv_heads, 1u);
   p.own_slots = std::max(768 / a.kv_heads, 1u);
   p.least = kWays;
