@@ -195,7 +195,15 @@ def test_table_far_wider_than_the_histories(E):
     Case([(700, [30, 0, 500])], 3, 8, 2, 128, 16, seed=7, width=4000).check(E)
 
 
-@pytest.mark.parametrize("T", [2, 8, 20])
+@pytest.mark.parametrize("T", [5, 20, 40])
+def test_table_that_could_hold_long_histories(E, T):
+    """What a table can hold chooses the tiles of groups of some 20, 80 and more rows, never the result."""
+    say("room", T)
+    for width in (None, 1100, 2100):                                   # pages of 16: up to 17600 and 33600 tokens
+        Case([(100, [0, 3, 40]), (70, [10])], T, 4, 2, 128, 16, seed=19, width=width).check(E)
+
+
+@pytest.mark.parametrize("T", [2, 8, 20, 40])
 def test_strangers_leave_rows_alone(E, T):
     """NaN and infinities in pages' unused rows, in pages of nobody, and in nodes that a row does not see."""
     say("strangers", T)
