@@ -529,8 +529,8 @@ enc_status enc_tree_attention(const enc_tree_attention_args *h_args, void *d_ws,
  * in all of its sequences. They are read where the first of them has them. An
  * entry of no group, and a group of one, share nothing. Numbers out of range
  * count as the nearest in it (starts: [0, batch], a start below an earlier one
- * as that one; d_shared: 0 to the shortest length in the group). Weights are
- * rounded to the values' type, results once more; softmax sums are fp32. */
+ * as that one; d_shared: 0 to the shortest length in the group). However many
+ * rows there are, the result is all that is rounded to the values' type. */
 typedef struct enc_prefix_attention_args {
   enc_tree_attention_args t;       /* as for enc_tree_attention */
   const int32_t *d_starts;         /* [groups + 1], ascending */

@@ -13,6 +13,12 @@
 // the second product. Which pieces there are the device finds from the lengths:
 // k_prefix_plan* cut shared and own work into equal shares.
 //
+// The matrix unit takes P in the values' type: it gets the rounding and the rounded
+// rest, two products, so that the result's own rounding is what is left. Before
+// the rest, 4 sequences over 1021 tokens took 16.1 us (16.3 with it), 64 over 8192
+// with 512 own tokens 63.0 (66.9), 16 over 131072 132.5 (133.1); 256 rows over
+// 131072 tokens, which wait for the matrix unit, 214 (263).
+//
 // k_shared, groups of many rows: eight waves to a workgroup, 64 or 128 rows, a KV
 // head and a range of keys. Keys and values go through LDS in stages of 64, used
 // by four tiles of rows each; two waves to a tile take half of a stage's keys
@@ -380,6 +386,38 @@ __device__ __forceinline__ PrefixItem item_of(const PrefixAttnArgs &k, uint32_t 
   return it;
 }
 
+// Weights as the matrix unit takes them, eight of a lane: rounded to the values'
+// type, and the rounded rest of each.
+template <typename T> __device__ __forceinline__ uint4 rounded(const float (&p)[8]) {
+  return make_uint4(pack2<T>(p[0], p[1]), pack2<T>(p[2], p[3]), pack2<T>(p[4], p[5]), pack2<T>(p[6], p[7]));
+}
+template <typename T> __device__ __forceinline__ uint4 rest_of(const float (&p)[8], uint4 r) {
+  const auto two = [](float a, float b, uint32_t w) { return pack2<T>(a - half_of<T>(w, 0), b - half_of<T>(w, 1)); };
+  return make_uint4(two(p[0], p[1], r.x), two(p[2], p[3], r.y), two(p[4], p[5], r.z), two(p[6], p[7], r.w));
+}
+
+// Where a cached token's row lies, in 16-byte units.
+__device__ __forceinline__ uint32_t cached_row(const PrefixAttnArgs &k, const int32_t *table, uint32_t key) {
+  const uint32_t entry = k.page.quot(key), page = min((uint32_t)max(table[entry], 0), k.a.n_pages - 1);
+  return page * (uint32_t)(k.a.cache_page / 8) + (key - entry * k.page.d) * (uint32_t)(k.a.cache_token / 8);
+}
+// Adds those of a run of values that are no finite numbers.
+template <typename T, int N> __device__ __forceinline__ void add_nonfinite(const T *p, float (&sum)[N]) {
+  uint32_t w[N / 2];
+  if constexpr (N == 8) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    w[0] = v.x, w[1] = v.y;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float x = half_of<T>(w[i / 2], i & 1);
+    if (!__builtin_isfinite(x)) sum[i] += x;
+  }
+}
+
 // ---- a piece
 
 // U: 16-row units of the tile. EXACT: head_dim is DP. OWN: the sequence's own
@@ -563,7 +601,7 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, const PrefixItem 
       }
     }
 
-    uint4 pf[U];
+    uint4 pf[U], pl[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if constexpr (SPECIAL) {
@@ -593,8 +631,8 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, const PrefixItem 
           if (!(seen[u] >> (16 * (j >> 2) + 4 * g4 + (j & 3)) & 1u)) p[u][j] = 0.f;
       }
       l[u] += ((p[u][0] + p[u][1]) + (p[u][2] + p[u][3])) + ((p[u][4] + p[u][5]) + (p[u][6] + p[u][7]));
-      pf[u] = make_uint4(pack2<T>(p[u][0], p[u][1]), pack2<T>(p[u][2], p[u][3]), pack2<T>(p[u][4], p[u][5]),
-                         pack2<T>(p[u][6], p[u][7]));
+      pf[u] = rounded<T>(p[u]);
+      pl[u] = rest_of<T>(p[u], pf[u]);
     }
 #pragma unroll
     for (int n = 0; n < NH; ++n)
@@ -607,7 +645,10 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, const PrefixItem 
                                        f & 1 ? 0x07060302u : 0x05040100u);
         const uint4 vf = make_uint4(w[0], w[1], w[2], w[3]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) o[u][n][f] = Half<T>::mfma(vf, pf[u], o[u][n][f]);
+        for (int u = 0; u < U; ++u) {
+          o[u][n][f] = Half<T>::mfma(vf, pf[u], o[u][n][f]);
+          o[u][n][f] = Half<T>::mfma(vf, pl[u], o[u][n][f]);
+        }
       }
     __builtin_amdgcn_sched_barrier(0);
     after_v();
@@ -650,8 +691,48 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, const PrefixItem 
       load_v(strip);
     }
   }
-  // Infinities and NaN went in as zeros, since 0 times them would reach rows
-  // that do not see them: add them to the rows that do.
+  // The rest of a weight may be 0 or below, and so may come no number, or the
+  // wrong infinity, of an infinite cached value. Every row sees that: where no row
+  // is finite, the values at fault are looked for and their sum is the result.
+    bool lost = true;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float zero = 0.f;
+#pragma unroll
+    for (int n = 0; n < NH; ++n)
+#pragma unroll
+      for (int f = 0; f < C; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) zero = fmaf(o[u][n][f][e], 0.f, zero);
+    lost = lost && rows_sum(zero) != 0.f;
+  }
+  if (__all(lost)) {
+    float sum[NH][4][C] = {};
+    for (strip = lo + wave; strip < min(hi, strips_ctx); strip += kWays)
+      for (uint32_t key = strip * 32; key < min(strip * 32 + 32, ctx); ++key) {
+        const T *row = reinterpret_cast<const T *>(vc + cached_row(k, table, first + key));
+#pragma unroll
+        for (int n = 0; n < NH; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t d = (n * 16 + 4 * g4 + i) * C;
+            if (EXACT || d < D) add_nonfinite(row + d, sum[n][i]);
+          }
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float none = 0.f * rows_sum(l[u]);   // a row of its own fault stays no number
+#pragma unroll
+      for (int n = 0; n < NH; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int f = 0; f < C; ++f)
+            if (sum[n][i][f] != 0.f) o[u][n][f][i] = sum[n][i][f] + none;
+    }
+  }
+  // Infinities and NaN of the tree went in as zeros, since 0 times them would
+  // reach rows that do not see them: add them to the rows that do.
   if (OWN && __any(strange)) {
     for (strip = lo + wave; strip < hi; strip += kWays) {
       if (strip < strips_ctx) continue;
@@ -939,10 +1020,10 @@ __global__ __launch_bounds__(512, 2) void k_shared(PrefixAttnArgs k) {
   auto values_at = [&](uint32_t buf) {
     return reinterpret_cast<const char *>(vs + (buf * kStage + half * 32 + 4 * g4 + (l16 >> 2)) * PITCH) + (l16 & 3) * 8;
   };
-  // The weights of a strip whose maxima are known, packed; l grows by them. With
-  // `masked` only the keys of `bits` weigh anything. `between`: what runs beside
-  // the exponentials.
-  auto weigh = [&](auto masked_, uint32_t bits, uint4 (&pf)[U], auto between) __attribute__((always_inline)) {
+  // The weights of a strip whose maxima are known, packed, and their rests; l grows
+  // by them. With `masked` only the keys of `bits` weigh anything. `between`: what
+  // runs beside the exponentials.
+  auto weigh = [&](auto masked_, uint32_t bits, uint4 (&pf)[U], uint4 (&pl)[U], auto between) __attribute__((always_inline)) {
     bool grown = false;
 #pragma unroll
     for (int u = 0; u < U; ++u) grown = grown || top[u] - mr[u] > slack;
@@ -969,8 +1050,8 @@ __global__ __launch_bounds__(512, 2) void k_shared(PrefixAttnArgs k) {
           if (!(bits >> (16 * (j >> 2) + 4 * g4 + (j & 3)) & 1u)) p[u][j] = 0.f;
       }
       l[u] += ((p[u][0] + p[u][1]) + (p[u][2] + p[u][3])) + ((p[u][4] + p[u][5]) + (p[u][6] + p[u][7]));
-      pf[u] = make_uint4(pack2<T>(p[u][0], p[u][1]), pack2<T>(p[u][2], p[u][3]), pack2<T>(p[u][4], p[u][5]),
-                         pack2<T>(p[u][6], p[u][7]));
+      pf[u] = rounded<T>(p[u]);
+      pl[u] = rest_of<T>(p[u], pf[u]);
     }
   };
 
@@ -1007,15 +1088,18 @@ __global__ __launch_bounds__(512, 2) void k_shared(PrefixAttnArgs k) {
       for (int j = 0; j < 8; ++j)
         if (!(bits >> (16 * (j >> 2) + 4 * g4 + (j & 3)) & 1u)) p[u][j] = -__builtin_inff();
     maxima();
-    uint4 pf[U];
-    weigh(std::true_type{}, bits, pf, [] {});
+    uint4 pf[U], pl[U];
+    weigh(std::true_type{}, bits, pf, pl, [] {});
     const char *vb = values_at(buf);
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
       const uint2 v0 = read_transposed(vb + 32 * f), v1 = read_transposed(vb + 16 * PITCH * 16 + 32 * f);
       const uint4 vf = make_uint4(v0.x, v0.y, v1.x, v1.y);
 #pragma unroll
-      for (int u = 0; u < U; ++u) o[u][f] = Half<T>::mfma(vf, pf[u], o[u][f]);
+      for (int u = 0; u < U; ++u) {
+        o[u][f] = Half<T>::mfma(vf, pf[u], o[u][f]);
+        o[u][f] = Half<T>::mfma(vf, pl[u], o[u][f]);
+      }
     }
   };
 
@@ -1026,8 +1110,8 @@ __global__ __launch_bounds__(512, 2) void k_shared(PrefixAttnArgs k) {
     if constexpr (PIPE) {
       read_k(k_buf);
       float x[U][8];
-      uint4 pf[U];
-      weigh(std::false_type{}, 0u, pf, [&] {
+      uint4 pf[U], pl[U];
+      weigh(std::false_type{}, 0u, pf, pl, [&] {
         __builtin_amdgcn_sched_barrier(0);
         scores(x);
       });
@@ -1048,12 +1132,14 @@ __global__ __launch_bounds__(512, 2) void k_shared(PrefixAttnArgs k) {
         const uint4 vf = make_uint4(v0.x, v0.y, v1.x, v1.y);
 #pragma unroll
         for (int u = 0; u < U; ++u) o[u][f] = Half<T>::mfma(vf, pf[u], o[u][f]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) o[u][f] = Half<T>::mfma(vf, pl[u], o[u][f]);
       }
       maxima();
 #pragma unroll
-      for (int i = 0; i < NF * U; ++i) {
+      for (int i = 0; i < 2 * NF * U; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -1121,6 +1207,40 @@ __global__ __launch_bounds__(512, 2) void k_shared(PrefixAttnArgs k) {
         turn_of(std::integral_constant<int, 1>{});
         if (st >= hi) break;
       }
+    }
+  }
+
+  // As in `piece`: infinite values, of the keys that were this wave's.
+  bool lost = busy;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float zero = 0.f;
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) zero = fmaf(o[u][f][e], 0.f, zero);
+    lost = lost && rows_sum(zero) != 0.f;
+  }
+  if (__all(lost)) {
+    const uint4 *values = static_cast<const uint4 *>(a.d_v_cache) + h * (a.cache_head / 8);
+    float sum[NF][4] = {};
+    for (st = lo; st < hi; ++st)
+      for (uint32_t key = st * kStage + half * 32; key < min(st * kStage + half * 32 + 32, ctx); ++key) {
+        const T *row = reinterpret_cast<const T *>(values + cached_row(k, table, key));
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          const uint32_t d = 16 * f + 4 * g4;
+          if (d < D) add_nonfinite(row + d, sum[f]);
+        }
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float none = 0.f * rows_sum(l[u]);
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (sum[f][e] != 0.f) o[u][f][e] = sum[f][e] + none;
     }
   }
 

@@ -1,0 +1,145 @@
+"""enc_prefix_attention's weights and values over their whole range, in every
+kernel that a call can reach, against the formula in 64 bits.
+
+Tolerances: those derived in test_gpu_prefix_attention.py, where nothing else is
+said."""
+import sys
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_gpu_prefix_attention import Case  # noqa: E402
+
+BF, FP = torch.bfloat16, torch.float16
+U = {BF: 2.0 ** -8, FP: 2.0 ** -11}
+INF = float("inf")
+
+
+def say(*a):
+    print("[gpu-case]", *a, flush=True)
+    sys.stdout.flush()
+
+
+@pytest.fixture(scope="module")
+def E():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from lossless_weight_compression_amd import enc
+    enc.lib()
+    return enc
+
+
+# groups, nodes, query and KV heads, head_dim, page. The rows of a group (sequences x nodes x heads of a KV head), on
+# average, and those of a sequence name the kernels.
+SHAPES = {
+    "12 rows, heads of 128": ([(90, [0, 20, 5]), (40, [1, 2, 3])], 1, 8, 2, 128, 16),
+    "12 rows, heads of 64": ([(90, [0, 20, 5]), (40, [1, 2, 3])], 2, 4, 2, 64, 16),
+    "12 rows, heads of 96": ([(70, [3, 40, 5])], 3, 4, 4, 96, 20),
+    "12 rows, heads of 200": ([(70, [3, 40, 5])], 1, 8, 2, 200, 16),
+    "30 rows of a sequence": ([(70, [9])], 15, 4, 2, 128, 16),
+    "48 rows, heads of 128": ([(90, list(range(12))), (20, [7] * 12)], 1, 8, 2, 128, 16),
+    "48 rows, heads of 64": ([(90, list(range(12))), (20, [7] * 12)], 1, 8, 2, 64, 16),
+    "48 rows, heads of 80": ([(90, list(range(12)))], 1, 4, 1, 80, 16),
+    "48 rows, heads of 256": ([(90, list(range(12))), (20, [7] * 12)], 1, 8, 2, 256, 16),
+    "80 rows, 40 of a sequence, heads of 128": ([(90, [0, 40]), (20, [9, 9])], 10, 8, 2, 128, 16),
+    "80 rows, 40 of a sequence, heads of 64": ([(90, [0, 40]), (20, [9, 9])], 10, 8, 2, 64, 16),
+    "80 rows, 40 of a sequence, heads of 256": ([(90, [0, 40])], 10, 8, 2, 256, 16),
+    "160 rows, heads of 128": ([(90, [i % 7 for i in range(40)])], 1, 8, 2, 128, 16),
+    "160 rows, 40 of a sequence, heads of 96": ([(100, [0, 40, 9, 3]), (20, [9, 9, 9, 9])], 10, 8, 2, 96, 16),
+    "160 rows, 40 of a sequence, heads of 64": ([(100, [0, 40, 9, 3])], 10, 8, 2, 64, 16),
+}
+
+
+class Whole(Case):
+    """q.k = 2^exp n, n whole and small, so that scores are exact."""
+
+    def __init__(self, shape, dt, seed, exp=0):
+        super().__init__(*SHAPES[shape], dt, seed=seed)
+        g = torch.Generator().manual_seed(seed)
+        a, b = exp // 2, exp - exp // 2
+        small = lambda x, e: torch.randint(-1, 2, x.shape, generator=g).to(x.dtype).cuda() * 2.0 ** e  # noqa: E731
+        self.q, self.kn = small(self.q, a), small(self.kn, b)
+        first, at = small(self.kc, b), 0
+        # equal rows stay equal: those of a prompt's last page were copies
+        for size, (prefix, tails) in zip([len(t) for _, t in SHAPES[shape][0]], SHAPES[shape][0]):
+            page, n = prefix // self.page, prefix % self.page
+            if n:
+                source = int(self.table[at, page])
+                for s in range(at, at + size):
+                    first[int(self.table[s, page]), :n] = first[source, :n]
+            at += size
+        self.kc = first
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_only_the_result_is_rounded(E, shape, dt):
+    """Weights count in more than 16 bits, whoever shares the keys. Scores are
+    exact here; the exponents that weights are powers of, at most 46 in size,
+    are off by three roundings of the scale, 2^-18 in all; what is left of a
+    weight in two parts is 2^-18 of it; a sum of n fp32 terms is off by n 2^-24
+    at most (150 keys): 2^-15 of sum p |v| bounds them all, beside the result's
+    own rounding, 2^-8 (BF16) or 2^-11 of it, or 2^-25 in FP16."""
+    say("prefix rounding", shape, dt)
+    c = Whole(shape, dt, 48)
+    out, _ = c.run(E)
+    want, _, size = c.want()
+    g = out.double().cpu().numpy()
+    bad = ~(abs(g - want) <= U[dt] * abs(want) + 2.0 ** -15 * size + (2.0 ** -25 if dt == FP else 0))
+    assert not bad.any(), "%d of %d outside" % (bad.sum(), bad.size)
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_infinite_cached_values(E, shape, dt):
+    """In rows that a group shares, and in one of a sequence's own: infinities of
+    the value's sign, no number where both meet or a value is none, and nothing
+    anywhere else."""
+    say("prefix infinite cached values", shape, dt)
+    c = Case(*SHAPES[shape], dt, seed=49)
+    base, lse = c.run(E)
+    prefix, tails = SHAPES[shape][0][0]
+    group = range(len(tails))
+    alone = max(group, key=lambda b: tails[b])                 # also has one in its own tokens
+    assert tails[alone] > 0
+    at = lambda b, t: (int(c.table[b, t // c.page]), t % c.page)  # noqa: E731
+    for t, d, x in ((0, 1, INF), (prefix // 2, 3, -INF), (prefix - 1, 6, INF), (3, 9, INF), (prefix - 2, 9, -INF),
+                    (prefix // 3, 12, float("nan"))):
+        for b in group:
+            c.vc[at(b, t) + (slice(None), d)] = x
+    c.vc[at(alone, prefix) + (slice(None), 14)] = -INF
+    out, l2 = c.run(E)
+    assert torch.equal(lse, l2)
+    got = out[list(group)].float()
+    assert (got[..., 1] == INF).all() and (got[..., 3] == -INF).all() and (got[..., 6] == INF).all()
+    assert got[..., [9, 12]].isnan().all()
+    assert (got[alone, ..., 14] == -INF).all()
+    # finite places differ at most by what rounding the weights does
+    want, _, size = c.want()
+    with np.errstate(invalid="ignore"):
+        fine = abs(out.double().cpu().numpy() - want) <= U[dt] * abs(want) + (U[dt] + 2.0 ** -10) * size + 1e-30
+    rest = [d for d in range(c.D) if d not in (1, 3, 6, 9, 12)]
+    for b in group:
+        assert fine[b][..., [d for d in rest if d != 14 or b != alone]].all()
+    others = [b for b in range(c.B) if b not in group]
+    assert torch.equal(out[others], base[others])
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("shape", [s for s in SHAPES if len(SHAPES[s][0][0][1]) > 2])
+def test_infinite_values_of_one_sequence(E, shape, dt):
+    """Infinities among one sequence's own tokens, or in its query: the others keep their bits."""
+    say("prefix one sequence's infinities", shape, dt)
+    c = Case(*SHAPES[shape], dt, seed=50)
+    base, lse = c.run(E)
+    prefix, tails = SHAPES[shape][0][0]
+    b = max(range(len(tails)), key=lambda b: tails[b])
+    others = [i for i in range(c.B) if i != b]
+    c.vc[int(c.table[b, prefix // c.page]), prefix % c.page] = INF
+    c.q[b, 0, 0, 0] = INF
+    out, l2 = c.run(E)
+    assert torch.equal(out[others], base[others]) and torch.equal(l2[others], lse[others])
+    assert not out[b].isfinite().any()
