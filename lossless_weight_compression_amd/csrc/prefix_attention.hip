@@ -396,6 +396,10 @@ template <typename T> __device__ __forceinline__ uint4 rest_of(const float (&p)[
   return make_uint4(two(p[0], p[1], r.x), two(p[2], p[3], r.y), two(p[4], p[5], r.z), two(p[6], p[7], r.w));
 }
 
+// (x - top) unit for scores of any size: their halves differ by a finite number.
+__device__ __forceinline__ float less_of(float x, float top, float unit) {
+  return fmaf(x, 0.5f, -0.5f * top) * (2.f * unit);
+}
 // Where a cached token's row lies, in 16-byte units.
 __device__ __forceinline__ uint32_t cached_row(const PrefixAttnArgs &k, const int32_t *table, uint32_t key) {
   const uint32_t entry = k.page.quot(key), page = min((uint32_t)max(table[entry], 0), k.a.n_pages - 1);
@@ -459,11 +463,13 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, const PrefixItem 
     }
   }
 
+  // m: half the maximum of q.k, before the scale. Halves of two finite scores
+  // differ by a finite number, so scale 0 and the least scales are like others.
   f32x4 o[U][NH][C];
-  float m[U], l[U];   // m: of q.k, before the scale
+  float m[U], l[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    m[u] = kLowest;
+    m[u] = 0.5f * kLowest;
     l[u] = 0.f;
 #pragma unroll
     for (int x = 0; x < NH; ++x)
@@ -556,7 +562,7 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, const PrefixItem 
   // values that are no keys' or (tree) not finite become 0. `after_k` and
   // `after_v` load the next strip's halves.
   bool strange = false;   // infinities or NaN were among the tree's values
-  const float c2 = k.unit, slack = k.slack;
+  const float c2 = 2.f * k.unit, slack = k.half_slack;
   auto compute = [&](auto special_, uint32_t strip, auto after_k, auto after_v) {
     constexpr bool SPECIAL = decltype(special_)::value;
     float p[U][8];
@@ -612,7 +618,7 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, const PrefixItem 
       float top = p[u][0];
 #pragma unroll
       for (int j = 1; j < 8; ++j) top = fmaxf(top, p[u][j]);
-      top = rows_max(top);
+      top = 0.5f * rows_max(top);
       if (__any(top - m[u] > slack)) {
         // only the rows concerned: what a row gives does not depend on the others
         const float up = top - m[u] > slack ? top : m[u], shrink = __builtin_amdgcn_exp2f((m[u] - up) * c2);
@@ -626,7 +632,7 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, const PrefixItem 
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // the difference first: exact where it matters, however large the scores
-        p[u][j] = __builtin_amdgcn_exp2f(fmaf(p[u][j] - m[u], c2, Half<T>::kLift2));
+        p[u][j] = __builtin_amdgcn_exp2f(fmaf(fmaf(p[u][j], 0.5f, -m[u]), c2, Half<T>::kLift2));
         if constexpr (SPECIAL)   // -infinity times a scale of 0 is no number
           if (!(seen[u] >> (16 * (j >> 2) + 4 * g4 + (j & 3)) & 1u)) p[u][j] = 0.f;
       }
@@ -802,7 +808,7 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, const PrefixItem 
   for (int u = 0; u < U; ++u) {
     if (it.row0 + 16 * u + l16 >= it.rows) continue;
     const uint64_t row = at + 16 * u + l16;
-    if (g4 == 0) *reinterpret_cast<float2 *>(k.part_ml + 2 * row) = make_float2(m[u], l[u]);
+    if (g4 == 0) *reinterpret_cast<float2 *>(k.part_ml + 2 * row) = make_float2(2.f * m[u], l[u]);
     float *dst = k.part + row * D;
 #pragma unroll
     for (int n = 0; n < NH; ++n)
@@ -1277,7 +1283,7 @@ __global__ __launch_bounds__(512, 2) void k_shared(PrefixAttnArgs k) {
   for (int u = 0; u < U; ++u) {
     const float m2 = mine[64 * i++], l2 = mine[64 * i++];
     const float up = fmaxf(mr[u], m2);
-    const float w1 = __builtin_amdgcn_exp2f((mr[u] - up) * c2), w2 = __builtin_amdgcn_exp2f((m2 - up) * c2);
+    const float w1 = __builtin_amdgcn_exp2f(less_of(mr[u], up, c2)), w2 = __builtin_amdgcn_exp2f(less_of(m2, up, c2));
     l[u] = l[u] * w1 + l2 * w2;
 #pragma unroll
     for (int f = 0; f < NF; ++f)
@@ -1337,7 +1343,7 @@ __global__ __launch_bounds__(256) void k_prefix_join(PrefixAttnArgs k) {
     const uint64_t p = row_of(s);
     const float2 part = ml[p];
     const f32x4 o = *reinterpret_cast<const f32x4 *>(sums + p * a.head_dim);
-    const float w = __builtin_amdgcn_exp2f(fmaxf(part.x - m, kLowest) * k.unit);
+    const float w = __builtin_amdgcn_exp2f(less_of(part.x, m, k.unit));
     l += w * part.y;
     acc += o * w;
   }
@@ -1527,8 +1533,9 @@ PrefixAttnPlan plan_prefix_attention(const enc_tree_attention_args &a, uint32_t 
 }
 
 hipError_t launch_prefix_attention(PrefixAttnArgs k, const PrefixAttnPlan &p, hipStream_t s) {
-  k.unit = std::min(std::fabs(k.a.scale) * kLog2e, -kLowest);
+  k.unit = std::min(std::fabs(k.a.scale) * kLog2e, -kLowest / 2);   // (twice that is used)
   k.slack = std::min(kSlack2 / k.unit, -kLowest);
+  k.half_slack = std::min(kSlack2 / 2 / k.unit, -kLowest);
   if (k.a.dtype == 1)
     launch_type<__bf16>(k, p, s);
   else

@@ -125,7 +125,8 @@ struct PrefixAttnArgs {
   uint32_t tile, own_tile, own_tiles;   // rows of a tile; tiles of a sequence's rows
   uint32_t slots, own_slots, least;     // pieces aimed at; strips in the smallest
   uint32_t mask_words;
-  float unit, slack;         // powers of two to a unit of a maximum; how far a strip may exceed it
+  float unit;                // powers of two to a unit of a maximum
+  float slack, half_slack;   // how far a strip may exceed it; half of that
   uint64_t own_rows;         // of the pieces of own tokens, the first
   float *part, *part_ml;     // [pieces, kv_heads, tile, head_dim], [.., 2] sums; maxima and weights' sums
   PrefixItem *items;

@@ -54,24 +54,24 @@ SHAPES = {
 
 
 class Whole(Case):
-    """q.k = 2^exp n, n whole and small, so that scores are exact."""
+    """q.k = 2^exp n, n whole and small (with `wide`, another 64 up or down for each key), so that scores are exact."""
 
-    def __init__(self, shape, dt, seed, exp=0):
+    def __init__(self, shape, dt, seed, exp=0, wide=False):
         super().__init__(*SHAPES[shape], dt, seed=seed)
         g = torch.Generator().manual_seed(seed)
         a, b = exp // 2, exp - exp // 2
         small = lambda x, e: torch.randint(-1, 2, x.shape, generator=g).to(x.dtype).cuda() * 2.0 ** e  # noqa: E731
-        self.q, self.kn = small(self.q, a), small(self.kn, b)
-        first, at = small(self.kc, b), 0
-        # equal rows stay equal: those of a prompt's last page were copies
-        for size, (prefix, tails) in zip([len(t) for _, t in SHAPES[shape][0]], SHAPES[shape][0]):
+        self.q, self.kn, self.kc = small(self.q, a), small(self.kn, b), small(self.kc, b)
+        if wide:
+            self.q[..., 0] = 32 * 2.0 ** a
+            for x in (self.kn, self.kc):
+                x[..., 0] = (torch.randint(0, 2, x.shape[:-1], generator=g).to(x.dtype).cuda() * 4 - 2) * 2.0 ** b
+        at = 0
+        for prefix, tails in SHAPES[shape][0]:     # equal rows stay equal: those of a prompt's last page were copies
             page, n = prefix // self.page, prefix % self.page
-            if n:
-                source = int(self.table[at, page])
-                for s in range(at, at + size):
-                    first[int(self.table[s, page]), :n] = first[source, :n]
-            at += size
-        self.kc = first
+            for s in range(at, at + len(tails) if n else at):
+                self.kc[int(self.table[s, page]), :n] = self.kc[int(self.table[at, page]), :n]
+            at += len(tails)
 
 
 @pytest.mark.parametrize("dt", [BF, FP])
@@ -143,3 +143,36 @@ def test_infinite_values_of_one_sequence(E, shape, dt):
     out, l2 = c.run(E)
     assert torch.equal(out[others], base[others]) and torch.equal(l2[others], lse[others])
     assert not out[b].isfinite().any()
+
+
+@pytest.mark.parametrize("exp", [0, 100, 120])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_scale_zero(E, shape, exp):
+    """Every row has the mean of what it sees, whatever its scores: up to some 10^37."""
+    say("prefix scale 0", shape, exp)
+    c = Whole(shape, BF, 51, exp)
+    c.scale = 0.0
+    c.check(E)
+    c.seen[:, c.T // 2] = False                    # a node that sees no other, nor itself
+    c.check(E)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -126, -2.0 ** -126, 2.0 ** -124])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_least_scales(E, shape, scale):
+    """Scores that differ by more than fp32 holds, brought to ordinary sizes by the scale: all keys count."""
+    say("prefix least scales", shape, scale)
+    c = Whole(shape, BF, 52, 121, wide=True)
+    c.scale = scale
+    c.check(E)
+
+
+@pytest.mark.parametrize("dt,exp", [(BF, 20), (BF, 30), (BF, 100), (BF, 120), (FP, 20), (FP, 27)])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_large_scores(E, shape, dt, exp):
+    """Scores of 10^6 to 10^36: the largest outweighs all others, equal ones share."""
+    say("prefix large scores", shape, dt, exp)
+    c = Whole(shape, dt, 53, exp)
+    c.check(E)
+    c.scale *= -1
+    c.check(E)
