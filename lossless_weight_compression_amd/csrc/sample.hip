@@ -405,16 +405,18 @@ __global__ __launch_bounds__(kWide) void k_plan(SampleKernelArgs k) {
     k.sums[(uint64_t)r * kBins + tid] = upto;
   }
   __syncthreads();
-  // the bin that a count or a sum is reached in (sums grow: each test is true once)
+  // The bin that a count or a sum is reached in. Counts grow, so that test is true
+  // once; sums of neighbouring bins are taken in different orders and may fall by a
+  // rounding, so the first bin counts.
   if (set.top_k && tid < kBins && n_upto >= set.top_k && n_upto - number < set.top_k) k_bin = tid;
   __syncthreads();
   const uint32_t kb = k_bin;
   const bool k_part = set.top_k && numbers[kb] > set.top_k;
   if (set.top_p < 1.0 && tid < kBins) {
     const double low = set.top_p * (k_part ? kb ? sums[kb - 1] : 0.0 : sums[kb]), high = set.top_p * sums[kb];
-    const double before = tid ? sums[tid - 1] : 0.0;
-    if (upto >= low && (tid == 0 || before < low)) p_low = tid;
-    if (upto >= high && (tid == 0 || before < high)) p_high = tid;
+    const uint64_t lows = __ballot(upto >= low), highs = __ballot(upto >= high);
+    if (lane == 0 && lows) atomicMin(&p_low, tid + __builtin_ctzll(lows));
+    if (lane == 0 && highs) atomicMin(&p_high, tid + __builtin_ctzll(highs));
   }
   __syncthreads();
   uint32_t bk = k_part ? kb : kNoBin, lo = set.top_p < 1.0 ? p_low : kNoBin, hi = set.top_p < 1.0 ? min(p_high, kb) : kb;
@@ -842,8 +844,9 @@ __global__ __launch_bounds__(kWide) void k_resolve(SampleKernelArgs k) {
   if (tid == kWide - 1) side[0] = incl;
   if (tid == 0) chosen = 0;
   __syncthreads();
+  // (with 1 the last one, whatever rounding does to sums of sums)
   const float u = a.d_u[row];
-  const double goal = (u > 0.f ? u < 1.f ? (double)u : 1.0 : 0.0) * side[0];
+  const double goal = u < 1.f ? (u > 0.f ? (double)u * side[0] : 0.0) : u >= 1.f ? __builtin_inf() : 0.0;
   // the first segment whose sum passes it; the last with anything if none does
   const uint64_t passes = __ballot(incl > goal && mine > 0.0), has = __ballot(mine > 0.0);
   if (lane == 0 && has)

@@ -1,0 +1,50 @@
+"""enc_sample where roundings of fp64 sums, or a second rounding of a result,
+would show."""
+import sys
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def say(*a):
+    print("[gpu-case]", *a, flush=True)
+    sys.stdout.flush()
+
+
+@pytest.fixture(scope="module")
+def E():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from lossless_weight_compression_amd import enc
+    enc.lib()
+    return enc
+
+
+@pytest.mark.parametrize("depth", [30.0, 38.0, 42.0, 45.0])
+@pytest.mark.parametrize("rows,V", [(1, 128256), (16, 128256), (64, 128256), (16, 32003), (300, 5000)])
+def test_last_token(E, rows, V, depth):
+    """u of 1 names the last kept token, also where it and many before it weigh less than a sum's rounding."""
+    say("u = 1", rows, V, depth)
+    g = torch.Generator().manual_seed(int(depth))
+    logits = 3.0 * torch.randn(rows, V, generator=g)
+    tail = V // 3
+    logits[:, -tail:] = logits.max(1, keepdim=True)[0] - depth
+    last = V - 1 - torch.arange(rows) % 3                     # the very last ones are not kept in some rows
+    for r in range(rows):
+        logits[r, int(last[r]) + 1:] = -float("inf")
+    token, _ = E.enc_sample(logits.cuda(), torch.ones(rows, device="cuda"))
+    assert torch.equal(token.cpu(), last.int())
+
+
+def test_equal_rows(E):
+    """Equal rows give equal tokens and probabilities, at cuts of every size."""
+    say("equal rows")
+    g = torch.Generator().manual_seed(7)
+    row = 2.0 * torch.randn(1, 50000, generator=g)
+    p = (torch.arange(1, 257) / 257.0).float().repeat_interleave(4)
+    u = torch.rand(256, generator=g).repeat_interleave(4)
+    token, probs = E.enc_sample(row.repeat(1024, 1).cuda(), u.cuda(), top_p=p.cuda(), return_probs=True)
+    token, probs = token.view(256, 4), probs.view(256, 4, -1)
+    assert (token == token[:, :1]).all() and (probs == probs[:, :1]).all()
