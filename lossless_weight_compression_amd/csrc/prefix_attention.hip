@@ -1376,15 +1376,17 @@ void launch_pieces(const PrefixAttnArgs &k, uint32_t items, hipStream_t s) {
 template <typename T, int DP>
 void launch_dim(const PrefixAttnArgs &k, const PrefixAttnPlan &p, hipStream_t s) {
   constexpr int US = DP <= 128 ? 2 : 1;   // units of many own rows
-  if (p.tile == 16) {
+  if (k.groups && p.tile == 16) {
     launch_pieces<T, DP, 1, 1>(k, p.items, s);
     return;
   }
-  const dim3 grid(p.most_shared * k.a.kv_heads), block(512);
-  if (p.tile == 64)
-    hipLaunchKernelGGL((k_shared<T, DP, 1>), grid, block, 0, s, k);
-  else if constexpr (DP <= 128)
-    hipLaunchKernelGGL((k_shared<T, DP, 2>), grid, block, 0, s, k);
+  if (k.groups) {   // (else nothing is shared)
+    const dim3 grid(p.most_shared * k.a.kv_heads), block(512);
+    if (p.tile == 64)
+      hipLaunchKernelGGL((k_shared<T, DP, 1>), grid, block, 0, s, k);
+    else if constexpr (DP <= 128)
+      hipLaunchKernelGGL((k_shared<T, DP, 2>), grid, block, 0, s, k);
+  }
   if (p.own_tile == 16)
     launch_pieces<T, DP, 0, 1>(k, p.most_own, s);
   else if constexpr (US > 1)
@@ -1485,7 +1487,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_shared(enc_cache c, cons
 
 // Tiles of 128 rows where groups have more than 64 on average (heads up to 128
 // values), of 64 where they have more than 16, of 16 below; a sequence's own rows
-// by 32 where there are more than 16 (heads above 128: 16).
+// by 32 where there are more than 16 (heads above 128: 16). Without groups there
+// are only own rows.
 PrefixAttnPlan plan_prefix_attention(const enc_tree_attention_args &a, uint32_t groups) {
   PrefixAttnPlan p;
   const uint32_t per = a.nodes * (a.q_heads / a.kv_heads);
@@ -1508,7 +1511,7 @@ PrefixAttnPlan plan_prefix_attention(const enc_tree_attention_args &a, uint32_t 
   // 52.8 (16 sequences of 8 nodes, 1000 own tokens, heads of 128), but 44.3 and
   // 42.6 with heads of 64 (40 sequences, 300 tokens). 64 rows: 62.6 and 60.6.
   p.own_tile = per > (a.head_dim > 64 ? 32 : 16) && !large ? 32 : 16;
-  if (p.tile == 16) p.own_tile = 16;   // one kernel for both
+  if (groups && p.tile == 16) p.own_tile = 16;   // one kernel for both
   p.own_tiles = (per + p.own_tile - 1) / p.own_tile;
   // Resident workgroups: one of eight waves to a compute unit, or two or three of
   // four. 64 sequences over 8192 shared tokens take 62.4 us; with twice as many
@@ -1520,7 +1523,7 @@ PrefixAttnPlan plan_prefix_attention(const enc_tree_attention_args &a, uint32_t 
   // pieces of `slots` equal shares of the work, and one more, a short one, for
   // every tile
   const uint64_t tiles = std::min<uint64_t>(rows / p.tile + groups, rows);
-  p.most_shared = (uint32_t)(p.slots + tiles);
+  p.most_shared = groups ? (uint32_t)(p.slots + tiles) : 0;
   p.most_own = (uint32_t)(p.own_slots + (uint64_t)a.batch * p.own_tiles);
   p.items = p.most_shared + p.most_own;
   const uint64_t n = (uint64_t)p.most_shared * a.kv_heads * p.tile + (uint64_t)p.most_own * a.kv_heads * p.own_tile;
