@@ -543,8 +543,9 @@ typedef struct enc_prefix_attention_args {
  * contents) holds the plan of the call, made on the device from lengths and
  * groups, and the sums of the pieces that rows are cut into, joined in a fixed
  * order: equal inputs give equal bits. Its size depends on batch, nodes, heads,
- * head_dim, groups and max_pages * page_size. Calls sharing one must not overlap.
- * Asynchronous. */
+ * head_dim, groups and max_pages * page_size; one of this size also serves every
+ * call of the same heads with no more of any of the others. Calls sharing one
+ * must not overlap. Asynchronous. */
 uint64_t enc_prefix_attention_workspace_bytes(const enc_prefix_attention_args *h_args);
 enc_status enc_prefix_attention(const enc_prefix_attention_args *h_args, void *d_ws, uint64_t ws_bytes,
                                 void *stream);
@@ -625,8 +626,9 @@ typedef struct enc_sample_args {
 
 /* vocab up to 2^22, rows up to 2^20; rows need no alignment beyond their
  * type's. d_probs must not overlap d_logits. The workspace may hold anything;
- * its size does not depend on the settings and stops growing at 1024 rows, or
- * some 300 MB; calls sharing one must not overlap. Asynchronous. */
+ * its size does not depend on the settings, stops growing at 1024 rows or some
+ * 300 MB, and serves every call of the same vocab with no more rows; calls
+ * sharing one must not overlap. Asynchronous. */
 uint64_t enc_sample_workspace_bytes(uint32_t rows, uint32_t vocab);
 enc_status enc_sample(const enc_sample_args *h_args, void *d_ws, uint64_t ws_bytes, void *stream);
 

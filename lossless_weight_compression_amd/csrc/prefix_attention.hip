@@ -1485,46 +1485,53 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_shared(enc_cache c, cons
 
 }  // namespace
 
-// Tiles of 128 rows where groups have more than 64 on average (heads up to 128
-// values), of 64 where they have more than 16, of 16 below; a sequence's own rows
-// by 32 where there are more than 16 (heads above 128: 16). Without groups there
-// are only own rows.
-PrefixAttnPlan plan_prefix_attention(const enc_tree_attention_args &a, uint32_t groups) {
-  PrefixAttnPlan p;
-  const uint32_t per = a.nodes * (a.q_heads / a.kv_heads);
-  const bool large = a.head_dim > 128;
-  const uint64_t rows = (uint64_t)a.batch * per, mean = rows / std::max(groups, 1u);
-  // Rows of a tile of the shared tokens. A tile that has rows to spare, or two
-  // tiles that each read the keys, cost more by the token; a call of less than
-  // some ten microseconds more of them starts later with the larger one (its
-  // first stage, the exchange between its waves, what it writes). Times in us,
-  // 8 KV heads of 128, for 1021 / 8192 / 131072 shared tokens:
-  //   32 rows: tiles of 16 16.1 / 27.2 / 139, one of 64 22.3 / 31.8 / 119;
-  //   64 rows: four tiles of 16 25 / 35 / 124, one of 64 23.7 / 34.7 / 123;
-  //   128 rows: two tiles of 64 25.1 / 36.5 / 165, one of 128 28.4 / 40.0 / 141;
-  //   256 rows, 8192 tokens, the shared tokens alone: 27 and 24; 1024 rows: 80 and 59.
-  // What a sequence's table can hold stands for its length, which the host does
-  // not know.
+namespace {
+
+// Average rows of a group from which tiles are of 64 and of 128 rows, and rows of
+// a sequence from which its own are of 32.
+//
+// A tile of shared tokens that has rows to spare, or two tiles that each read the
+// keys, cost more by the token; a call of less than some ten microseconds more of
+// them starts later with the larger one (its first stage, the exchange between its
+// waves, what it writes). Times in us, 8 KV heads of 128, for 1021 / 8192 / 131072
+// shared tokens:
+//   32 rows: tiles of 16 16.1 / 27.2 / 139, one of 64 22.3 / 31.8 / 119;
+//   64 rows: four tiles of 16 25 / 35 / 124, one of 64 23.7 / 34.7 / 123;
+//   128 rows: two tiles of 64 25.1 / 36.5 / 165, one of 128 28.4 / 40.0 / 141;
+//   256 rows, 8192 tokens, the shared tokens alone: 27 and 24; 1024 rows: 80 and 59.
+// What a sequence's table can hold stands for its length, which the host does
+// not know.
+//
+// Of own tokens. 32 rows of a sequence: two tiles of 16 take 48.9 us, one of 32
+// 52.8 (16 sequences of 8 nodes, 1000 own tokens, heads of 128), but 44.3 and
+// 42.6 with heads of 64 (40 sequences, 300 tokens). 64 rows: 62.6 and 60.6.
+struct TileRule {
+  bool large;   // heads above 128 values: no tiles of 128 rows, nor of 32 own ones
+  uint64_t from64, from128, own32;
+};
+TileRule tile_rule(const enc_tree_attention_args &a) {
   const uint64_t room = (uint64_t)a.max_pages * a.page_size;
-  p.tile = mean > (room > 16384 ? 64 : 128) && !large ? 128 : mean > (room > 32768 ? 16 : 32) ? 64 : 16;
-  // Of own tokens. 32 rows of a sequence: two tiles of 16 take 48.9 us, one of 32
-  // 52.8 (16 sequences of 8 nodes, 1000 own tokens, heads of 128), but 44.3 and
-  // 42.6 with heads of 64 (40 sequences, 300 tokens). 64 rows: 62.6 and 60.6.
-  p.own_tile = per > (a.head_dim > 64 ? 32 : 16) && !large ? 32 : 16;
-  if (groups && p.tile == 16) p.own_tile = 16;   // one kernel for both
-  p.own_tiles = (per + p.own_tile - 1) / p.own_tile;
-  // Resident workgroups: one of eight waves to a compute unit, or two or three of
-  // four. 64 sequences over 8192 shared tokens take 62.4 us; with twice as many
-  // shares of the shared tokens 73.5, with three quarters 64.9; with half or twice
-  // as many shares of the own ones 62.4 and 60.9.
-  p.slots = std::max((p.tile == 16 ? 512 : 256) / a.kv_heads, 1u);
+  return {a.head_dim > 128, room > 32768 ? 17u : 33u, room > 16384 ? 65u : 129u, a.head_dim > 64 ? 33u : 17u};
+}
+
+// The plan for given tiles: pieces of `slots` equal shares of the work, and one
+// more, a short one, for every tile.
+//
+// Resident workgroups: one of eight waves to a compute unit, or two or three of
+// four. 64 sequences over 8192 shared tokens take 62.4 us; with twice as many
+// shares of the shared tokens 73.5, with three quarters 64.9; with half or twice
+// as many shares of the own ones 62.4 and 60.9.
+PrefixAttnPlan plan_of(const enc_tree_attention_args &a, uint32_t groups, uint32_t tile, uint32_t own_tile,
+                       uint64_t tiles, uint64_t own_tiles_of_all) {
+  PrefixAttnPlan p;
+  p.tile = tile;
+  p.own_tile = own_tile;
+  p.own_tiles = (a.nodes * (a.q_heads / a.kv_heads) + own_tile - 1) / own_tile;
+  p.slots = std::max((tile == 16 ? 512 : 256) / a.kv_heads, 1u);
   p.own_slots = std::max(768 / a.kv_heads, 1u);
   p.least = kWays;
-  // pieces of `slots` equal shares of the work, and one more, a short one, for
-  // every tile
-  const uint64_t tiles = std::min<uint64_t>(rows / p.tile + groups, rows);
   p.most_shared = groups ? (uint32_t)(p.slots + tiles) : 0;
-  p.most_own = (uint32_t)(p.own_slots + (uint64_t)a.batch * p.own_tiles);
+  p.most_own = (uint32_t)(p.own_slots + own_tiles_of_all);
   p.items = p.most_shared + p.most_own;
   const uint64_t n = (uint64_t)p.most_shared * a.kv_heads * p.tile + (uint64_t)p.most_own * a.kv_heads * p.own_tile;
   p.part_bytes = align_up(4 * n * a.head_dim, 256);
@@ -1533,6 +1540,46 @@ PrefixAttnPlan plan_prefix_attention(const enc_tree_attention_args &a, uint32_t 
   p.batch_bytes = align_up(4ull * a.batch, 256);
   p.group_bytes = align_up(4ull * (groups + 1), 256);
   return p;
+}
+
+}  // namespace
+
+PrefixAttnPlan plan_prefix_attention(const enc_tree_attention_args &a, uint32_t groups) {
+  const TileRule rule = tile_rule(a);
+  const uint32_t per = a.nodes * (a.q_heads / a.kv_heads);
+  const uint64_t rows = (uint64_t)a.batch * per, mean = rows / std::max(groups, 1u);
+  const uint32_t tile = !groups ? 16 : mean >= rule.from128 && !rule.large ? 128 : mean >= rule.from64 ? 64 : 16;
+  // (with tiles of 16 one kernel takes both)
+  const uint32_t own_tile = per >= rule.own32 && !rule.large && (!groups || tile > 16) ? 32 : 16;
+  return plan_of(a, groups, tile, own_tile, std::min<uint64_t>(rows / tile + groups, rows),
+                 (uint64_t)a.batch * ((per + own_tile - 1) / own_tile));
+}
+
+// Enough for every call with no more sequences, nodes, groups or room in the
+// table: fewer groups have larger tiles, so the most over the tiles that such calls
+// can choose, each with as many of them as there can be.
+uint64_t prefix_attention_bytes(const enc_tree_attention_args &a, uint32_t groups) {
+  const TileRule rule = tile_rule(a);
+  const uint32_t per = a.nodes * (a.q_heads / a.kv_heads);
+  const uint64_t rows = (uint64_t)a.batch * per;
+  uint64_t most = 0;
+  const auto consider = [&](uint32_t any, uint32_t tile, uint32_t own_tile, uint64_t tiles, uint64_t own) {
+    most = std::max(most, plan_of(a, any, tile, own_tile, tiles, own).total());
+  };
+  for (uint32_t own_tile = 16; own_tile <= (per >= rule.own32 && !rule.large ? 32u : 16u); own_tile += 16) {
+    const uint64_t own = (uint64_t)a.batch * ((per + own_tile - 1) / own_tile);
+    consider(0, 16, own_tile, 0, own);
+    if (!groups) continue;
+    if (own_tile == 16) {
+      const uint64_t few = std::min<uint64_t>(rows, 33ull * groups);   // at most 32 rows a group, on average
+      consider(groups, 16, 16, std::min<uint64_t>(few / 16 + groups, few), std::min(own, few));
+    }
+    if (rows >= rule.from64)
+      consider(groups, 64, own_tile, rows / 64 + std::min<uint64_t>(groups, rows / rule.from64), own);
+    if (rows >= rule.from128 && !rule.large)
+      consider(groups, 128, own_tile, rows / 128 + std::min<uint64_t>(groups, rows / rule.from128), own);
+  }
+  return most;
 }
 
 hipError_t launch_prefix_attention(PrefixAttnArgs k, const PrefixAttnPlan &p, hipStream_t s) {

@@ -1054,6 +1054,12 @@ SamplePlan plan_sample(uint32_t rows, uint32_t vocab) {
   return p;
 }
 
+// The plan grows with the rows but where it goes over to longer segments.
+uint64_t sample_bytes(uint32_t rows, uint32_t vocab) {
+  const uint32_t large = (uint32_t)((vocab + 7ull + 16383) / 16384), few = std::min(rows, 255 / large);
+  return std::max(plan_sample(rows, vocab).total(), few ? plan_sample(few, vocab).total() : 0);
+}
+
 hipError_t launch_sample(SampleKernelArgs k, const SamplePlan &p, hipStream_t s) {
   for (uint64_t row0 = 0; row0 < k.a.rows; row0 += p.rows) {
     k.row0 = (uint32_t)row0;

@@ -241,7 +241,7 @@ enc_status enc_tree_attention(const enc_tree_attention_args *a, void *d_ws, uint
 uint64_t enc_prefix_attention_workspace_bytes(const enc_prefix_attention_args *a) {
   set_error(ENC_OK, "%s", "");
   if (check_prefix(a) != ENC_OK || a->t.batch == 0) return 0;
-  return plan_prefix_attention(a->t, a->groups).total();
+  return prefix_attention_bytes(a->t, a->groups);
 }
 
 enc_status enc_prefix_attention(const enc_prefix_attention_args *a, void *d_ws, uint64_t ws_bytes, void *stream) {
@@ -332,8 +332,7 @@ enc_status enc_verify_tree(const enc_verify_args *a, void *d_ws, uint64_t ws_byt
 uint64_t enc_sample_workspace_bytes(uint32_t rows, uint32_t vocab) {
   set_error(ENC_OK, "%s", "");
   if (!rows || rows > (1u << 20) || !vocab || vocab > (1u << 22)) return 0;
-  const SamplePlan p = plan_sample(rows, vocab);
-  return p.bins + p.segs + p.sums + p.row_bytes + p.list;
+  return sample_bytes(rows, vocab);
 }
 
 enc_status enc_sample(const enc_sample_args *a, void *d_ws, uint64_t ws_bytes, void *stream) {
@@ -354,7 +353,7 @@ enc_status enc_sample(const enc_sample_args *a, void *d_ws, uint64_t ws_bytes, v
   if (a->logits_row >> 40 || a->probs_row >> 40) return unsupported("a stride of 2^40 or more");
   if (a->d_probs && a->rows > 1 && a->probs_row < a->vocab) return invalid("rows of probs overlap");
   const SamplePlan p = plan_sample(a->rows, a->vocab);
-  const uint64_t need = p.bins + p.segs + p.sums + p.row_bytes + p.list;
+  const uint64_t need = p.total();
   if (!d_ws || !aligned(d_ws, 16)) return invalid("workspace is NULL or not 16-byte aligned");
   if (ws_bytes < need)
     return set_error(ENC_ERR_CAPACITY, "workspace of %llu bytes, %llu needed", (unsigned long long)ws_bytes,

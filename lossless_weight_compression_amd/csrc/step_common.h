@@ -142,6 +142,7 @@ struct PrefixAttnPlan {
   uint64_t total() const { return part_bytes + ml_bytes + item_bytes + 4 * batch_bytes + 4 * group_bytes + 256; }
 };
 PrefixAttnPlan plan_prefix_attention(const enc_tree_attention_args &a, uint32_t groups);
+uint64_t prefix_attention_bytes(const enc_tree_attention_args &a, uint32_t groups);   // for it and all smaller calls
 hipError_t launch_prefix_attention(PrefixAttnArgs k, const PrefixAttnPlan &p, hipStream_t s);
 hipError_t launch_cache_shared(const enc_cache &c, const int32_t *seqs, uint32_t batch, const int32_t *starts,
                                uint32_t groups, int32_t *shared, hipStream_t s);
@@ -182,8 +183,10 @@ struct SamplePlan {
   uint32_t rows;             // at a time
   uint32_t segment, segments;
   uint64_t bins, segs, sums, row_bytes, list;   // bytes of the workspace's parts
+  uint64_t total() const { return bins + segs + sums + row_bytes + list; }
 };
 SamplePlan plan_sample(uint32_t rows, uint32_t vocab);
+uint64_t sample_bytes(uint32_t rows, uint32_t vocab);   // for it and all calls of fewer rows
 hipError_t launch_sample(SampleKernelArgs k, const SamplePlan &p, hipStream_t s);
 
 struct CommitArgs {

@@ -891,7 +891,8 @@ def enc_prefix_attention_workspace_bytes(q, k_new, table, k_cache, starts):
 
 
 def prefix_attention_workspace(q, k_new, table, k_cache, starts):
-    """A workspace for enc_prefix_attention of these shapes (no initialisation needed)."""
+    """A workspace for enc_prefix_attention of these shapes (no initialisation needed), and for every call of the same
+    heads with no more sequences, nodes, groups or pages in a row of the table."""
     return _empty_u8(enc_prefix_attention_workspace_bytes(q, k_new, table, k_cache, starts), q.device)
 
 
@@ -999,7 +1000,7 @@ def enc_sample_workspace_bytes(rows, vocab):
 
 
 def sample_workspace(logits):
-    """A workspace for enc_sample of this shape (no initialisation needed)."""
+    """A workspace for enc_sample of this shape (no initialisation needed), and of fewer rows."""
     return _empty_u8(max(enc_sample_workspace_bytes(*logits.shape), 16), logits.device)
 
 

@@ -7,7 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_prefix_attention import Case  # noqa: E402
+from test_gpu_prefix_attention import Case, compare  # noqa: E402
 from test_gpu_prefix_attention_scores import SHAPES  # noqa: E402
 
 BF, FP = torch.bfloat16, torch.float16
@@ -40,3 +40,24 @@ def test_no_groups_prompt(E):
     say("prefix without groups, prompt")
     for D, T in ((64, 17), (64, 200), (256, 100)):
         Case([(0, [700]), (0, [33])], T, 4, 2, D, 16, seed=62).check(E, mask=False, starts=[0], shared=[])
+
+
+def test_one_workspace_for_all(E):
+    """A workspace of the largest call serves smaller ones, which write nothing past it; a call that needs more than it
+    is given is refused."""
+    say("prefix workspace")
+    T, H, G, D = 10, 8, 2, 128
+    biggest = Case([(90, [i % 5 for i in range(8)])] * 4, T, H, G, D, 16, seed=63)
+    starts = torch.zeros(5, dtype=torch.int32, device="cuda")
+    size = E.enc_prefix_attention_workspace_bytes(biggest.q, biggest.kn, torch.from_numpy(biggest.table), biggest.kc, starts)
+    room = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    for members, groups, nodes in ((8, 4, 10), (8, 1, 10), (1, 1, 10), (4, 4, 10), (8, 4, 1), (2, 1, 1), (3, 2, 4), (1, 4, 1)):
+        c = Case([(90, [i % 5 for i in range(members)])] * groups, nodes, H, G, D, 16, seed=64)
+        say("prefix workspace", members, groups, nodes)
+        want, wl, magnitude = c.want()
+        for kw in (dict(), dict(starts=[0], shared=[])):
+            out, lse = c.run(E, ws=room[:size], **kw)
+            compare(out, lse, want, wl, magnitude)
+    assert (room[size:] == 0xA5).all()
+    with pytest.raises(E.EncError):
+        biggest.run(E, ws=room[:1024])

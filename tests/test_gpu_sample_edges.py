@@ -48,3 +48,18 @@ def test_equal_rows(E):
     token, probs = E.enc_sample(row.repeat(1024, 1).cuda(), u.cuda(), top_p=p.cuda(), return_probs=True)
     token, probs = token.view(256, 4), probs.view(256, 4, -1)
     assert (token == token[:, :1]).all() and (probs == probs[:, :1]).all()
+
+
+def test_one_workspace_for_all(E):
+    """A workspace of the largest batch serves smaller ones, which write nothing past it."""
+    say("sampling workspace")
+    g = torch.Generator().manual_seed(8)
+    logits, u = (3.0 * torch.randn(40, 128256, generator=g)).cuda(), torch.rand(40, generator=g).cuda()
+    p = torch.full((1,), 0.9, device="cuda")
+    size = E.enc_sample_workspace_bytes(40, 128256)
+    room = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    want, _ = E.enc_sample(logits, u, top_p=p)
+    for rows in (40, 32, 31, 30, 16, 1):
+        token, _ = E.enc_sample(logits[:rows], u[:rows], top_p=p, ws=room[:size])
+        assert torch.equal(token, want[:rows])
+    assert (room[size:] == 0xA5).all()
