@@ -63,3 +63,19 @@ def test_one_workspace_for_all(E):
         token, _ = E.enc_sample(logits[:rows], u[:rows], top_p=p, ws=room[:size])
         assert torch.equal(token, want[:rows])
     assert (room[size:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("n,dtype,want", [
+    # 1 / n = 381 / (2^28 - 1): just above the half between 190 and 191 2^-27
+    (704555, torch.bfloat16, 191 * 2.0 ** -27),
+    # 1 / n = 1801 / (2^25 - 1): just above the half between 900 and 901 2^-24
+    (18631, torch.float16, 901 * 2.0 ** -24),
+    # 1 / n = 251 / (2^25 + 1): just below the half between 125 and 126 2^-24
+    (133683, torch.float16, 125 * 2.0 ** -24),
+])
+@pytest.mark.parametrize("logits_dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_probabilities_are_rounded_once(E, n, dtype, want, logits_dtype):
+    """Equal probabilities that fp32 puts on a half of the output's type, where they are not."""
+    say("probabilities", n, dtype, logits_dtype)
+    _, probs = E.enc_sample(torch.zeros(1, n, dtype=logits_dtype, device="cuda"), return_probs=True, probs_dtype=dtype)
+    assert (probs.double() == want).all()
