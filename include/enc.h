@@ -530,7 +530,9 @@ enc_status enc_tree_attention(const enc_tree_attention_args *h_args, void *d_ws,
  * entry of no group, and a group of one, share nothing. Numbers out of range
  * count as the nearest in it (starts: [0, batch], a start below an earlier one
  * as that one; d_shared: 0 to the shortest length in the group). However many
- * rows there are, the result is all that is rounded to the values' type. */
+ * rows there are, the result is all that is rounded to the values' type. One
+ * launch more than enc_tree_attention: faster from 4 sequences over some 8000
+ * tokens, 2 over 100000 or 64 over 1000. */
 typedef struct enc_prefix_attention_args {
   enc_tree_attention_args t;       /* as for enc_tree_attention */
   const int32_t *d_starts;         /* [groups + 1], ascending */

@@ -10,7 +10,8 @@
 // is one workgroup's, all of it in registers, 8 consecutive values to a thread
 // and NV times that: all of a row's loads (weights and gates too) are on their
 // way before the first sum, and a row costs one barrier, or two with the norm
-// after the block.
+// after the block. Above 16384 values (NV = 4) weights and gates are loaded when
+// they are needed, and still some 40 of a thread's registers spill to memory.
 //
 // A row's 16-byte results are stored past the caches: many rows at once come to
 // 6.2 TB/s instead of 5.5, and a kernel that reads them next is no slower (two
@@ -18,8 +19,10 @@
 // of 4096, 11.8 against 14.0 for 792 of 2560).
 //
 // Measured: 1 row of 4096 3.4 us (a launch alone takes about 2), 792 rows of 2560
-// 6.0 us, 8192 rows of 4096 (BF16 y, FP32 h, 470 MB) 76 us = 6.2 TB/s, where a
-// large copy reaches 5.1; 515 odd rows of 1537, one value a load, 6.9 us.
+// 6.0 us, 8192 rows of 4096 (FP32 y and h, 470 MB) 76 us = 6.2 TB/s, where a
+// large copy reaches 5.1; 515 odd rows of 1537, one value a load, 6.9 us. The widest
+// rows (FP32 y and h, both norms): 2048 of 16384 90 us = 5.2 TB/s, 2048 of 16392 159 =
+// 3.0, 1024 of 32768 134 = 3.5, one of them 14.4, 1024 of 32767 156 = 3.0.
 #include "step_common.h"
 
 #include <algorithm>

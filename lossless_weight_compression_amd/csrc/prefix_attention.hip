@@ -22,13 +22,14 @@
 // k_shared, groups of many rows: eight waves to a workgroup, 64 or 128 rows, a KV
 // head and a range of keys. Keys and values go through LDS in stages of 64, used
 // by four tiles of rows each; two waves to a tile take half of a stage's keys
-// each. Two stages are on their way in registers, three lie in LDS: with one on
-// its way 131072 tokens took 145 us instead of 102. Long ranges of many rows run at 743
-// TFLOP/s (256 rows, from 8192 to 32768 tokens; 3200 cycles a stage of 64 keys):
-// the vector unit is the busiest (51% of the cycles; the matrix unit 23), with the
-// exponentials and conversions; a piece's start and end, some 10 us, is the rest
-// of a short call. Few rows are bound by HBM: 64 rows, 131072 tokens of 8 heads, 102
-// us = 5.3 TB/s.
+// each. Two stages are on their way in registers, three lie in LDS (with one on
+// its way times are within 2%, 131072 tokens either way 132 us a call). Long ranges
+// of many rows run at 560 TFLOP/s of the formula's operations, 840 with the rests'
+// (256 rows, from 8192 to 32768 tokens; some 4000 cycles a stage of 64 keys): the
+// vector unit is busy 48% of the cycles, with the exponentials and conversions, the
+// matrix unit 34%, LDS 20%; a piece's start and end, some 10 us, is the rest of a
+// short call. Few rows are bound by HBM: 64 rows, 131072 tokens of 8 heads, 103 us =
+// 5.2 TB/s.
 //
 // k_pieces, each sequence's own tokens and tree, and groups of few rows: four
 // waves hold the same rows and take strips of 32 keys in turn, straight from
@@ -36,12 +37,14 @@
 // registers; the waves' sums are joined through LDS before they are written, so
 // that a range costs one set of partial sums, not four. It is bound by HBM, and in
 // short calls by the way from the table to the keys. (For the shared tokens of
-// many rows it took 33 us with 32 rows to a wave and 45 with 64, k_shared 24.)
+// many rows it took 33 us with 32 rows to a wave and 45 with 64, k_shared 24, all
+// without the rests.)
 //
 // Measured, BF16, heads of 128, 32 query and 8 KV heads, whole call on the device:
-// 4 sequences over 1021 shared tokens 15.9 us (plan 5.9, pieces 7.4, join 4.1); 64
-// over 8192 with 512 own tokens at most 62.4 (5.9, shared 24.0, own 21.6, join 6.6;
-// 5.4 for enc_cache_shared); 16 over 131072 132 (5.9, 102, 15, 7.8).
+// 4 sequences over 1021 shared tokens 16.2 us (plan 6.1, pieces 7.2, join 4.7); 64
+// over 8192 with 512 own tokens at most 66.9 (6.1, shared 26.7, own 22.2, join 6.7;
+// 5.2 for enc_cache_shared); 16 over 131072 133 (6.1, 103, 15.4, 8.0). Heads of 256:
+// 16 over 8192 with 300 own 53.
 #include "attention_math.h"
 #include "group_math.h"
 #include "step_common.h"
@@ -1493,18 +1496,22 @@ namespace {
 // A tile of shared tokens that has rows to spare, or two tiles that each read the
 // keys, cost more by the token; a call of less than some ten microseconds more of
 // them starts later with the larger one (its first stage, the exchange between its
-// waves, what it writes). Times in us, 8 KV heads of 128, for 1021 / 8192 / 131072
-// shared tokens:
-//   32 rows: tiles of 16 16.1 / 27.2 / 139, one of 64 22.3 / 31.8 / 119;
-//   64 rows: four tiles of 16 25 / 35 / 124, one of 64 23.7 / 34.7 / 123;
-//   128 rows: two tiles of 64 25.1 / 36.5 / 165, one of 128 28.4 / 40.0 / 141;
-//   256 rows, 8192 tokens, the shared tokens alone: 27 and 24; 1024 rows: 80 and 59.
-// What a sequence's table can hold stands for its length, which the host does
-// not know.
+// waves, what it writes). Whole calls in us, 8 KV heads of 128, for 1021 / 8192 /
+// 131072 shared tokens in tiles of 16, 64 and 128:
+//     32 rows: 16.5 / 27.6 / 140, 23.1 / 32.1 / 123, 25.1 / 34.9 / 131;
+//     64 rows: 18.5 / 30.4 / 218, 24.8 / 34.7 / 124, 26.4 / 36.6 / 134;
+//    128 rows: 23.7 / 38.1 / 369, 26.1 / 37.4 / 181, 29.4 / 41.1 / 160;
+//    256 rows: 27.9 / 59.1 / 644, 31.0 / 45.8 / 309, 33.9 / 46.7 / 258;
+//   1024 rows: 60.6 / 175 / -, 52.9 / 110 / -, 55.7 / 99 / -.
+// So the rule costs up to a third where 33 to 256 rows share some 1000 tokens, 10 to
+// 14% where 33 to 64 share 8192, and up to 2% otherwise. What a sequence's
+// table can hold stands for its length, which the host does not know: in a table
+// far wider than the histories a call takes the figures of the longer ones' tiles.
 //
-// Of own tokens. 32 rows of a sequence: two tiles of 16 take 48.9 us, one of 32
-// 52.8 (16 sequences of 8 nodes, 1000 own tokens, heads of 128), but 44.3 and
-// 42.6 with heads of 64 (40 sequences, 300 tokens). 64 rows: 62.6 and 60.6.
+// Of own tokens, in tiles of 16 and of 32 rows: 32 rows of a sequence 32.5 and 35.7
+// us (16 sequences of 8 nodes, 1000 own tokens, heads of 128), 25.6 and 25.7 with
+// heads of 64 (40 sequences, 300 tokens); 64 rows 42.3 and 40.4, heads of 64 35.7
+// and 37.2; 256 rows 91.6 and 77.6.
 struct TileRule {
   bool large;   // heads above 128 values: no tiles of 128 rows, nor of 32 own ones
   uint64_t from64, from128, own32;
@@ -1518,9 +1525,9 @@ TileRule tile_rule(const enc_tree_attention_args &a) {
 // more, a short one, for every tile.
 //
 // Resident workgroups: one of eight waves to a compute unit, or two or three of
-// four. 64 sequences over 8192 shared tokens take 62.4 us; with twice as many
-// shares of the shared tokens 73.5, with three quarters 64.9; with half or twice
-// as many shares of the own ones 62.4 and 60.9.
+// four. 64 sequences over 8192 shared tokens take 66.7 us; with twice as many
+// shares of the shared tokens 78.2, with three quarters 70.2; with half or twice
+// as many shares of the own ones 66.7 and 65.7.
 PrefixAttnPlan plan_of(const enc_tree_attention_args &a, uint32_t groups, uint32_t tile, uint32_t own_tile,
                        uint64_t tiles, uint64_t own_tiles_of_all) {
   PrefixAttnPlan p;
