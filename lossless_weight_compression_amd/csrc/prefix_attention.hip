@@ -408,21 +408,37 @@ __device__ __forceinline__ uint32_t cached_row(const PrefixAttnArgs &k, const in
   const uint32_t entry = k.page.quot(key), page = min((uint32_t)max(table[entry], 0), k.a.n_pages - 1);
   return page * (uint32_t)(k.a.cache_page / 8) + (key - entry * k.page.d) * (uint32_t)(k.a.cache_token / 8);
 }
-// Adds those of a run of values that are no finite numbers.
-template <typename T, int N> __device__ __forceinline__ void add_nonfinite(const T *p, float (&sum)[N]) {
-  uint32_t w[N / 2];
-  if constexpr (N == 8) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(p);
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    w[0] = v.x, w[1] = v.y;
+// Adds those values that are no finite numbers, N runs of C; a run is live(n) or
+// not there. Rarely is there one.
+template <typename T, int N, int C, typename L>
+__device__ __forceinline__ void add_nonfinite(const T *row, int stride, L live, float (&sum)[N][C]) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  constexpr uint32_t E = Half<T>::kExp;
+  uint32_t w[N][C / 2];
+  u16x2 top = {0, 0};   // greatest exponents
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    if constexpr (C == 8) {
+      const uint4 v = live(n) ? *reinterpret_cast<const uint4 *>(row + n * stride) : make_uint4(0, 0, 0, 0);
+      w[n][0] = v.x, w[n][1] = v.y, w[n][2] = v.z, w[n][3] = v.w;
+    } else {
+      const uint2 v = live(n) ? *reinterpret_cast<const uint2 *>(row + n * stride) : make_uint2(0, 0);
+      w[n][0] = v.x, w[n][1] = v.y;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float x = half_of<T>(w[i / 2], i & 1);
-    if (!__builtin_isfinite(x)) sum[i] += x;
-  }
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i)
+      top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[n][i] & (E | E << 16)));
+  if (top.x != E && top.y != E) return;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const float x = half_of<T>(w[n][i / 2], i & 1);
+      if (!__builtin_isfinite(x)) sum[n][i] += x;
+    }
 }
 
 // ---- a piece
@@ -702,8 +718,9 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, const PrefixItem 
   }
   // The rest of a weight may be 0 or below, and so may come no number, or the
   // wrong infinity, of an infinite cached value. Every row sees that: where no row
-  // is finite, the values at fault are looked for and their sum is the result.
-    bool lost = true;
+  // is finite, though the weights of some are, the values at fault are looked for
+  // and their sum is the result (16 sequences over 131072 tokens then take 2.2 ms).
+  bool lost = true, weighed = false;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     float zero = 0.f;
@@ -714,20 +731,24 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, const PrefixItem 
 #pragma unroll
         for (int e = 0; e < 4; ++e) zero = fmaf(o[u][n][f][e], 0.f, zero);
     lost = lost && rows_sum(zero) != 0.f;
+    weighed = weighed || __builtin_isfinite(rows_sum(l[u]));
   }
-  if (__all(lost)) {
-    float sum[NH][4][C] = {};
-    for (strip = lo + wave; strip < min(hi, strips_ctx); strip += kWays)
-      for (uint32_t key = strip * 32; key < min(strip * 32 + 32, ctx); ++key) {
-        const T *row = reinterpret_cast<const T *>(vc + cached_row(k, table, first + key));
+  if (__all(lost) && __any(weighed)) {
+    float sum[NH][4][1][C] = {};
+    for (strip = lo + wave; strip < min(hi, strips_ctx); strip += kWays) {
+      const uint32_t at = cached_row(k, table, first + min(strip * 32 + (lane & 31), ctx - 1));
+#pragma unroll 4
+      for (int key = 0; key < 32; ++key) {   // (the last one more than once)
+        const T *row = reinterpret_cast<const T *>(vc + (uint32_t)__shfl((int)at, key));
 #pragma unroll
         for (int n = 0; n < NH; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t d = (n * 16 + 4 * g4 + i) * C;
-            if (EXACT || d < D) add_nonfinite(row + d, sum[n][i]);
+            add_nonfinite(row + d, 0, [&](int) { return EXACT || d < D; }, sum[n][i]);
           }
       }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const float none = 0.f * rows_sum(l[u]);   // a row of its own fault stays no number
@@ -737,7 +758,7 @@ __device__ __forceinline__ void piece(const PrefixAttnArgs &k, const PrefixItem 
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int f = 0; f < C; ++f)
-            if (sum[n][i][f] != 0.f) o[u][n][f][i] = sum[n][i][f] + none;
+            if (sum[n][i][0][f] != 0.f) o[u][n][f][i] = sum[n][i][0][f] + none;
     }
   }
   // Infinities and NaN of the tree went in as zeros, since 0 times them would
@@ -1220,7 +1241,7 @@ __global__ __launch_bounds__(512, 2) void k_shared(PrefixAttnArgs k) {
   }
 
   // As in `piece`: infinite values, of the keys that were this wave's.
-  bool lost = busy;
+  bool lost = busy, weighed = false;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     float zero = 0.f;
@@ -1229,19 +1250,21 @@ __global__ __launch_bounds__(512, 2) void k_shared(PrefixAttnArgs k) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) zero = fmaf(o[u][f][e], 0.f, zero);
     lost = lost && rows_sum(zero) != 0.f;
+    weighed = weighed || __builtin_isfinite(rows_sum(l[u]));
   }
-  if (__all(lost)) {
+  if (__all(lost) && __any(weighed)) {
     const uint4 *values = static_cast<const uint4 *>(a.d_v_cache) + h * (a.cache_head / 8);
-    float sum[NF][4] = {};
-    for (st = lo; st < hi; ++st)
-      for (uint32_t key = st * kStage + half * 32; key < min(st * kStage + half * 32 + 32, ctx); ++key) {
-        const T *row = reinterpret_cast<const T *>(values + cached_row(k, table, key));
+    float sum[NF / 4][4][4] = {};
+    for (st = lo; st < hi && st * kStage + half * 32 < ctx; ++st) {
+      const uint32_t at = cached_row(k, table, min(st * kStage + half * 32 + (lane & 31), ctx - 1));
+#pragma unroll 2
+      for (int key = 0; key < 32; ++key) {
+        const T *row = reinterpret_cast<const T *>(values + (uint32_t)__shfl((int)at, key));
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          const uint32_t d = 16 * f + 4 * g4;
-          if (d < D) add_nonfinite(row + d, sum[f]);
-        }
+        for (int n = 0; n < NF / 4; ++n)
+          add_nonfinite(row + 64 * n + 4 * g4, 16, [&](int f) { return 64 * n + 16 * f + 4 * g4 < D; }, sum[n]);
       }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const float none = 0.f * rows_sum(l[u]);
@@ -1249,7 +1272,7 @@ __global__ __launch_bounds__(512, 2) void k_shared(PrefixAttnArgs k) {
       for (int f = 0; f < NF; ++f)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (sum[f][e] != 0.f) o[u][f][e] = sum[f][e] + none;
+          if (sum[f / 4][f % 4][e] != 0.f) o[u][f][e] = sum[f / 4][f % 4][e] + none;
     }
   }
 
